@@ -295,6 +295,153 @@ int ds_topk_merge(const int32_t* lens, int64_t rows, int64_t n, int k, int dtype
 int ds_topk_noalloc(const void* x, int64_t rows, int64_t n, int64_t row_stride, int k, int dtype, uint64_t seed,
                     void* out_vals, int32_t* out_idx, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Operators beside the selection: routing to experts (the top-k gate with its gradient), a
+ * sampler's probabilities and the verification of drafted tokens. The conventions above hold
+ * (device pointers, asynchronous on `stream`, whole validation before anything is enqueued),
+ * with these differences: rows and outputs need no more than their element's alignment
+ * (DS_ERR_ALIGNMENT otherwise), and -inf has a meaning of its own, stated per entry. `stream`
+ * belongs to the current device, as the memory does. No entry allocates or synchronises, so all
+ * can be captured in a graph; one that needs scratch memory takes it from the caller.
+ */
+
+/* scores of the experts */
+#define DS_SCORE_SOFTMAX 0 /* s = softmax(x) over all experts of the row */
+#define DS_SCORE_SIGMOID 1 /* s = 1 / (1 + exp(-x)) */
+
+#define DS_MAX_EXPERTS 1024
+#define DS_MAX_ROUTE_K 64
+#define DS_MAX_ROUTE_GROUPS 64
+
+/*
+ * How ds_route scores, limits and weighs. NULL means { DS_SCORE_SOFTMAX, 1, 1, 1, 0, 1.0f };
+ * groups, topk_groups and group_top of zero mean one group, all groups, and one.
+ *   groups       G: the row's experts are G equal runs of consecutive experts (G divides the
+ *                experts).
+ *   topk_groups  only the experts of the topk_groups best groups can be chosen
+ *                (topk_groups * experts / groups >= k).
+ *   group_top    a group's score is the sum of its group_top (1 or 2) best selection scores.
+ *   renormalize  non-zero: the weights are divided by the sum of the chosen experts' scores.
+ *   scale        a finite factor of all weights.
+ */
+typedef struct ds_route_config {
+  int32_t score;
+  int32_t groups;
+  int32_t topk_groups;
+  int32_t group_top;
+  int32_t renormalize;
+  float scale;
+} ds_route_config;
+
+/*
+ * ds_route -- the k experts of every row of logits and their weights.
+ *   s_e = score of x[r, e]; c_e = s_e + bias[e] (the selection score). Groups are chosen by
+ *   the sum of their best c, then the k largest c in them, larger first. The weight of a chosen
+ *   expert is scale * s_e, divided by the sum of the chosen s when `renormalize` is set: the
+ *   bias moves the choice only.
+ * The order is exact: c is evaluated in double precision, and without a bias the order is
+ * that of the logits themselves; equal scores go to the smaller group and expert.
+ * An expert whose logit or bias is -inf is masked: it is never chosen and, with a logit of
+ * -inf, takes no part in the softmax. A group's score counts its unmasked experts, and a group
+ * without any is chosen after all others. Slots that no expert is left for hold index -1 and
+ * weight 0, and weights whose scores sum to zero are 0. +inf is the limit (softmax: the +inf
+ * logits share the mass evenly). NaN: the row's output is unspecified.
+ *   x            [rows, experts] of dtype, rows row_stride elements apart.
+ *   experts      1 <= experts <= DS_MAX_EXPERTS; 1 <= k <= min(DS_MAX_ROUTE_K, experts).
+ *   bias         NULL, or [experts] float.
+ *   out_weights  [rows, k] float, or NULL.
+ *   out_idx      [rows, k] int32, or NULL. Not both NULL.
+ *   counts       NULL, or [experts] int32: the number of rows that chose each expert is ADDED
+ *                to it (the load that a balancing bias is updated from).
+ */
+int ds_route(const void* x, int64_t rows, int64_t experts, int64_t row_stride, int k, int dtype, const float* bias,
+             const ds_route_config* cfg, float* out_weights, int32_t* out_idx, int32_t* counts, void* stream);
+
+/*
+ * ds_route_grad -- the gradient of ds_route's weights to the logits, the choice held fixed.
+ *   With g_j the gradient of slot j's weight, s the scores (computed again from x), S the sum
+ *   of the chosen s and h_e the sum of scale * g_j over the slots that chose e:
+ *     renormalize:  ds_e = (h_e - sum_i h_i s_i / S) / S for the chosen experts (0 if S is 0)
+ *     otherwise:    ds_e = h_e
+ *     sigmoid:      dx_e = ds_e s_e (1 - s_e)
+ *     softmax:      dx_e = s_e (ds_e - sum_i ds_i s_i), over all experts
+ *   (the softmax with renormalize is zero for the experts that were not chosen). The bias has
+ *   no gradient.
+ *   idx           [rows, k] int32: ds_route's out_idx; entries outside [0, experts) count as
+ *                 slots without an expert. An expert that fills several slots of a row counts
+ *                 once in S for each of them.
+ *   grad_weights  [rows, k] float.
+ *   grad_x        [rows, experts] of dtype, rows grad_stride elements apart; written whole.
+ *   cfg           the forward call's (groups, topk_groups and group_top are checked the same
+ *                 way and not used otherwise).
+ */
+int ds_route_grad(const void* x, int64_t rows, int64_t experts, int64_t row_stride, int k, int dtype,
+                  const ds_route_config* cfg, const int32_t* idx, const float* grad_weights, void* grad_x,
+                  int64_t grad_stride, void* stream);
+
+/*
+ * ds_softmax -- the probabilities of every row of logits at a temperature:
+ *   out[r, i] = exp((x[r, i] - m) / t_r) / sum, m the row's maximum, t_r = temperature[r].
+ * A temperature that is not above zero is the limit: 1 at the first maximum, 0 elsewhere. -inf
+ * has probability 0, a row of -inf alone gives zeros, and +inf logits share the mass evenly.
+ *   x            [rows, n] of dtype, 1 <= n <= 2^31 - 1.
+ *   temperature  NULL (1 everywhere), or [rows] float on the device.
+ *   out          [rows, n] of out_dtype, rows out_stride elements apart; does not overlap x.
+ *   workspace    ds_softmax_workspace_size bytes, 8-byte aligned (NULL when that is 0). Its
+ *                contents on entry do not matter; calls that share it must not overlap in time.
+ */
+int ds_softmax(const void* x, int64_t rows, int64_t n, int64_t row_stride, int dtype, const float* temperature,
+               void* out, int64_t out_stride, int out_dtype, void* workspace, size_t ws_bytes, void* stream);
+int ds_softmax_workspace_size(int64_t rows, int64_t n, int dtype, size_t* bytes);
+
+/*
+ * ds_topk_softmax -- ds_softmax restricted to a row's top-k list, as a whole row and as a list.
+ *   The list (vals, idx) is ds_topk's: sorted by value, larger first, padded with index -1.
+ *   Row r uses its first ks[r] entries (clamped to [1, k]); top_p keeps the shortest prefix
+ *   of those whose mass reaches top_p[r] of theirs (at least one entry); the kept entries'
+ *   probabilities sum to 1. Temperatures and infinities as in ds_softmax. The prefix is
+ *   decided in double precision.
+ *   vals         [rows, k] of dtype; idx [rows, k] int32 (entries outside [0, n) are skipped in
+ *                `out` and have no mass, like ds_topk's padding). 1 <= k <= DS_MAX_K.
+ *   ks, temperature, top_p  NULL, or [rows] on the device (int32, float, float).
+ *   out          NULL, or [rows, n] of out_dtype, rows out_stride elements apart; written whole.
+ *   out_list     NULL, or [rows, k] float: the entries' probabilities (0 past the prefix). Not
+ *                both NULL.
+ */
+int ds_topk_softmax(const void* vals, const int32_t* idx, int64_t rows, int k, int dtype, const int32_t* ks,
+                    const float* temperature, const float* top_p, int64_t n, void* out, int64_t out_stride,
+                    int out_dtype, float* out_list, void* stream);
+
+/*
+ * ds_verify -- drafted tokens against the target's probabilities, with given random numbers.
+ *   Sequence b has drafts t_0 .. t_{len-1}, target rows p_0 .. p_len and draft rows q_0 ..
+ *   Draft j is accepted iff accept_u[b, j] * q_j[t_j] < p_j[t_j]. At the first draft r that is
+ *   not, the next token is drawn from max(p_r - q_r, 0), and from p_len when all are accepted:
+ *   the first i with sum_{<= i} > sample_u[b] * sum of all. A residual without mass falls back
+ *   to p_r; p_r without mass gives token -1. So an accepted or drawn token has the target's
+ *   distribution, and drafts = 0 is plain sampling. Products and sums are in double precision.
+ *   target       [batch, drafts + 1, n] of dtype: row b * (drafts + 1) + j, target_stride
+ *                elements apart. Rows need not sum to 1 exactly.
+ *   draft        [batch, drafts, n] of dtype, draft_stride elements apart, or NULL: the drafts
+ *                are certain (q_j is 1 at t_j and 0 elsewhere).
+ *   draft_tokens [batch, drafts] int32 (NULL when drafts is 0). A token outside [0, n) is
+ *                not accepted.
+ *   draft_lens   NULL (all `drafts`), or [batch] int32, clamped to [0, drafts]; rows and tokens
+ *                past a sequence's length are not read.
+ *   accept_u     [batch, drafts] float in [0, 1) (NULL when drafts is 0); sample_u [batch].
+ *   drafts       0 <= drafts <= DS_MAX_DRAFTS.
+ *   out_tokens   [batch, drafts + 1] int32: the accepted drafts, the drawn token, then -1.
+ *   out_accepted [batch] int32: the number of accepted drafts.
+ *   workspace    ds_verify_workspace_size bytes, 8-byte aligned, as in ds_softmax.
+ * Probabilities are not negative and not NaN (a row that breaks this has an unspecified token).
+ */
+#define DS_MAX_DRAFTS 64
+int ds_verify(const void* target, int64_t target_stride, const void* draft, int64_t draft_stride,
+              const int32_t* draft_tokens, const int32_t* draft_lens, const float* accept_u, const float* sample_u,
+              int64_t batch, int drafts, int64_t n, int dtype, int32_t* out_tokens, int32_t* out_accepted,
+              void* workspace, size_t ws_bytes, void* stream);
+int ds_verify_workspace_size(int64_t batch, int64_t n, int dtype, size_t* bytes);
+
 /*
  * ds_probe_read -- measurement aid, not part of top-k (tutorial chapter 37, section 6.1: the
  * method's measure is how close it comes to reading the input once; this is the plain read

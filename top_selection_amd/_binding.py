@@ -31,6 +31,11 @@ MERGE_AUTO, MERGE_LISTS, MERGE_SELECT = 0, 1, 2
 SCHEDULE_AUTO, SCHEDULE_FREE, SCHEDULE_LOCKSTEP = 0, 1, 2
 OUTPUT_UNSORTED, OUTPUT_INDEX_INT64 = 1, 2
 SHARE_AUTO, SHARE_OFF, SHARE_ON = 0, 1, 2
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+DS_MAX_EXPERTS = 1024
+DS_MAX_ROUTE_K = 64
+DS_MAX_ROUTE_GROUPS = 64
+DS_MAX_DRAFTS = 64
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # DS_LIBRARY names another build of the library (e.g. one with host-side sanitizers)
@@ -50,6 +55,11 @@ class ds_config(ctypes.Structure):
                 ("merge", ctypes.c_int32), ("schedule", ctypes.c_int32),
                 ("depth", ctypes.c_int32), ("output", ctypes.c_int32), ("warmup", ctypes.c_int32),
                 ("share", ctypes.c_int32)]
+
+
+class ds_route_config(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 STATS_FIELDS = ["appended", "compactions", "work", "max_len", "reads", "index_sum", "monotone", "slice_lo",
@@ -91,6 +101,21 @@ def lib() -> ctypes.CDLL:
             L.ds_probe_sink_words.restype = i64
             L.ds_probe_copy.argtypes = [vp, vp, i64, vp]
             L.ds_probe_copy.restype = ci
+            rcp, szp, sz = ctypes.POINTER(ds_route_config), ctypes.POINTER(ctypes.c_size_t), ctypes.c_size_t
+            L.ds_route.argtypes = [vp, i64, i64, i64, ci, ci, vp, rcp, vp, vp, vp, vp]
+            L.ds_route.restype = ci
+            L.ds_route_grad.argtypes = [vp, i64, i64, i64, ci, ci, rcp, vp, vp, vp, i64, vp]
+            L.ds_route_grad.restype = ci
+            L.ds_softmax.argtypes = [vp, i64, i64, i64, ci, vp, vp, i64, ci, vp, sz, vp]
+            L.ds_softmax.restype = ci
+            L.ds_softmax_workspace_size.argtypes = [i64, i64, ci, szp]
+            L.ds_softmax_workspace_size.restype = ci
+            L.ds_topk_softmax.argtypes = [vp, vp, i64, ci, ci, vp, vp, vp, i64, vp, i64, ci, vp, vp]
+            L.ds_topk_softmax.restype = ci
+            L.ds_verify.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, i64, ci, i64, ci, vp, vp, vp, sz, vp]
+            L.ds_verify.restype = ci
+            L.ds_verify_workspace_size.argtypes = [i64, i64, ci, szp]
+            L.ds_verify_workspace_size.restype = ci
             L.ds_status_string.argtypes = [ci]
             L.ds_status_string.restype = ctypes.c_char_p
             _lib = L
@@ -279,6 +304,231 @@ def ds_topk_merge(rows: int, n: int, k: int, dtype: int, seed: int = 0, workspac
     if st != DS_OK:
         raise DSError(st, "ds_topk_merge")
     return out_vals, out_idx
+
+
+# ------------------------------------------------------- the operators beside the selection
+def _rows_of(x, what: str):
+    """The (row stride) of the last two dimensions of a device tensor with contiguous rows."""
+    if not x.is_cuda:
+        raise ValueError(f"{what} must be a device tensor")
+    if x.shape[-1] > 1 and x.stride(-1) != 1:
+        raise ValueError(f"rows of {what} must be contiguous (stride(-1) == 1)")
+
+
+def _matrix(x, what: str):
+    """rows, n, row stride of a 2-D device tensor with contiguous rows."""
+    if x.dim() != 2:
+        raise ValueError(f"{what} must be 2-D")
+    _rows_of(x, what)
+    rows, n = x.shape
+    return rows, n, x.stride(0) if rows > 1 else max(n, 1)
+
+
+def _batch_rows(x, what: str):
+    """batch, rows per sequence, n, row stride of a 3-D device tensor whose rows lie evenly apart."""
+    if x.dim() != 3:
+        raise ValueError(f"{what} must be 3-D")
+    _rows_of(x, what)
+    b, m, n = x.shape
+    if m > 1:
+        stride = x.stride(1)
+        if b > 1 and x.stride(0) != m * stride:
+            raise ValueError(f"rows of {what} must lie evenly apart (stride(0) == shape[1] * stride(1))")
+    else:
+        stride = x.stride(0) if b > 1 else n
+    return b, m, n, stride
+
+
+def _operand(t, what: str, dtype, shape, device):
+    """The address of an optional contiguous device tensor of the given type, shape and device."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _call(name: str, device, stream, args) -> None:
+    """Calls the C entry with the stream last, with `device` current (the stream is the given
+    one, or torch's current stream on that device)."""
+    torch = _torch()
+    if device.index is not None and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            st = getattr(lib(), name)(*args, _stream_handle(stream, device))
+    else:
+        st = getattr(lib(), name)(*args, _stream_handle(stream, device))
+    if st != DS_OK:
+        raise DSError(st, name)
+
+
+def _scratch(size_of, rows: int, n: int, dt: int, workspace, device, stream):
+    """The call's workspace (kept by the caller until the call has been made), its address and
+    its bytes: the one given, or one of the needed size from torch, which is told about a
+    stream that is not its current one."""
+    if workspace is None:
+        b = ctypes.c_size_t(0)
+        if size_of(rows, n, dt, ctypes.byref(b)) != DS_OK or b.value == 0:  # the call itself reports what is wrong
+            return None, None, 0
+        torch = _torch()
+        workspace = torch.empty(b.value, dtype=torch.uint8, device=device)
+        if stream is not None and stream != torch.cuda.current_stream(device):
+            workspace.record_stream(stream)
+        return workspace, workspace.data_ptr(), b.value
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _workspace_size(name: str, rows: int, n: int, dtype: int) -> int:
+    b = ctypes.c_size_t(0)
+    st = getattr(lib(), name)(rows, n, dtype, ctypes.byref(b))
+    if st != DS_OK:
+        raise DSError(st, name)
+    return int(b.value)
+
+
+def ds_softmax_workspace_size(rows: int, n: int, dtype: int) -> int:
+    return _workspace_size("ds_softmax_workspace_size", rows, n, dtype)
+
+
+def ds_verify_workspace_size(batch: int, n: int, dtype: int) -> int:
+    return _workspace_size("ds_verify_workspace_size", batch, n, dtype)
+
+
+def ds_route(x, k: int, bias=None, score: int = SCORE_SOFTMAX, groups: int = 1, topk_groups: int = 0,
+             group_top: int = 1, renormalize: bool = False, scale: float = 1.0, counts=None, weights: bool = True,
+             out_weights=None, out_idx=None, stream=None):
+    """The k experts of every row of the logits x [rows, experts] (bf16 or fp32) and their
+    weights; see include/dstopk.h.
+
+    Returns (weights [rows, k] fp32 or None, indices [rows, k] int32). bias: fp32 [experts],
+    moves the choice only. counts: int32 [experts], gets the rows that chose each expert added.
+    """
+    torch = _torch()
+    rows, n, rs = _matrix(x, "x")
+    dt, dev, shape = dtype_code(x), x.device, (rows, k)
+    if weights and out_weights is None:
+        out_weights = torch.empty(shape, dtype=torch.float32, device=dev)
+    if out_idx is None:
+        out_idx = torch.empty(shape, dtype=torch.int32, device=dev)
+    cfg = ds_route_config(score, groups, topk_groups, group_top, 1 if renormalize else 0, scale)
+    _call("ds_route", dev, stream,
+          (x.data_ptr(), rows, n, rs, k, dt, _operand(bias, "bias", torch.float32, (n,), dev), ctypes.byref(cfg),
+           _operand(out_weights, "out_weights", torch.float32, shape, dev),
+           _operand(out_idx, "out_idx", torch.int32, shape, dev),
+           _operand(counts, "counts", torch.int32, (n,), dev)))
+    return out_weights, out_idx
+
+
+def ds_route_grad(x, idx, grad_weights, score: int = SCORE_SOFTMAX, renormalize: bool = False, scale: float = 1.0,
+                  out=None, stream=None):
+    """The gradient of ds_route's weights to its logits x, for the chosen experts idx [rows, k]
+    int32 and the weights' gradient [rows, k] fp32; [rows, experts] of x's dtype."""
+    torch = _torch()
+    rows, n, rs = _matrix(x, "x")
+    dt, dev = dtype_code(x), x.device
+    if idx.dim() != 2:
+        raise ValueError("idx must be 2-D [rows, k]")
+    k = idx.shape[1]
+    if out is None:
+        out = torch.empty((rows, n), dtype=x.dtype, device=dev)
+    _, _, os = _matrix(out, "out")
+    if out.dtype != x.dtype or tuple(out.shape) != (rows, n) or out.device != dev:
+        raise ValueError("out must be [rows, experts] of x's dtype on x's device")
+    cfg = ds_route_config(score, 1, 1, 1, 1 if renormalize else 0, scale)
+    _call("ds_route_grad", dev, stream,
+          (x.data_ptr(), rows, n, rs, k, dt, ctypes.byref(cfg), _operand(idx, "idx", torch.int32, (rows, k), dev),
+           _operand(grad_weights, "grad_weights", torch.float32, (rows, k), dev), out.data_ptr(), os))
+    return out
+
+
+def _out_rows(out, out_dtype, rows: int, n: int, dev):
+    torch = _torch()
+    if out is None:
+        out = torch.empty((rows, n), dtype=out_dtype or torch.float32, device=dev)
+    _, _, os = _matrix(out, "out")
+    if tuple(out.shape) != (rows, n) or out.device != dev or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out must be [rows, n] of out_dtype on the inputs' device")
+    return out, os
+
+
+def ds_softmax(x, temperature=None, out_dtype=None, out=None, workspace=None, stream=None):
+    """Probabilities [rows, n] (fp32, or out_dtype / out's type) of the logits x [rows, n] (bf16
+    or fp32) at a temperature per row (fp32 [rows] on the device; not above 0: one-hot at the
+    first maximum); see include/dstopk.h."""
+    torch = _torch()
+    rows, n, rs = _matrix(x, "x")
+    dt, dev = dtype_code(x), x.device
+    out, os = _out_rows(out, out_dtype, rows, n, dev)
+    keep, ws, ws_bytes = _scratch(lib().ds_softmax_workspace_size, rows, n, dt, workspace, dev, stream)
+    _call("ds_softmax", dev, stream,
+          (x.data_ptr(), rows, n, rs, dt, _operand(temperature, "temperature", torch.float32, (rows,), dev),
+           out.data_ptr(), os, dtype_code(out), ws, ws_bytes))
+    return out
+
+
+def ds_topk_softmax(vals, idx, n: int, ks=None, temperature=None, top_p=None, out_dtype=None, out=None,
+                    out_list=None, rows_out: bool = True, stream=None):
+    """Probabilities of the rows' top-k lists (vals, idx) [rows, k] as ds_topk returns them, as
+    whole rows [rows, n] (zeros elsewhere): the first ks[r] entries (int32 [rows]) at
+    temperature[r], cut to the shortest prefix that holds top_p[r] of their mass (both fp32
+    [rows]). out_list: an fp32 [rows, k] tensor that gets the entries' probabilities too.
+    rows_out=False: only the list is written. Returns the whole rows, or out_list."""
+    torch = _torch()
+    if vals.dim() != 2 or not vals.is_cuda or not vals.is_contiguous():
+        raise ValueError("vals must be a contiguous 2-D device tensor [rows, k]")
+    rows, k = vals.shape
+    dt, dev = dtype_code(vals), vals.device
+    if rows_out:
+        out, os = _out_rows(out, out_dtype, rows, n, dev)
+    else:
+        out, os = None, n
+        if out_list is None:
+            out_list = torch.empty((rows, k), dtype=torch.float32, device=dev)
+    f32 = torch.float32
+    _call("ds_topk_softmax", dev, stream,
+          (vals.data_ptr(), _operand(idx, "idx", torch.int32, (rows, k), dev), rows, k, dt,
+           _operand(ks, "ks", torch.int32, (rows,), dev), _operand(temperature, "temperature", f32, (rows,), dev),
+           _operand(top_p, "top_p", f32, (rows,), dev), n, out.data_ptr() if rows_out else None, os,
+           dtype_code(out) if rows_out else FP32, _operand(out_list, "out_list", f32, (rows, k), dev)))
+    return out if rows_out else out_list
+
+
+def ds_verify(target, draft, draft_tokens, accept_u, sample_u, draft_lens=None, out_tokens=None, out_accepted=None,
+              workspace=None, stream=None):
+    """Verification of drafted tokens: target [batch, drafts + 1, n] and draft [batch, drafts, n]
+    (or None: certain drafts) probabilities, bf16 or fp32; draft_tokens int32 and accept_u fp32
+    [batch, drafts]; sample_u fp32 [batch]; draft_lens int32 [batch]. See include/dstopk.h.
+
+    Returns (tokens [batch, drafts + 1] int32: the accepted drafts, the drawn token, then -1;
+    accepted [batch] int32).
+    """
+    torch = _torch()
+    batch, m, n, ts = _batch_rows(target, "target")
+    dt, dev, K = dtype_code(target), target.device, m - 1
+    if K < 0:
+        raise ValueError("target must hold at least one row per sequence")
+    dp, dstride = None, n
+    if draft is not None and K > 0:
+        b2, k2, n2, dstride = _batch_rows(draft, "draft")
+        if (b2, k2, n2) != (batch, K, n) or draft.dtype != target.dtype or draft.device != dev:
+            raise ValueError("draft must be [batch, drafts, n] of target's dtype on its device")
+        dp = draft.data_ptr()
+    if out_tokens is None:
+        out_tokens = torch.empty((batch, m), dtype=torch.int32, device=dev)
+    if out_accepted is None:
+        out_accepted = torch.empty((batch,), dtype=torch.int32, device=dev)
+    if K > 0 and (draft_tokens is None or accept_u is None) or sample_u is None:
+        raise ValueError("draft_tokens, accept_u and sample_u are needed")
+    i32, f32 = torch.int32, torch.float32
+    keep, ws, ws_bytes = _scratch(lib().ds_verify_workspace_size, batch, n, dt, workspace, dev, stream)
+    _call("ds_verify", dev, stream,
+          (target.data_ptr(), ts, dp, dstride, _operand(draft_tokens, "draft_tokens", i32, (batch, K), dev),
+           _operand(draft_lens, "draft_lens", i32, (batch,), dev),
+           _operand(accept_u, "accept_u", f32, (batch, K), dev), _operand(sample_u, "sample_u", f32, (batch,), dev),
+           batch, K, n, dt, _operand(out_tokens, "out_tokens", i32, (batch, m), dev),
+           _operand(out_accepted, "out_accepted", i32, (batch,), dev), ws, ws_bytes))
+    return out_tokens, out_accepted
 
 
 def stats_buffer(rows: int, slices: int, device):

@@ -37,6 +37,10 @@ UNITS = [(f"select_{dt}{'_stats' if st else ''}{'_ext' if ex else ''}", "ds_sele
            "-mllvm", "-amdgpu-kernarg-preload-count=15"])
          for d, dt in ((0, "bf16"), (1, "fp32")) for st in (0, 1) for ex in (0, 1)] + [
     ("merge", "ds_merge.hip", ["-mllvm", "-amdgpu-kernarg-preload-count=14"]),
+    ("route", "ds_route.hip", []),
+    ("probs", "ds_probs.hip", []),
+    ("verify", "ds_verify.hip", []),
+    ("rows_api", "ds_rows_api.cpp", []),
     ("noalloc", "ds_noalloc.hip", []),
     ("api", "ds_api.cpp", [])]
 

@@ -1,0 +1,297 @@
+// A sampler's probabilities: softmax of whole rows at a temperature, and of top-k lists.
+#include "ds_rows_device.h"
+
+namespace ds {
+namespace {
+
+constexpr int kSoftWaves = 8;
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kLog2E = 1.44269504088896341f;
+
+// exp((v - m) / t) with scale = log2(e) / t; exactly 1 at the maximum, infinities included.
+__device__ __forceinline__ float soft_exp(float v, float m, float scale) {
+  return v == m ? 1.0f : __builtin_amdgcn_exp2f((v - m) * scale);
+}
+
+// (maximum, sum) of two parts of a row. A part without any mass is (-inf, 0).
+__device__ __forceinline__ float2 soft_join(float2 a, float2 b, float scale) {
+  const float m = fmaxf(a.x, b.x);
+  if (m == kNegInf) return make_float2(kNegInf, 0.0f);
+  return make_float2(m, a.y * soft_exp(a.x, m, scale) + b.y * soft_exp(b.x, m, scale));
+}
+
+// A part of a greedy row: its maximum and the bits of the first index that holds it.
+__device__ __forceinline__ float2 first_join(float2 a, float2 b) {
+  const bool take = b.x > a.x || (b.x == a.x && __float_as_uint(b.y) < __float_as_uint(a.y));
+  return take ? b : a;
+}
+
+__device__ __forceinline__ float2 wave_xor(float2 v, int o) {
+  return make_float2(__shfl_xor(v.x, o), __shfl_xor(v.y, o));
+}
+
+__device__ __forceinline__ float row_scale(const float* temperature, int64_t r, bool* greedy) {
+  const float t = temperature ? temperature[r] : 1.0f;
+  *greedy = !(t > 0.0f);
+  return *greedy ? 0.0f : kLog2E / t;
+}
+
+// One workgroup per (row, slice): the slice's maximum and sum.
+template <int DT>
+__global__ __launch_bounds__(kSoftWaves * 64) void softmax_stats_kernel(SoftmaxParams p) {
+  using E = Elem<DT>;
+  using V = Vec<DT, E::kPer16>;
+  const int64_t unit = p.unit0 + blockIdx.x;
+  const int64_t r = unit / p.slices;
+  const int sl = static_cast<int>(unit - r * p.slices);
+  const int64_t lo = sl * p.slice, hi = lo + p.slice < p.n ? lo + p.slice : p.n;
+  const typename E::T* x = static_cast<const typename E::T*>(p.x) + r * p.row_stride;
+  bool greedy;
+  const float scale = row_scale(p.temperature, r, &greedy);
+  constexpr int N = E::kPer16;
+  float2 a = make_float2(kNegInf, greedy ? __uint_as_float(0xFFFFFFFFu) : 0.0f);
+  for (int64_t i = lo + static_cast<int64_t>(threadIdx.x) * N; i < hi; i += kSoftWaves * 64 * N) {
+    float v[N];
+    if (i + N <= hi) {
+      const typename V::type q = *reinterpret_cast<const typename V::unaligned*>(x + i);
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = E::widen(q[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = i + j < hi ? E::widen(x[i + j]) : kNegInf;
+    }
+    if (greedy) {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (v[j] > a.x) a = make_float2(v[j], __uint_as_float(static_cast<uint32_t>(i + j)));
+    } else {
+      float m = a.x;
+#pragma unroll
+      for (int j = 0; j < N; ++j) m = fmaxf(m, v[j]);
+      if (m != kNegInf) {
+        float z = a.y * soft_exp(a.x, m, scale);
+#pragma unroll
+        for (int j = 0; j < N; ++j) z += soft_exp(v[j], m, scale);
+        a = make_float2(m, z);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const float2 b = wave_xor(a, o);
+    a = greedy ? first_join(a, b) : soft_join(a, b, scale);
+  }
+  __shared__ float2 of_wave[kSoftWaves];
+  if ((threadIdx.x & 63) == 0) of_wave[threadIdx.x >> 6] = a;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kSoftWaves; ++w) a = greedy ? first_join(a, of_wave[w]) : soft_join(a, of_wave[w], scale);
+    p.part[unit] = a;
+  }
+}
+
+// One workgroup per (row, slice): joins the row's parts and writes the slice.
+template <int DT, int OT>
+__global__ __launch_bounds__(kSoftWaves * 64) void softmax_write_kernel(SoftmaxParams p) {
+  using E = Elem<DT>;
+  using O = Elem<OT>;
+  constexpr int N = E::kPer16;
+  using V = Vec<DT, N>;
+  using W = Vec<OT, N>;
+  const int64_t unit = p.unit0 + blockIdx.x;
+  const int64_t r = unit / p.slices;
+  const int sl = static_cast<int>(unit - r * p.slices);
+  const int64_t lo = sl * p.slice, hi = lo + p.slice < p.n ? lo + p.slice : p.n;
+  const typename E::T* x = static_cast<const typename E::T*>(p.x) + r * p.row_stride;
+  typename O::T* out = static_cast<typename O::T*>(p.out) + r * p.out_stride;
+  bool greedy;
+  const float scale = row_scale(p.temperature, r, &greedy);
+  const float2* part = p.part + r * p.slices;
+  const int lane = threadIdx.x & 63;
+  float2 a = make_float2(kNegInf, greedy ? __uint_as_float(0xFFFFFFFFu) : 0.0f);
+  for (int i = lane; i < p.slices; i += 64) a = greedy ? first_join(a, part[i]) : soft_join(a, part[i], scale);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const float2 b = wave_xor(a, o);
+    a = greedy ? first_join(a, b) : soft_join(a, b, scale);
+  }
+  const bool empty = a.x == kNegInf;
+  const int64_t first = greedy && !empty ? static_cast<int64_t>(__float_as_uint(a.y)) : -1;
+  const float inv = greedy || empty ? 0.0f : 1.0f / a.y;
+  for (int64_t i = lo + static_cast<int64_t>(threadIdx.x) * N; i < hi; i += kSoftWaves * 64 * N) {
+    float v[N];
+    const bool full = i + N <= hi;
+    if (greedy || empty) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = i + j == first ? 1.0f : 0.0f;
+    } else if (full) {
+      const typename V::type q = *reinterpret_cast<const typename V::unaligned*>(x + i);
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = soft_exp(E::widen(q[j]), a.x, scale) * inv;
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = i + j < hi ? soft_exp(E::widen(x[i + j]), a.x, scale) * inv : 0.0f;
+    }
+    if (full) {
+      typename W::type q;
+#pragma unroll
+      for (int j = 0; j < N; ++j) q[j] = O::narrow(v[j]);
+      *reinterpret_cast<typename W::unaligned*>(out + i) = q;
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (i + j < hi) out[i + j] = O::narrow(v[j]);
+    }
+  }
+}
+
+// One workgroup per (row, slice of the output): every workgroup of a row computes the list's
+// probabilities (at most 4096 entries, in double: the prefix's end is exact), clears its
+// slice and writes the entries that fall in it.
+constexpr int kListWaves = 8;
+constexpr int kListThreads = kListWaves * 64;
+
+template <class T>
+__device__ __forceinline__ T block_sum(T v, T* of_wave) {  // of_wave: kListWaves words of LDS
+  v = wave_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) of_wave[threadIdx.x >> 6] = v;
+  __syncthreads();
+  T t = 0;
+  for (int w = 0; w < kListWaves; ++w) t += of_wave[w];
+  return t;
+}
+
+template <int DT, int OT>
+__global__ __launch_bounds__(kListThreads) void list_softmax_kernel(ListSoftmaxParams p) {
+  using E = Elem<DT>;
+  using O = Elem<OT>;
+  constexpr int kPer = DS_MAX_K / kListThreads;  // entries per thread, consecutive
+  __shared__ double of_wave[kListWaves];
+  __shared__ int first_of_wave[kListWaves];
+  const int64_t unit = p.unit0 + blockIdx.x;
+  const int64_t r = unit / p.slices;
+  const int sl = static_cast<int>(unit - r * p.slices);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const typename E::T* vals = static_cast<const typename E::T*>(p.vals) + r * p.k;
+  const int32_t* idx = p.idx + r * p.k;
+  const float t = p.temperature ? p.temperature[r] : 1.0f;
+  const bool greedy = !(t > 0.0f);
+  int used = p.ks ? p.ks[r] : p.k;
+  used = used < 1 ? 1 : (used > p.k ? p.k : used);
+  const int per = (p.k + kListThreads - 1) / kListThreads;
+  const int base = threadIdx.x * per;
+  float v[kPer];
+  int at[kPer];
+  int first = p.k;  // the first entry that names an element: the list's maximum
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int i = base + j;
+    const bool live = j < per && i < used;
+    at[j] = live ? idx[i] : -1;
+    v[j] = live ? E::widen(vals[i]) : 0.0f;
+    if (at[j] < 0 || at[j] >= p.n) at[j] = -1;
+    if (at[j] >= 0 && first == p.k) first = i;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const int b = __shfl_xor(first, o);
+    first = b < first ? b : first;
+  }
+  if (lane == 0) first_of_wave[wave] = first;
+  __syncthreads();
+  for (int w = 0; w < kListWaves; ++w) first = first_of_wave[w] < first ? first_of_wave[w] : first;
+  const float m = first < p.k ? E::widen(vals[first]) : kNegInf;
+  double e[kPer];
+  double mine = 0.0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const bool live = at[j] >= 0 && m != kNegInf && (!greedy || base + j == first);
+    e[j] = !live ? 0.0
+           : v[j] == m ? 1.0
+                       : exp((static_cast<double>(v[j]) - static_cast<double>(m)) / static_cast<double>(t));
+    mine += e[j];
+  }
+  double total = block_sum(mine, of_wave);
+  if (p.top_p) {
+    // the mass before each entry: the waves before this one, the lanes before this one, then
+    // this thread's own entries
+    double before = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const double b = __shfl_up(before, o);
+      if (lane >= o) before += b;
+    }
+    before -= mine;
+    for (int w = 0; w < wave; ++w) before += of_wave[w];
+    const double most = static_cast<double>(p.top_p[r]) * total;
+    mine = 0.0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const double q = e[j];
+      if (!(before < most) && base + j != first) e[j] = 0.0;
+      before += q;
+      mine += e[j];
+    }
+    total = block_sum(mine, of_wave);
+  }
+  const double inv = total > 0.0 ? 1.0 / total : 0.0;
+  if (p.out_list && sl == 0) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (j < per && base + j < p.k) p.out_list[r * p.k + base + j] = static_cast<float>(e[j] * inv);
+  }
+  if (!p.out) return;
+  const int64_t lo = sl * p.slice, hi = lo + p.slice < p.n ? lo + p.slice : p.n;
+  typename O::T* out = static_cast<typename O::T*>(p.out) + r * p.out_stride;
+  constexpr int N = O::kPer16;
+  using W = Vec<OT, N>;
+  for (int64_t i = lo + static_cast<int64_t>(threadIdx.x) * N; i < hi; i += kListThreads * N) {
+    if (i + N <= hi) {
+      *reinterpret_cast<typename W::unaligned*>(out + i) = typename W::type(0);
+    } else {
+      for (int j = 0; i + j < hi; ++j) out[i + j] = O::narrow(0.0f);
+    }
+  }
+  __syncthreads();  // the zeros are written before the entries go over them
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    if (at[j] >= lo && at[j] < hi && e[j] > 0.0) out[at[j]] = O::narrow(static_cast<float>(e[j] * inv));
+}
+
+}  // namespace
+
+RowCut cut_softmax(int64_t rows, int64_t n) {
+  constexpr int64_t step = kSoftWaves * 64 * 8;
+  if (rows < 1) rows = 1;
+  const int64_t most = (n + step - 1) / step, want = (kCus * 4 + rows - 1) / rows;
+  const int64_t slices = want < 1 ? 1 : (want > most ? most : want);
+  const int64_t slice = ((n + slices - 1) / slices + step - 1) / step * step;
+  return {slice, static_cast<int32_t>((n + slice - 1) / slice)};
+}
+
+RowCut cut_list_softmax(int64_t rows, int64_t n) { return cut_softmax(rows, n); }
+
+template <int DT>
+static hipError_t softmax_dt(int out_dtype, const SoftmaxParams& p, hipStream_t s) {
+  const int64_t units = p.rows * p.slices;
+  const hipError_t e = launch_units(softmax_stats_kernel<DT>, p, units, kSoftWaves * 64, s);
+  if (e != hipSuccess) return e;
+  return out_dtype == DS_BF16 ? launch_units(softmax_write_kernel<DT, DS_BF16>, p, units, kSoftWaves * 64, s)
+                              : launch_units(softmax_write_kernel<DT, DS_FP32>, p, units, kSoftWaves * 64, s);
+}
+
+hipError_t launch_softmax(int dtype, int out_dtype, const SoftmaxParams& p, hipStream_t s) {
+  return dtype == DS_BF16 ? softmax_dt<DS_BF16>(out_dtype, p, s) : softmax_dt<DS_FP32>(out_dtype, p, s);
+}
+
+hipError_t launch_list_softmax(int dtype, int out_dtype, const ListSoftmaxParams& p, hipStream_t s) {
+  const int64_t units = p.rows * p.slices;
+  if (dtype == DS_BF16)
+    return out_dtype == DS_BF16 ? launch_units(list_softmax_kernel<DS_BF16, DS_BF16>, p, units, kListThreads, s)
+                                : launch_units(list_softmax_kernel<DS_BF16, DS_FP32>, p, units, kListThreads, s);
+  return out_dtype == DS_BF16 ? launch_units(list_softmax_kernel<DS_FP32, DS_BF16>, p, units, kListThreads, s)
+                              : launch_units(list_softmax_kernel<DS_FP32, DS_FP32>, p, units, kListThreads, s);
+}
+
+}  // namespace ds
