@@ -25,6 +25,10 @@ struct RouteParams {
   float* out_weights;
   int32_t* out_idx;
   int32_t* counts;
+  // set by the launcher: experts of a group (all without a limit), and how lanes share them
+  int32_t run;
+  int32_t per_lane;
+  int32_t lanes_log2;
 };
 
 struct RouteGradParams {
