@@ -1,4 +1,6 @@
 // Routing to experts and its gradient.
+#include <type_traits>
+
 #include "ds_rows_device.h"
 
 namespace ds {
@@ -9,100 +11,242 @@ constexpr float kNegInf = -__builtin_huge_valf();
 constexpr double kNone = -__builtin_huge_val();  // the selection score of a masked or taken expert
 constexpr float kLog2E = 1.44269504088896341f;
 
+// The value of a lane of the other half of 2^(LEVEL + 1) lanes, where the lanes of a half hold
+// equal values (a butterfly's do after LEVEL levels): by data-parallel moves, no LDS.
+template <int LEVEL>
+__device__ __forceinline__ uint32_t from_partner(uint32_t v) {
+  if constexpr (LEVEL == 0) return __builtin_amdgcn_update_dpp(0u, v, 0xB1, 0xF, 0xF, false);   // xor 1
+  if constexpr (LEVEL == 1) return __builtin_amdgcn_update_dpp(0u, v, 0x4E, 0xF, 0xF, false);   // xor 2
+  if constexpr (LEVEL == 2) return __builtin_amdgcn_update_dpp(0u, v, 0x141, 0xF, 0xF, false);  // 8 lanes reversed
+  if constexpr (LEVEL == 3) return __builtin_amdgcn_update_dpp(0u, v, 0x140, 0xF, 0xF, false);  // 16 lanes reversed
+  if constexpr (LEVEL == 4) {
+    const auto q = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return (threadIdx.x & 16u) ? q[0] : q[1];
+  }
+  if constexpr (LEVEL == 5) {
+    const auto q = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return (threadIdx.x & 32u) ? q[0] : q[1];
+  }
+}
+template <int LEVEL>
+__device__ __forceinline__ int from_partner(int v) {
+  return static_cast<int>(from_partner<LEVEL>(static_cast<uint32_t>(v)));
+}
+template <int LEVEL>
+__device__ __forceinline__ float from_partner(float v) {
+  return __uint_as_float(from_partner<LEVEL>(__float_as_uint(v)));
+}
+template <int LEVEL>
+__device__ __forceinline__ double from_partner(double v) {
+  return __hiloint2double(from_partner<LEVEL>(__double2hiint(v)), from_partner<LEVEL>(__double2loint(v)));
+}
+
+// f over 2^LEVELS neighbouring lanes, in all of them.
+template <int LEVELS, class T, class F>
+__device__ __forceinline__ T row_reduce(T v, F f) {
+  if constexpr (LEVELS > 0) v = f(v, from_partner<0>(v));
+  if constexpr (LEVELS > 1) v = f(v, from_partner<1>(v));
+  if constexpr (LEVELS > 2) v = f(v, from_partner<2>(v));
+  if constexpr (LEVELS > 3) v = f(v, from_partner<3>(v));
+  if constexpr (LEVELS > 4) v = f(v, from_partner<4>(v));
+  if constexpr (LEVELS > 5) v = f(v, from_partner<5>(v));
+  return v;
+}
+
+template <class T>
+__device__ __forceinline__ T plus(T a, T b) { return a + b; }
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
 // ------------------------------------------------------------------ the exact choice of a row
-// A whole wave chooses for one row with everything that decides in double; c: LDS room of
-// p.experts doubles that is the wave's own. Rows that the fast kernel cannot decide come here,
-// and every row where no fast kernel fits.
-template <int DT, int SCORE>
-__device__ __forceinline__ void route_row_exact(const RouteParams& p, int64_t r, double* c) {
+// A whole wave chooses for one row with everything that decides in double; expert e is in lane
+// e % 64, room: exact_room(64 V) bytes of LDS, the wave's own. Rows that the fast kernel cannot
+// decide come here, and every row where no fast kernel fits. Out of line: its registers would
+// otherwise count against the fast kernel's, which seldom calls it. It reads the parameters
+// where the launch left them (a kernel's only argument), with scalar loads. A lone wave waits
+// for every one of its instructions, so what is done per row is kept short: a row's time is
+// the tail of a launch in which any row comes here.
+__device__ __forceinline__ const void* params_of_launch() {
+  return (const void*)__builtin_amdgcn_kernarg_segment_ptr();
+}
+
+__device__ __forceinline__ uint64_t uniform(uint64_t v) {
+  return static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32)))) << 32 |
+         static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v)));
+}
+
+// LDS bytes of a row with room for n experts: their scores, their indices, the lanes' best.
+__host__ __device__ constexpr int exact_room(int n) { return n * 12 + 64 * 4; }
+
+// The two largest of a group's selection scores.
+struct Top2 {
+  double a, b;
+};
+__device__ __forceinline__ Top2 join(Top2 u, Top2 v) {
+  const double lo = u.a > v.a ? v.a : u.a, next = u.b > v.b ? u.b : v.b;
+  return {u.a > v.a ? u.a : v.a, lo > next ? lo : next};
+}
+template <int LEVEL>
+__device__ __forceinline__ Top2 from_partner(Top2 v) {
+  return {from_partner<LEVEL>(v.a), from_partner<LEVEL>(v.b)};
+}
+
+template <int DT, int SCORE, int V>
+__device__ __noinline__ void route_row_exact(const void* params, int64_t row, uint8_t* lds) {
   using E = Elem<DT>;
+  typedef const __attribute__((address_space(4))) RouteParams* ScalarParams;
+  const ScalarParams p = (ScalarParams)uniform(reinterpret_cast<uint64_t>(params));
+  const int64_t r = static_cast<int64_t>(uniform(static_cast<uint64_t>(row)));
+  const typename E::T* x = static_cast<const typename E::T*>(p->x) + r * p->row_stride;
+  const float* const biases = p->bias;
+  const int experts = p->experts, k = p->k, groups = p->groups, size = p->group_size, topk_groups = p->topk_groups;
+  const bool two = p->group_top > 1, renorm = p->renorm != 0;
+  const float scale = p->scale;
+  float* const out_weights = p->out_weights;
+  int32_t *const out_idx = p->out_idx, *const counts = p->counts;
+  // (as LDS addresses: a generic pointer's accesses take longer)
+  const auto room = (__attribute__((address_space(3))) double*)reinterpret_cast<double*>(lds);
+  const auto room_at = (__attribute__((address_space(3))) int32_t*)(room + 64 * V);
+  const auto lane_best = (__attribute__((address_space(3))) float*)(room_at + 64 * V);
   const int lane = threadIdx.x & 63;
-  const typename E::T* x = static_cast<const typename E::T*>(p.x) + r * p.row_stride;
-  float m = kNegInf;
-  double inv = 1.0;
-  if constexpr (SCORE == DS_SCORE_SOFTMAX) {
-    for (int e = lane; e < p.experts; e += 64) m = fmaxf(m, E::widen(x[e]));
-    m = wave_max(m);
-  }
-  const auto term = [&](float v) {  // the score, the softmax's without its division
-    if constexpr (SCORE == DS_SCORE_SOFTMAX)
-      return v == kNegInf ? 0.0 : v == m ? 1.0 : exp(static_cast<double>(v) - static_cast<double>(m));
-    else
-      return 1.0 / (1.0 + exp(-static_cast<double>(v)));
-  };
-  if constexpr (SCORE == DS_SCORE_SOFTMAX) {
-    double z = 0.0;
-    for (int e = lane; e < p.experts; e += 64) z += term(E::widen(x[e]));
-    z = wave_sum(z);
-    inv = z > 0.0 ? 1.0 / z : 0.0;
-  }
-  const bool limited = p.topk_groups < p.groups;
-  // without a bias the order is that of the logits; sums of scores for the groups are not
-  const bool sums = limited && !p.bias && p.group_top > 1;
-  const auto choice = [&](int e, bool score) {
-    const float v = E::widen(x[e]);
-    if (v == kNegInf) return kNone;
-    if (p.bias) return term(v) * inv + static_cast<double>(p.bias[e]);
-    return score ? term(v) * inv : static_cast<double>(v);
-  };
-  for (int e = lane; e < p.experts; e += 64) c[e] = choice(e, sums);
-  __builtin_amdgcn_wave_barrier();
-  if (limited) {
-    double top = kNone, second = kNone;
-    if (lane < p.groups)
-      for (int j = 0; j < p.group_size; ++j) {
-        const double q = c[lane * p.group_size + j];
-        second = q > top ? top : (q > second ? q : second);
-        top = q > top ? q : top;
-      }
-    const double score = p.group_top > 1 && second != kNone ? top + second : top;
-    int rank = 0;
-    for (int o = 0; o < p.groups; ++o) {
-      const double other = __shfl(score, o);
-      rank += other > score || (other == score && o < lane);
-    }
-    const uint64_t keep = __ballot(lane < p.groups && rank < p.topk_groups);
-    __builtin_amdgcn_wave_barrier();
-    for (int e = lane; e < p.experts; e += 64) {
-      if (!((keep >> (e / p.group_size)) & 1)) c[e] = kNone;
-      else if (sums) c[e] = choice(e, false);
-    }
-    __builtin_amdgcn_wave_barrier();
-  }
-  int my_e = -1;
-  for (int j = 0; j < p.k; ++j) {
-    double best = kNone;
-    int at = 0x7FFFFFFF;
-    for (int e = lane; e < p.experts; e += 64)
-      if (c[e] > best) best = c[e], at = e;
+  float xv[V], bias[V];
+  double s[V], c[V];
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-      const double ob = __shfl_xor(best, o);
-      const int oa = __shfl_xor(at, o);
-      if (ob > best || (ob == best && oa < at)) best = ob, at = oa;
+  for (int v = 0; v < V; ++v) {
+    const int e = v * 64 + lane;
+    xv[v] = e < experts ? E::widen(x[e]) : kNegInf;
+    bias[v] = biases && e < experts ? biases[e] : 0.0f;
+  }
+  if constexpr (SCORE == DS_SCORE_SOFTMAX) {
+    float m = kNegInf;
+#pragma unroll
+    for (int v = 0; v < V; ++v) m = fmaxf(m, xv[v]);
+    m = row_reduce<6>(m, [](float a, float b) { return larger(a, b); });
+    double z = 0.0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      s[v] = xv[v] == kNegInf ? 0.0 : xv[v] == m ? 1.0 : exp(static_cast<double>(xv[v]) - static_cast<double>(m));
+      z += s[v];
+      if (V > 4) __builtin_amdgcn_sched_barrier(0);  // one exp at a time: the registers of many cost more
     }
-    if (at == 0x7FFFFFFF) break;  // nothing left
-    if ((at & 63) == lane) c[at] = kNone;
-    if (lane == j) my_e = at;
+    z = row_reduce<6>(z, plus<double>);
+    const double inv = z > 0.0 ? 1.0 / z : 0.0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v] *= inv;
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      s[v] = 1.0 / (1.0 + exp(-static_cast<double>(xv[v])));
+      if (V > 4) __builtin_amdgcn_sched_barrier(0);
+    }
   }
-  const double s = my_e >= 0 ? term(E::widen(x[my_e])) * inv : 0.0;
-  const double total = wave_sum(s);
-  if (lane < p.k) {
-    const double w = !p.renorm ? s : total > 0.0 ? s / total : 0.0;
-    if (p.out_weights) p.out_weights[r * p.k + lane] = static_cast<float>(w * static_cast<double>(p.scale));
-    if (p.out_idx) p.out_idx[r * p.k + lane] = my_e;
-    if (p.counts && my_e >= 0) atomicAdd(p.counts + my_e, 1);
+  const bool limited = topk_groups < groups;
+  // without a bias the order is that of the logits; sums of scores for the groups are not
+  const bool sums = limited && !biases && two;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    c[v] = xv[v] == kNegInf ? kNone
+           : biases         ? s[v] + static_cast<double>(bias[v])
+                            : static_cast<double>(xv[v]);
+  if (limited) {
+    wave_sync();
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (v * 64 + lane < experts) room[v * 64 + lane] = sums && c[v] != kNone ? s[v] : c[v];
+    wave_sync();
+    int levels = 6;  // 2^levels lanes share a group
+    while ((64 >> levels) < groups) --levels;
+    const int group = lane >> levels, part = lane & ((1 << levels) - 1);
+    Top2 top = {kNone, kNone};
+    if (group < groups)
+      for (int j = part; j < size; j += 1 << levels)
+        top = join(top, Top2{room[group * size + j], kNone});
+    if (levels > 0) top = join(top, from_partner<0>(top));
+    if (levels > 1) top = join(top, from_partner<1>(top));
+    if (levels > 2) top = join(top, from_partner<2>(top));
+    if (levels > 3) top = join(top, from_partner<3>(top));
+    if (levels > 4) top = join(top, from_partner<4>(top));
+    if (levels > 5) top = join(top, from_partner<5>(top));
+    const double score = two && top.b != kNone ? top.a + top.b : top.a;
+    int rank = 0;
+    for (int o0 = 0; o0 < groups; o0 += 8)
+#pragma unroll
+      for (int o = o0; o < o0 + 8; ++o) {
+        const double other = __shfl(score, (o << levels) & 63);
+        rank += (o < groups) & ((other > score) | ((other == score) & (o < group)));
+      }
+    const uint64_t keep = __ballot(group < groups && rank < topk_groups);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = v * 64 + lane;
+      if (e < experts && !((keep >> ((e / size) << levels)) & 1)) c[v] = kNone;
+    }
   }
-  __builtin_amdgcn_wave_barrier();
+  // A bound that at least k experts reach, the k-th largest of the lanes' best (everything, if
+  // fewer lanes hold any); rounded to fp32, as what is compared with it. The experts that reach
+  // it are listed and ranked by counting.
+  float best = kNegInf;
+#pragma unroll
+  for (int v = 0; v < V; ++v) best = fmaxf(best, static_cast<float>(c[v]));
+  wave_sync();
+  lane_best[lane] = best;
+  wave_sync();
+  int above = 0;
+#pragma unroll 16
+  for (int o = 0; o < 64; ++o) above += lane_best[o] > best;
+  const float bound = -row_reduce<6>(above < k ? -best : kNegInf, [](float a, float b) { return larger(a, b); });
+  int listed = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const bool in = c[v] > kNone && static_cast<float>(c[v]) >= bound;
+    const uint64_t mask = __ballot(in);
+    if (in) {
+      const int at = listed + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
+                                                        __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0u));
+      room[at] = c[v];
+      room_at[at] = v * 64 + lane;
+    }
+    listed += __builtin_popcountll(mask);
+  }
+  wave_sync();
+  int rank[V];
+  double total = 0.0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    rank[v] = k;
+    const bool in = c[v] > kNone && static_cast<float>(c[v]) >= bound;
+    if (__any(in)) {
+      int n = 0;
+#pragma unroll 4
+      for (int o = 0; o < listed; ++o) n += (room[o] > c[v]) | ((room[o] == c[v]) & (room_at[o] < v * 64 + lane));
+      rank[v] = in ? n : k;
+      total += rank[v] < k ? s[v] : 0.0;
+    }
+  }
+  total = row_reduce<6>(total, plus<double>);
+  const double factor = static_cast<double>(scale);
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (rank[v] < k) {
+      const double w = !renorm ? s[v] : total > 0.0 ? s[v] / total : 0.0;
+      if (out_weights) out_weights[r * k + rank[v]] = static_cast<float>(w * factor);
+      if (out_idx) out_idx[r * k + rank[v]] = v * 64 + lane;
+      if (counts) atomicAdd(counts + v * 64 + lane, 1);
+    }
+  if (lane >= listed && lane < k) {  // slots that no expert is left for
+    if (out_weights) out_weights[r * k + lane] = 0.0f;
+    if (out_idx) out_idx[r * k + lane] = -1;
+  }
+  wave_sync();
 }
 
 template <int DT, int SCORE>
 __global__ __launch_bounds__(kRouteWaves * 64) void route_exact_kernel(RouteParams p) {
-  __shared__ double c[kRouteWaves][DS_MAX_EXPERTS];
+  __shared__ __attribute__((aligned(16))) uint8_t room[kRouteWaves][exact_room(DS_MAX_EXPERTS)];
   const int wave = threadIdx.x >> 6;
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRouteWaves + wave; r < p.rows;
        r += static_cast<int64_t>(gridDim.x) * kRouteWaves)
-    route_row_exact<DT, SCORE>(p, r, c[wave]);
+    route_row_exact<DT, SCORE, DS_MAX_EXPERTS / 64>(params_of_launch(), r, room[wave]);
 }
 
 // ------------------------------------------------------------------------- the fast kernel
@@ -124,33 +268,6 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_exact_kernel(RoutePara
 // conversion add 2. Two keys: 2 * 6 + 1 and 2 * 66 + 1. Logits themselves: the subtraction and the
 // conversion, 2 * 1.5. bf16 logits are keys without loss.
 enum RouteMode { kBySigmoid, kBySoftmax, kByLogit };
-
-template <int LEVEL>
-__device__ __forceinline__ uint32_t from_partner(uint32_t v) {
-  // a lane of the other half of 2^(LEVEL + 1) lanes, whose values within a half are equal
-  if constexpr (LEVEL == 0) return __builtin_amdgcn_update_dpp(0u, v, 0xB1, 0xF, 0xF, false);   // xor 1
-  if constexpr (LEVEL == 1) return __builtin_amdgcn_update_dpp(0u, v, 0x4E, 0xF, 0xF, false);   // xor 2
-  if constexpr (LEVEL == 2) return __builtin_amdgcn_update_dpp(0u, v, 0x141, 0xF, 0xF, false);  // 8 lanes reversed
-  if constexpr (LEVEL == 3) return __builtin_amdgcn_update_dpp(0u, v, 0x140, 0xF, 0xF, false);  // 16 lanes reversed
-  if constexpr (LEVEL == 4) {
-    const auto q = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    return (threadIdx.x & 16u) ? q[0] : q[1];
-  }
-}
-template <int LEVEL>
-__device__ __forceinline__ float from_partner(float v) {
-  return __uint_as_float(from_partner<LEVEL>(__float_as_uint(v)));
-}
-
-template <int LEVELS, class T, class F>
-__device__ __forceinline__ T row_reduce(T v, F f) {
-  if constexpr (LEVELS > 0) v = f(v, from_partner<0>(v));
-  if constexpr (LEVELS > 1) v = f(v, from_partner<1>(v));
-  if constexpr (LEVELS > 2) v = f(v, from_partner<2>(v));
-  if constexpr (LEVELS > 3) v = f(v, from_partner<3>(v));
-  if constexpr (LEVELS > 4) v = f(v, from_partner<4>(v));
-  return v;
-}
 
 __device__ __forceinline__ void order2(uint32_t& a, uint32_t& b) {  // a >= b
   const uint32_t hi = a > b ? a : b, lo = a > b ? b : a;
@@ -181,31 +298,47 @@ __device__ __forceinline__ void clean_down(uint32_t* a) {
       if ((i & d) == 0) order2(a[i], a[i + d]);
 }
 
-template <int LEVEL, int KP>
-__device__ __forceinline__ void merge_partner(uint32_t* list) {
-  uint32_t t[KP];
+// The KP best of a sorted list and another's (given reversed: o[i] is its entry KP - 1 - i);
+// `dropped` keeps the best key that was not among them.
+template <int KP>
+__device__ __forceinline__ void merge_down(uint32_t* list, const uint32_t* o, uint32_t& dropped) {
 #pragma unroll
   for (int i = 0; i < KP; ++i) {
-    const uint32_t o = from_partner<LEVEL>(list[KP - 1 - i]);
-    t[i] = list[i] > o ? list[i] : o;
+    const uint32_t hi = larger(list[i], o[i]);
+    dropped = larger(dropped, list[i] < o[i] ? list[i] : o[i]);
+    list[i] = hi;
   }
-#pragma unroll
-  for (int i = 0; i < KP; ++i) list[i] = t[i];
   clean_down<KP>(list);
 }
 
+template <int LEVEL, int KP>
+__device__ __forceinline__ void merge_partner(uint32_t* list, uint32_t& dropped) {
+  uint32_t o[KP];
+#pragma unroll
+  for (int i = 0; i < KP; ++i) o[i] = from_partner<LEVEL>(list[KP - 1 - i]);
+  dropped = larger(dropped, from_partner<LEVEL>(dropped));
+  merge_down<KP>(list, o, dropped);
+}
+
 template <int DT, int SCORE, int MODE, int L, int V, int KP>
-__global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteParams p) {
+__global__ __launch_bounds__(kRouteWaves * 64, V == 32 && KP == 16 ? 3 : 4) void route_kernel(RouteParams p) {
   using E = Elem<DT>;
   using T = typename E::T;
-  constexpr int N = E::kPer16 < V ? E::kPer16 : V;
+  constexpr int N = E::kPer16;
+  static_assert(V % N == 0, "a lane's experts are whole vectors");
   constexpr int LEVELS = __builtin_ctz(L), IB = __builtin_ctz(L * V), QB = 32 - IB;
   constexpr uint32_t kFirst = 1u << IB;  // the smallest key of an expert that can be chosen
   constexpr float kTop = static_cast<float>((1 << (QB < 24 ? QB : 24)) - 64);  // whole numbers of fp32
   constexpr bool kExactKeys = MODE == kByLogit && DT == DS_BF16;
   constexpr int kSlack = MODE == kBySigmoid ? 13 : MODE == kBySoftmax ? 133 : kExactKeys ? -1 : 4;
-  __shared__ double room[kRouteWaves][L * V];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, sub = lane & (L - 1);
+  constexpr bool kSteps = MODE != kByLogit;
+  constexpr int kPad = V + 4;  // (lanes read their V steps by 16 bytes: no two in the same banks)
+  constexpr int kLane = V * static_cast<int>(sizeof(T)) + 16;  // a lane's experts in LDS; the 16 bytes spread the banks
+  constexpr int kTile = 64 * kLane, kExact = exact_room(L * V);
+  // a wave's rows on their way to the lanes that take them, or route_row_exact's room
+  __shared__ __attribute__((aligned(16))) uint8_t room[kRouteWaves][kTile > kExact ? kTile : kExact];
+  __shared__ __attribute__((aligned(16))) float steps[kSteps ? L * kPad : 4];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, sub = lane & (L - 1);
   const int group = sub >> p.lanes_log2, part = sub & ((1 << p.lanes_log2) - 1);
   const int first = group * p.run + part * p.per_lane;  // the lane's first expert
   const bool limited = p.topk_groups < p.groups;
@@ -214,13 +347,14 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteParams p) 
   if (group >= p.experts / p.run || have < 0) have = 0;
   const bool full = __ballot(have != V) == 0;
 
-  // c = s + b as a key: (s + b - least b) * per_unit, plus one
-  float step[V];
+  // c = s + b as a key: (s + b - least b) * per_unit + 1; `steps` holds the bias' part by
+  // position, and -inf (key 0) where there is no expert
   float per_unit = kTop;
   bool undecided = false;  // no key can hold the biases' range
-  if constexpr (MODE != kByLogit) {
-    float lo = __builtin_huge_valf(), hi = kNegInf;
+  if constexpr (kSteps) {
+    float lo = 0.0f, hi = 0.0f;
     if (p.bias) {
+      lo = __builtin_huge_valf(), hi = kNegInf;
       for (int e = lane; e < p.experts; e += 64) {
         const float b = p.bias[e];
         hi = fmaxf(hi, b);
@@ -228,35 +362,75 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteParams p) 
       }
       hi = wave_max(hi);
       lo = -wave_max(-lo);
-    } else {
-      lo = hi = 0.0f;
     }
     const float range = hi - lo + 1.0f;
     undecided = !(range < 1e30f);
     per_unit = kTop / range;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      step[v] = p.bias && v < have ? fmaf(p.bias[first + v] - lo, per_unit, 1.0f) : 1.0f;
+    for (int i = threadIdx.x; i < L * V; i += kRouteWaves * 64) {
+      const int of = i / V, v = i % V, run_at = (of & ((1 << p.lanes_log2) - 1)) * p.per_lane + v;
+      const int e = (of >> p.lanes_log2) * p.run + run_at;
+      float q = kNegInf;
+      if (v < p.per_lane && run_at < p.run && e < p.experts)
+        q = p.bias ? fmaf(p.bias[e] - lo, per_unit, 1.0f) : 1.0f;
+      steps[of * kPad + v] = q;
+    }
+    __syncthreads();
   }
 
   const T* xs = static_cast<const T*>(p.x);
   constexpr int kRows = 64 / L;
-  for (int64_t r0 = (static_cast<int64_t>(blockIdx.x) * kRouteWaves + wave) * kRows; r0 < p.rows;
-       r0 += static_cast<int64_t>(gridDim.x) * kRouteWaves * kRows) {
+  const int64_t first_row = (static_cast<int64_t>(blockIdx.x) * kRouteWaves + wave) * kRows;
+  const int64_t row_step = static_cast<int64_t>(gridDim.x) * kRouteWaves * kRows;
+  // the rows of the next turn are loaded while this turn's are worked on
+  typename Vec<DT, N>::type ahead[V / N];
+  const auto fetch = [&](int64_t r0) {
+    if (full) {  // 64 vectors in memory's order at a time
+#pragma unroll
+      for (int i = 0; i < V / N; ++i) {
+        const int at = i * 64 + lane, of = at / (L * V / N);
+        const int64_t r = r0 + of < p.rows ? r0 + of : p.rows - 1;
+        ahead[i] = *reinterpret_cast<const typename Vec<DT, N>::unaligned*>(xs + r * p.row_stride +
+                                                                           at % (L * V / N) * N);
+      }
+    } else {
+      const int64_t r = r0 + lane / L < p.rows ? r0 + lane / L : p.rows - 1;
+      const T* row = xs + r * p.row_stride;
+      int last = have > 0 ? first + have - 1 : 0;  // slots past the lane's experts load its last one
+      asm("" : "+v"(last));                        // (not kept as one address per slot)
+#pragma unroll
+      for (int v = 0; v < V; ++v) ahead[v / N][v % N] = row[first + v < last ? first + v : last];
+    }
+  };
+  // Turns are taken 64 at a time; lane i keeps which rows of turn i need the exact choice.
+  for (int64_t turn0 = first_row; turn0 < p.rows; turn0 += 64 * row_step) {
+  fetch(turn0);
+  uint64_t left = 0;
+  int turn = 0;
+  for (int64_t r0 = turn0; turn < 64 && r0 < p.rows; r0 += row_step, ++turn) {
     const int64_t r = r0 + lane / L < p.rows ? r0 + lane / L : p.rows - 1;
     const T* row = xs + r * p.row_stride;
     float x[V];
-    if (full) {
+    if (full) {  // through LDS, so that each lane has its run of experts
+      typedef typename Vec<DT, N>::type VT;
+      wave_sync();
 #pragma unroll
-      for (int v = 0; v < V; v += N) {
-        const typename Vec<DT, N>::type q = *reinterpret_cast<const typename Vec<DT, N>::unaligned*>(row + first + v);
-#pragma unroll
-        for (int j = 0; j < N; ++j) x[v + j] = E::widen(q[j]);
+      for (int i = 0; i < V / N; ++i) {
+        const int at = i * 64 + lane;
+        *reinterpret_cast<VT*>(room[wave] + at / (V / N) * kLane + at % (V / N) * 16) = ahead[i];
       }
-    } else {
+      wave_sync();
 #pragma unroll
-      for (int v = 0; v < V; ++v) x[v] = v < have ? E::widen(row[first + v]) : kNegInf;
+      for (int i = 0; i < V / N; ++i) ahead[i] = *reinterpret_cast<const VT*>(room[wave] + lane * kLane + i * 16);
     }
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = E::widen(ahead[v / N][v % N]);
+    if (!full) {
+      int n = have;
+      asm volatile("" : "+v"(n));  // compared in every turn, not kept as one mask per slot
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[v] = v < n ? x[v] : kNegInf;
+    }
+    if (r0 + row_step < p.rows) fetch(r0 + row_step);
     // the softmax's maximum and sum
     float m = 0.0f, inv = 1.0f;
     const bool soft = SCORE == DS_SCORE_SOFTMAX;
@@ -278,82 +452,87 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteParams p) 
       inv = 1.0f / z;  // at least one term is 1
     }
     uint32_t key[V];
+    const uint32_t place = static_cast<uint32_t>(L * V - 1 - sub * V);  // (its low bits are ones: place - v is place ^ v)
+    float least = x[0];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       uint32_t q;
+      const float step = kSteps ? steps[sub * kPad + v] : 0.0f;
       if constexpr (MODE == kBySigmoid) {
         const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x[v] * -kLog2E));
-        q = static_cast<uint32_t>(fmaf(s, per_unit, step[v]));
+        q = static_cast<uint32_t>(fmaf(s, per_unit, step));
       } else if constexpr (MODE == kBySoftmax) {
-        q = static_cast<uint32_t>(fmaf(e[v] * inv, per_unit, step[v]));
+        q = static_cast<uint32_t>(fmaf(e[v] * inv, per_unit, step));
       } else if constexpr (DT == DS_BF16) {
         const uint32_t u = __float_as_uint(x[v] + 0.0f);  // -0 as +0
         q = ((u ^ (static_cast<int32_t>(u) < 0 ? 0xFFFFFFFFu : 0x80000000u)) >> 16) + 1u;
       } else {
         q = static_cast<uint32_t>(fmaf(fmaxf(x[v] - m, -32.0f), kTop / 32.0f, kTop + 1.0f));
       }
-      q = x[v] == kNegInf ? 0u : q;
-      key[v] = (q << IB) | static_cast<uint32_t>(L * V - 1 - (sub * V + v));
+      key[v] = (q << IB) | (place ^ static_cast<uint32_t>(v));
+      least = fminf(least, x[v]);
     }
-    // a lane's KP best
-    uint32_t list[KP];
+    if (__any(least == kNegInf)) {  // masked logits
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = x[v] == kNegInf ? 0u : key[v];
+    }
+    // a lane's KP best; the barriers keep one block's network from being mixed with the next's,
+    // which takes more registers than it gains
+    uint32_t list[KP], dropped = 0u;
 #pragma unroll
     for (int i = 0; i < KP; ++i) list[i] = i < V ? key[i] : 0u;
     sort_down<(V < KP ? V : KP)>(list);
 #pragma unroll
     for (int b = KP; b < V; b += KP) {
-      uint32_t t[KP];
+      __builtin_amdgcn_sched_barrier(0);
+      uint32_t t[KP], o[KP];
 #pragma unroll
       for (int i = 0; i < KP; ++i) t[i] = key[b + i];
       sort_down<KP>(t);
 #pragma unroll
-      for (int i = 0; i < KP; ++i) list[i] = list[i] > t[KP - 1 - i] ? list[i] : t[KP - 1 - i];
-      clean_down<KP>(list);
+      for (int i = 0; i < KP; ++i) o[i] = t[KP - 1 - i];
+      merge_down<KP>(list, o, dropped);
     }
     bool close = undecided || (MODE == kByLogit && m == __builtin_huge_valf());
-    bool out = false;  // the lane's group is left out
-    const auto rank_groups = [&] {
+    const auto rank_groups = [&](auto level) {  // of the lists of 2^level lanes
       const uint32_t a = list[0] >> IB, b = list[1] >> IB;
       close |= p.group_top > 1 && a != 0u && b == 0u;  // a sum of one: not comparable in steps
       const uint32_t sum = p.group_top > 1 ? a + b : a;
       const uint32_t mine = (sum << 6) | static_cast<uint32_t>(63 - group);
-      int rank = 0;
-      for (int o = 0; o < p.groups; ++o)
-        rank += static_cast<uint32_t>(__shfl(static_cast<int>(mine), (lane & ~(L - 1)) + (o << p.lanes_log2))) > mine;
-      out = rank >= p.topk_groups;
-      const auto least = [](uint32_t u, uint32_t w) { return u < w ? u : w; };
-      const auto most = [](uint32_t u, uint32_t w) { return u > w ? u : w; };
-      const uint32_t in = row_reduce<LEVELS>(out ? 0xFFFFFFFFu : sum, least);
-      const uint32_t over = row_reduce<LEVELS>(out ? sum : 0u, most);
-      close |= over != 0u && static_cast<int>(in - over) <= (p.group_top > 1 ? 2 * kSlack : kSlack);
-      if (out) {
+      int rank = 0;  // (lanes without a group have the smallest keys)
 #pragma unroll
-        for (int i = 0; i < KP; ++i) list[i] = 0u;
-      }
+      for (int o = 0; o < (L >> level()); ++o)
+        rank += static_cast<uint32_t>(__shfl(static_cast<int>(mine), (lane & ~(L - 1)) + (o << level()))) > mine;
+      const bool out = rank >= p.topk_groups;
+      const auto least = [](uint32_t u, uint32_t w) { return u < w ? u : w; };
+      const uint32_t in = row_reduce<LEVELS>(out ? 0xFFFFFFFFu : sum, least);
+      const uint32_t over = row_reduce<LEVELS>(out ? sum : 0u, [](uint32_t u, uint32_t w) { return larger(u, w); });
+      close |= over != 0u && static_cast<int>(in - over) <= (p.group_top > 1 ? 2 * kSlack : kSlack);
+      dropped = out ? 0u : dropped;
+#pragma unroll
+      for (int i = 0; i < KP; ++i) list[i] = out ? 0u : list[i];
     };
 #define DS_LEVEL(n)                                        \
   if constexpr (LEVELS > n) {                              \
-    if (limited && p.lanes_log2 == n) rank_groups();       \
-    merge_partner<n, KP>(list);                            \
+    if (limited && p.lanes_log2 == n) rank_groups(std::integral_constant<int, n>()); \
+    merge_partner<n, KP>(list, dropped);                   \
   }
     DS_LEVEL(0) DS_LEVEL(1) DS_LEVEL(2) DS_LEVEL(3) DS_LEVEL(4)
 #undef DS_LEVEL
-    // the first expert left out
-    uint32_t last = 0u;
+    // Neighbours of the list (the last one's is the best key left out) too close to be told
+    // apart. A list may go on past k: its later neighbours only send a row to the exact choice
+    // for nothing.
+    if constexpr (!kExactKeys) {
+      constexpr uint32_t kNear = static_cast<uint32_t>(kSlack + 1) << IB;  // a gap of at most kSlack steps is below
+      uint32_t gap = list[KP - 1] - dropped;
 #pragma unroll
-    for (int i = 0; i < KP; ++i) last = i == p.k - 1 ? list[i] : last;
-    uint32_t next = 0u;
+      for (int i = 0; i + 1 < KP; ++i) gap = list[i] - list[i + 1] < gap ? list[i] - list[i + 1] : gap;
+      if (__any(gap < kNear)) {  // (or there is nothing at these places)
+        close |= (list[KP - 1] - dropped < kNear) & (dropped >= kFirst);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const uint32_t q = key[v] < last ? key[v] : 0u;
-      next = next > q ? next : q;
+        for (int i = 0; i + 1 < KP; ++i) close |= (list[i] - list[i + 1] < kNear) & (list[i + 1] >= kFirst);
+      }
     }
-    next = row_reduce<LEVELS>(out ? 0u : next, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
-    close |= next >= kFirst && static_cast<int>((last >> IB) - (next >> IB)) <= kSlack;
-#pragma unroll
-    for (int i = 0; i + 1 < KP; ++i)
-      close |= i + 1 < p.k && list[i + 1] >= kFirst &&
-               static_cast<int>((list[i] >> IB) - (list[i + 1] >> IB)) <= kSlack;
     close = row_reduce<LEVELS>(close ? 1u : 0u, [](uint32_t a, uint32_t b) { return a | b; }) != 0u;
     // slot j in lane j % L: the weights
     constexpr int kSlots = KP > L ? KP / L : 1;
@@ -362,9 +541,21 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteParams p) 
     float total = 0.0f;
 #pragma unroll
     for (int t = 0; t < kSlots; ++t) {
-      uint32_t mine = 0u;
+      uint32_t mine;
+      if constexpr (KP >= L) {  // slots t L to t L + L - 1, by the bits of the lane
+        uint32_t of[L];
 #pragma unroll
-      for (int i = t * L; i < KP && i < (t + 1) * L; ++i) mine = i == t * L + sub ? list[i] : mine;
+        for (int i = 0; i < L; ++i) of[i] = list[t * L + i];
+#pragma unroll
+        for (int b = L / 2; b >= 1; b /= 2)
+#pragma unroll
+          for (int i = 0; i < b; ++i) of[i] = (sub & b) ? of[i + b] : of[i];
+        mine = of[0];
+      } else {
+        mine = 0u;
+#pragma unroll
+        for (int i = 0; i < KP; ++i) mine = i == sub ? list[i] : mine;
+      }
       const uint32_t pos = static_cast<uint32_t>(L * V - 1) - (mine & (kFirst - 1u));
       const int owner = static_cast<int>(pos / V);
       at[t] = mine >= kFirst && t * L + sub < p.k
@@ -393,12 +584,19 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteParams p) 
         if (p.counts && at[t] >= 0) atomicAdd(p.counts + at[t], 1);
       }
     }
-    uint64_t rest = __ballot(mine && close && sub == 0);
-    while (rest) {
-      const int l = __builtin_ctzll(rest);
-      rest &= rest - 1;
-      route_row_exact<DT, SCORE>(p, r0 + l / L, room[wave]);
+    const uint64_t rest = __ballot(mine && close && sub == 0);
+    if (lane == turn) left = rest;
+  }
+  if (__any(left != 0)) {
+    for (int t = 0; t < turn; ++t) {
+      uint64_t rest = __shfl(left, t);
+      while (rest) {
+        const int l = __builtin_ctzll(rest);
+        rest &= rest - 1;
+        route_row_exact<DT, SCORE, L * V / 64>(params_of_launch(), turn0 + t * row_step + l / L, room[wave]);
+      }
     }
+  }
   }
 }
 
@@ -466,14 +664,14 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_grad_kernel(RouteGradP
   }
 }
 
-uint32_t route_grid(int64_t rows, int64_t rows_per_group) {
-  const int64_t need = (rows + rows_per_group - 1) / rows_per_group, most = kCus * 8;
+uint32_t route_grid(int64_t rows, int64_t rows_per_group, int64_t per_cu) {
+  const int64_t need = (rows + rows_per_group - 1) / rows_per_group, most = kCus * per_cu;
   return static_cast<uint32_t>(need < most ? need : most);
 }
 
 template <int DT, int SCORE, int MODE, int L, int V>
 hipError_t route_shape(const RouteParams& p, hipStream_t s) {
-  const dim3 g(route_grid(p.rows, kRouteWaves * (64 / L))), b(kRouteWaves * 64);
+  const dim3 g(route_grid(p.rows, kRouteWaves * (64 / L), 4)), b(kRouteWaves * 64);
   if (p.k <= 8) hipLaunchKernelGGL((route_kernel<DT, SCORE, MODE, L, V, 8>), g, b, 0, s, p);
   else hipLaunchKernelGGL((route_kernel<DT, SCORE, MODE, L, V, 16>), g, b, 0, s, p);
   return hipGetLastError();
@@ -504,7 +702,7 @@ hipError_t route_mode(RouteParams p, hipStream_t s) {
     }
     return route_shape<DT, SCORE, MODE, 32, 32>(p, s);
   }
-  hipLaunchKernelGGL((route_exact_kernel<DT, SCORE>), dim3(route_grid(p.rows, kRouteWaves)), dim3(kRouteWaves * 64), 0, s, p);
+  hipLaunchKernelGGL((route_exact_kernel<DT, SCORE>), dim3(route_grid(p.rows, kRouteWaves, 4)), dim3(kRouteWaves * 64), 0, s, p);
   return hipGetLastError();
 }
 
@@ -518,7 +716,7 @@ hipError_t route_dt(int score, const RouteParams& p, hipStream_t s) {
 
 #define DS_ROUTE_V(KERN, DT, SCORE)                                                                              \
   do {                                                                                                           \
-    const dim3 g(route_grid(p.rows, kRouteWaves)), b(kRouteWaves * 64);                                          \
+    const dim3 g(route_grid(p.rows, kRouteWaves, 16)), b(kRouteWaves * 64);                                          \
     if (p.experts <= 64) hipLaunchKernelGGL((KERN<DT, SCORE, 1>), g, b, 0, s, p);                                \
     else if (p.experts <= 128) hipLaunchKernelGGL((KERN<DT, SCORE, 2>), g, b, 0, s, p);                          \
     else if (p.experts <= 256) hipLaunchKernelGGL((KERN<DT, SCORE, 4>), g, b, 0, s, p);                          \

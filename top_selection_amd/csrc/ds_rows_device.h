@@ -41,6 +41,13 @@ __device__ __forceinline__ float wave_max(float v) {
   return v;
 }
 
+// Orders a wave's LDS accesses: what its lanes wrote before is what they read after.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 template <class T>
 __device__ __forceinline__ T wave_sum(T v) {
 #pragma unroll
