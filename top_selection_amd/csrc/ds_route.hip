@@ -11,50 +11,6 @@ constexpr float kNegInf = -__builtin_huge_valf();
 constexpr double kNone = -__builtin_huge_val();  // the selection score of a masked or taken expert
 constexpr float kLog2E = 1.44269504088896341f;
 
-// The value of a lane of the other half of 2^(LEVEL + 1) lanes, where the lanes of a half hold
-// equal values (a butterfly's do after LEVEL levels): by data-parallel moves, no LDS.
-template <int LEVEL>
-__device__ __forceinline__ uint32_t from_partner(uint32_t v) {
-  if constexpr (LEVEL == 0) return __builtin_amdgcn_update_dpp(0u, v, 0xB1, 0xF, 0xF, false);   // xor 1
-  if constexpr (LEVEL == 1) return __builtin_amdgcn_update_dpp(0u, v, 0x4E, 0xF, 0xF, false);   // xor 2
-  if constexpr (LEVEL == 2) return __builtin_amdgcn_update_dpp(0u, v, 0x141, 0xF, 0xF, false);  // 8 lanes reversed
-  if constexpr (LEVEL == 3) return __builtin_amdgcn_update_dpp(0u, v, 0x140, 0xF, 0xF, false);  // 16 lanes reversed
-  if constexpr (LEVEL == 4) {
-    const auto q = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    return (threadIdx.x & 16u) ? q[0] : q[1];
-  }
-  if constexpr (LEVEL == 5) {
-    const auto q = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    return (threadIdx.x & 32u) ? q[0] : q[1];
-  }
-}
-template <int LEVEL>
-__device__ __forceinline__ int from_partner(int v) {
-  return static_cast<int>(from_partner<LEVEL>(static_cast<uint32_t>(v)));
-}
-template <int LEVEL>
-__device__ __forceinline__ float from_partner(float v) {
-  return __uint_as_float(from_partner<LEVEL>(__float_as_uint(v)));
-}
-template <int LEVEL>
-__device__ __forceinline__ double from_partner(double v) {
-  return __hiloint2double(from_partner<LEVEL>(__double2hiint(v)), from_partner<LEVEL>(__double2loint(v)));
-}
-
-// f over 2^LEVELS neighbouring lanes, in all of them.
-template <int LEVELS, class T, class F>
-__device__ __forceinline__ T row_reduce(T v, F f) {
-  if constexpr (LEVELS > 0) v = f(v, from_partner<0>(v));
-  if constexpr (LEVELS > 1) v = f(v, from_partner<1>(v));
-  if constexpr (LEVELS > 2) v = f(v, from_partner<2>(v));
-  if constexpr (LEVELS > 3) v = f(v, from_partner<3>(v));
-  if constexpr (LEVELS > 4) v = f(v, from_partner<4>(v));
-  if constexpr (LEVELS > 5) v = f(v, from_partner<5>(v));
-  return v;
-}
-
-template <class T>
-__device__ __forceinline__ T plus(T a, T b) { return a + b; }
 __device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
 

@@ -90,17 +90,18 @@ struct VerifyParams {
   int64_t n;
   int32_t* out_tokens;
   int32_t* out_accepted;
-  int64_t slice;
+  int64_t slice;   // units per workgroup
   int32_t slices;
   int64_t unit0;
-  double* part;  // [batch][slices][2]: sums of the residual and of the target row
+  double* part;    // [batch][units]: the units' sums (ds_verify.hip)
+  int2* verdicts;  // [batch], after them; set by the launcher
 };
 
 hipError_t launch_route(int dtype, int score, const RouteParams& p, hipStream_t s);
 hipError_t launch_route_grad(int dtype, int score, const RouteGradParams& p, hipStream_t s);
 hipError_t launch_softmax(int dtype, int out_dtype, const SoftmaxParams& p, hipStream_t s);
 hipError_t launch_list_softmax(int dtype, int out_dtype, const ListSoftmaxParams& p, hipStream_t s);
-hipError_t launch_verify(int dtype, const VerifyParams& p, hipStream_t s);
+hipError_t launch_verify(int dtype, VerifyParams p, hipStream_t s);
 
 // The compute units that a launch is sized for (MI355X).
 constexpr int64_t kCus = 256;
@@ -115,6 +116,14 @@ struct RowCut {
 };
 RowCut cut_softmax(int64_t rows, int64_t n);
 RowCut cut_list_softmax(int64_t rows, int64_t n);
-RowCut cut_verify(int64_t batch, int64_t n);
+
+// How sequences are cut for the verification: `slices` workgroups of `slice` units each, and
+// the workspace for the units' sums (slices == 0: one workgroup per sequence and no workspace).
+struct VerifyCut {
+  int64_t slice;
+  int32_t slices;
+  size_t bytes;
+};
+VerifyCut cut_verify(int64_t batch, int64_t n, int dtype);
 
 }  // namespace ds

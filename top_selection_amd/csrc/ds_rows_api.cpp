@@ -45,9 +45,6 @@ int check_workspace(const void* ws, size_t have, size_t need) {
 }
 
 size_t softmax_bytes(int64_t rows, const ds::RowCut& c) { return static_cast<size_t>(rows) * c.slices * sizeof(float2); }
-size_t verify_bytes(int64_t batch, const ds::RowCut& c) {
-  return static_cast<size_t>(batch) * c.slices * 2 * sizeof(double);
-}
 
 }  // namespace
 
@@ -174,7 +171,7 @@ int ds_topk_softmax(const void* vals, const int32_t* idx, int64_t rows, int k, i
 
 int ds_verify_workspace_size(int64_t batch, int64_t n, int dtype, size_t* bytes) {
   if (!bytes || !known(dtype) || !rows_ok(batch, n, n)) return DS_ERR_INVALID_ARG;
-  *bytes = verify_bytes(batch, ds::cut_verify(batch, n));
+  *bytes = ds::cut_verify(batch, n, dtype).bytes;
   return DS_OK;
 }
 
@@ -194,8 +191,8 @@ int ds_verify(const void* target, int64_t target_stride, const void* draft, int6
   if (misaligned(target, eb) || misaligned(draft, eb) || misaligned(draft_tokens, 4) || misaligned(draft_lens, 4) ||
       misaligned(accept_u, 4) || misaligned(sample_u, 4) || misaligned(out_tokens, 4) || misaligned(out_accepted, 4))
     return DS_ERR_ALIGNMENT;
-  const ds::RowCut c = ds::cut_verify(batch, n);
-  const int st = check_workspace(workspace, ws_bytes, verify_bytes(batch, c));
+  const ds::VerifyCut c = ds::cut_verify(batch, n, dtype);
+  const int st = check_workspace(workspace, ws_bytes, c.bytes);
   if (st != DS_OK) return st;
   (void)hipGetLastError();
   ds::VerifyParams p{};

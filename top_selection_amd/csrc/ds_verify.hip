@@ -4,36 +4,48 @@
 namespace ds {
 namespace {
 
-constexpr int kVerifyWaves = 8;
+constexpr int kVerifyWaves = 16;
 constexpr int kVerifyThreads = kVerifyWaves * 64;
+constexpr int kVerifyLoads = 4;  // 16-byte loads of each row that a lane has in flight
 
-// What the acceptance tests of sequence b decide; the same in every lane. `refused` is the
-// position of the next token: its target row, and its draft row when it is below `len`.
+// Rows are summed in units of consecutive elements, one wave per unit; the drawn token is
+// found from the units' sums and by reading one unit again.
+template <int DT>
+constexpr int kVerifyUnit = 64 * Elem<DT>::kPer16 * kVerifyLoads;  // 1024 fp32 or 2048 bf16 elements
+constexpr int kVerifyLdsUnits = 2048;  // units of a row that one workgroup draws from alone
+
+// What the acceptance tests of a sequence decide; the same in every lane.
 struct Verdict {
-  int len;      // drafts of the sequence
-  int next;     // accepted drafts, and the row the next token is drawn from
+  int len;        // drafts of the sequence
+  int next;       // accepted drafts, and the row the next token is drawn from
+  int32_t token;  // the draft that was refused (next < len)
 };
 
+// The drafts' tokens and numbers are asked for together with the length, and all rows' elements
+// together: two waits for memory, whatever the number of drafts.
 template <int DT>
 __device__ __forceinline__ Verdict judge(const VerifyParams& p, int64_t b, int lane) {
   using E = Elem<DT>;
   const typename E::T* target = static_cast<const typename E::T*>(p.target);
   const typename E::T* draft = static_cast<const typename E::T*>(p.draft);
+  const int j = lane < p.drafts ? lane : 0;
   int len = p.lens ? p.lens[b] : p.drafts;
+  const int32_t t = p.drafts ? p.tokens[b * p.drafts + j] : 0;
+  const float u = p.drafts ? p.accept_u[b * p.drafts + j] : 0.0f;
   len = len < 0 ? 0 : (len > p.drafts ? p.drafts : len);
   bool fails = false;
   if (lane < len) {
-    const int32_t t = p.tokens[b * p.drafts + lane];
     fails = true;
     if (t >= 0 && t < p.n) {
       // both factors have at most 24 significant bits: the product is exact in double
       const double pt = E::widen(target[(b * (p.drafts + 1) + lane) * p.target_stride + t]);
       const double qt = draft ? E::widen(draft[(b * p.drafts + lane) * p.draft_stride + t]) : 1.0f;
-      fails = !(static_cast<double>(p.accept_u[b * p.drafts + lane]) * qt < pt);
+      fails = !(static_cast<double>(u) * qt < pt);
     }
   }
   const uint64_t bad = __ballot(fails);
-  return {len, bad ? __builtin_ctzll(bad) : len};
+  const int next = bad ? __builtin_ctzll(bad) : len;
+  return {len, next, __shfl(t, next & 63)};
 }
 
 // The rows the next token is drawn from: element i has mass max(p - q, 0).
@@ -41,6 +53,8 @@ template <int DT>
 struct Rows {
   using E = Elem<DT>;
   using T = typename E::T;
+  static constexpr int N = E::kPer16;
+  using V = Vec<DT, N>;
   const T* p;
   const T* q;       // NULL: no draft row
   int64_t without;  // an element without mass (a refused certain draft), or -1
@@ -49,158 +63,253 @@ struct Rows {
     p = static_cast<const T*>(v.target) + (b * (v.drafts + 1) + d.next) * v.target_stride;
     const bool refused = d.next < d.len;
     q = refused && v.draft ? static_cast<const T*>(v.draft) + (b * v.drafts + d.next) * v.draft_stride : nullptr;
-    without = refused && !v.draft ? v.tokens[b * v.drafts + d.next] : -1;
+    without = refused && !v.draft ? d.token : -1;
   }
-  __device__ __forceinline__ double mass(int64_t i, float pv, float qv) const {
-    const double m = static_cast<double>(pv) - static_cast<double>(qv);
-    return i == without || !(m > 0.0) ? 0.0 : m;
+
+  // The masses of the lane's elements of a unit, in vectors `step` elements apart from the
+  // lane's first, unit + lane * first on. Elements past n have none. The difference of two fp32 is
+  // taken in double: it is the sums' terms that must not be rounded to fp32.
+  template <int kFirst, int kStep>
+  __device__ __forceinline__ void masses(int64_t unit, int64_t n, int lane, double (&m)[kVerifyLoads][N]) const {
+    typename V::type pv[kVerifyLoads], qv[kVerifyLoads];
+    const int64_t at = unit + lane * kFirst;
+    if (unit + kVerifyUnit<DT> <= n) {
+#pragma unroll
+      for (int u = 0; u < kVerifyLoads; ++u)
+        pv[u] = *reinterpret_cast<const typename V::unaligned*>(p + at + u * kStep);
+      if (q) {
+#pragma unroll
+        for (int u = 0; u < kVerifyLoads; ++u)
+          qv[u] = *reinterpret_cast<const typename V::unaligned*>(q + at + u * kStep);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < kVerifyLoads; ++u)
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const int64_t i = at + u * kStep + j;
+          pv[u][j] = i < n ? p[i] : T(0);
+          if (q) qv[u][j] = i < n ? q[i] : T(0);
+        }
+    }
+    const int64_t gone = without - at;  // where the lane would hold the element without mass
+    const int skip = gone >= 0 && gone < kVerifyUnit<DT> ? static_cast<int>(gone) : -1;
+#pragma unroll
+    for (int u = 0; u < kVerifyLoads; ++u)
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        double d = static_cast<double>(E::widen(pv[u][j]));
+        if (q) {
+          d -= static_cast<double>(E::widen(qv[u][j]));
+          d = fmax(d, 0.0);
+        } else if (without >= 0) {
+          d = skip == u * kStep + j ? 0.0 : d;
+        }
+        m[u][j] = d;
+      }
   }
-  __device__ __forceinline__ double mass_at(int64_t i) const {
-    return mass(i, E::widen(p[i]), q ? E::widen(q[i]) : 0.0f);
+
+  __device__ __forceinline__ double sum(int64_t unit, int64_t n, int lane) const {
+    double m[kVerifyLoads][N], t = 0.0;
+    masses<N, 64 * N>(unit, n, lane, m);  // in memory's order
+#pragma unroll
+    for (int u = 0; u < kVerifyLoads; ++u)
+#pragma unroll
+      for (int j = 0; j < N; ++j) t += m[u][j];
+    return wave_sum(t);
   }
 };
 
-template <class T>
-__device__ __forceinline__ T block_total(T v, T* of_wave) {
-  v = wave_sum(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) of_wave[threadIdx.x >> 6] = v;
-  __syncthreads();
-  T t = 0;
-  for (int w = 0; w < kVerifyWaves; ++w) t += of_wave[w];
-  return t;
+// v moved by a data-parallel pattern; lanes that it does not reach, or that the row mask leaves
+// out, get 0.
+template <int PATTERN, int ROWS>
+__device__ __forceinline__ double moved(double v) {
+  return __hiloint2double(
+      __builtin_amdgcn_update_dpp(0, __double2hiint(v), PATTERN, ROWS, 0xF, true),
+      __builtin_amdgcn_update_dpp(0, __double2loint(v), PATTERN, ROWS, 0xF, true));
 }
 
-// One workgroup per (sequence, slice): the slice's residual mass and the target's own.
+// The sum up to and with each lane: shifts within the rows of 16 lanes, then each row's last
+// sum to the next row, and the second row's to the upper half.
+__device__ __forceinline__ double scan_lanes(double v) {
+  v += moved<0x111, 0xF>(v);  // by 1
+  v += moved<0x112, 0xF>(v);  // by 2
+  v += moved<0x114, 0xF>(v);  // by 4
+  v += moved<0x118, 0xF>(v);  // by 8
+  v += moved<0x142, 0xA>(v);  // lane 15 of rows 0 and 2 to rows 1 and 3
+  v += moved<0x143, 0xC>(v);  // lane 31 to rows 2 and 3
+  return v;
+}
+
+__device__ __forceinline__ double of_lane(double v, int lane) {  // lane: the same everywhere
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), lane),
+                          __builtin_amdgcn_readlane(__double2loint(v), lane));
+}
+
+// One wave: the element that the point share * total falls on. sums: the units' masses, total
+// their (positive) sum.
 template <int DT>
-__global__ __launch_bounds__(kVerifyThreads) void verify_sums_kernel(VerifyParams p) {
-  using E = Elem<DT>;
-  constexpr int N = E::kPer16;
-  using V = Vec<DT, N>;
-  __shared__ double of_wave[kVerifyWaves];
-  const int64_t unit = p.unit0 + blockIdx.x;
-  const int64_t b = unit / p.slices;
-  const int sl = static_cast<int>(unit - b * p.slices);
-  const Verdict d = judge<DT>(p, b, threadIdx.x & 63);
-  const Rows<DT> rows(p, b, d);
-  const int64_t lo = sl * p.slice, hi = lo + p.slice < p.n ? lo + p.slice : p.n;
-  double rest = 0.0, whole = 0.0;
-  for (int64_t i = lo + static_cast<int64_t>(threadIdx.x) * N; i < hi; i += kVerifyThreads * N) {
-    if (i + N <= hi) {
-      const typename V::type pv = *reinterpret_cast<const typename V::unaligned*>(rows.p + i);
-      typename V::type qv = typename V::type(0);
-      if (rows.q) qv = *reinterpret_cast<const typename V::unaligned*>(rows.q + i);
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        rest += rows.mass(i + j, E::widen(pv[j]), E::widen(qv[j]));
-        whole += static_cast<double>(E::widen(pv[j]));
-      }
-    } else {
-      for (int64_t j = i; j < hi; ++j) rest += rows.mass_at(j), whole += static_cast<double>(E::widen(rows.p[j]));
+__device__ __forceinline__ int32_t draw(const Rows<DT>& rows, const double* sums, int units, int64_t n, double total,
+                                        double share, int lane) {
+  constexpr int N = Elem<DT>::kPer16, kRun = kVerifyLoads * N;
+  const double point = share * total;
+  // the first unit whose end passes the point; by rounding none may: the last one with mass
+  int unit = -1;
+  double before = 0.0, start = 0.0;
+  for (int c = 0; c < units; c += 64) {
+    const double s = c + lane < units ? sums[c + lane] : 0.0;
+    const double end = start + scan_lanes(s);
+    const uint64_t some = __ballot(s > 0.0), past = some & __ballot(end > point);
+    if (some) {
+      const int l = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(some);
+      unit = c + l;
+      before = of_lane(end, l) - of_lane(s, l);
     }
+    if (past) break;
+    start = of_lane(end, 63);
   }
-  rest = block_total(rest, of_wave);
-  whole = block_total(whole, of_wave);
-  if (threadIdx.x == 0) {
-    p.part[2 * unit] = rest;
-    p.part[2 * unit + 1] = whole;
-  }
+  // within the unit each lane takes a run of elements
+  double m[kVerifyLoads][N];
+  const int64_t first = static_cast<int64_t>(unit) * kVerifyUnit<DT>;
+  rows.template masses<kRun, N>(first, n, lane, m);
+  double s = 0.0;
+#pragma unroll
+  for (int u = 0; u < kVerifyLoads; ++u)
+#pragma unroll
+    for (int j = 0; j < N; ++j) s += m[u][j];
+  double sum = before + (scan_lanes(s) - s);
+  int hit = -1, with = -1;
+#pragma unroll
+  for (int u = 0; u < kVerifyLoads; ++u)
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      sum += m[u][j];
+      const bool some = m[u][j] > 0.0;
+      with = some ? u * N + j : with;
+      hit = some && hit < 0 && sum > point ? u * N + j : hit;
+    }
+  const uint64_t hits = __ballot(hit >= 0), withs = __ballot(with >= 0);
+  const int l = hits ? __builtin_ctzll(hits) : 63 - __builtin_clzll(withs | 1);
+  return static_cast<int32_t>(first + l * kRun + __builtin_amdgcn_readlane(hits ? hit : with, l));
 }
 
-// One workgroup per sequence: finds the slice in which the running sum passes the drawn
-// point, then the element in it.
+// The sum of the units' masses, in every lane of every wave.
+__device__ __forceinline__ double sum_units(const double* sums, int units, int lane) {
+  double t = 0.0;
+  for (int i = lane; i < units; i += 64) t += sums[i];
+  return wave_sum(t);
+}
+
+__device__ __forceinline__ void answer(const VerifyParams& p, int64_t b, Verdict d, int32_t token, int lane) {
+  for (int j = lane; j <= p.drafts; j += 64)
+    p.out_tokens[b * (p.drafts + 1) + j] = j < d.next ? p.tokens[b * p.drafts + j] : (j == d.next ? token : -1);
+  if (lane == 0) p.out_accepted[b] = d.next;
+}
+
+// A workgroup sums all units of a sequence and draws; a residual without mass is given up for
+// the target's row, and a row without mass gives -1.
 template <int DT>
-__global__ __launch_bounds__(kVerifyThreads) void verify_pick_kernel(VerifyParams p) {
-  __shared__ double of_wave[kVerifyWaves];
-  __shared__ int64_t found[kVerifyWaves], last[kVerifyWaves];
-  const int64_t b = p.unit0 + blockIdx.x;
+__device__ __forceinline__ void draw_alone(const VerifyParams& p, int64_t b, Verdict d, Rows<DT> rows, double* sums) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const Verdict d = judge<DT>(p, b, lane);
-  Rows<DT> rows(p, b, d);
-  const double* part = p.part + 2 * b * p.slices;
+  const int units = static_cast<int>((p.n + kVerifyUnit<DT> - 1) / kVerifyUnit<DT>);
   double total = 0.0;
-  int which = 0;
-  for (int i = 0; i < p.slices; ++i) total += part[2 * i];
-  if (!(total > 0.0)) {  // no residual: draw from the target's row itself
-    which = 1;
+  for (int turn = 0; turn < 2; ++turn) {
+    for (int i = wave; i < units; i += kVerifyWaves) {
+      const double s = rows.sum(static_cast<int64_t>(i) * kVerifyUnit<DT>, p.n, lane);
+      if (lane == 0) sums[i] = s;
+    }
+    __syncthreads();
+    total = sum_units(sums, units, lane);
+    if (total > 0.0) break;  // (the same in every wave)
+    __syncthreads();
     rows.q = nullptr;
     rows.without = -1;
-    total = 0.0;
-    for (int i = 0; i < p.slices; ++i) total += part[2 * i + 1];
   }
-  int64_t token = -1;
-  if (total > 0.0) {
-    const double point = static_cast<double>(p.sample_u[b]) * total;
-    double before = 0.0;
-    int sl = -1, at = 0;
-    for (; at < p.slices; ++at) {  // the first slice whose end passes the point
-      const double m = part[2 * at + which];
-      if (m > 0.0) sl = at;
-      if (before + m > point) break;
-      before += m;
-    }
-    if (at == p.slices) before -= part[2 * sl + which];  // rounding: the last slice with mass
-    const int64_t lo = sl * p.slice, hi = lo + p.slice < p.n ? lo + p.slice : p.n;
-    const int64_t per = (hi - lo + kVerifyThreads - 1) / kVerifyThreads;
-    const int64_t my_lo = lo + threadIdx.x * per < hi ? lo + threadIdx.x * per : hi;
-    const int64_t my_hi = my_lo + per < hi ? my_lo + per : hi;
-    double mine = 0.0;
-    int64_t my_last = -1, my_found = INT64_MAX;
-    for (int64_t i = my_lo; i < my_hi; ++i) {
-      const double m = rows.mass_at(i);
-      mine += m;
-      if (m > 0.0) my_last = i;
-    }
-    double sum = mine;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const double other = __shfl_up(sum, o);
-      if (lane >= o) sum += other;
-    }
-    if (lane == 63) of_wave[wave] = sum;
-    __syncthreads();
-    sum -= mine;
-    for (int w = 0; w < wave; ++w) sum += of_wave[w];
-    sum += before;
-    for (int64_t i = my_lo; i < my_hi; ++i) {
-      const double m = rows.mass_at(i);
-      sum += m;
-      if (m > 0.0 && sum > point) {
-        my_found = i;
-        break;
-      }
-    }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-      const int64_t f = __shfl_xor(my_found, o), l = __shfl_xor(my_last, o);
-      my_found = f < my_found ? f : my_found;
-      my_last = l > my_last ? l : my_last;
-    }
-    if (lane == 0) found[wave] = my_found, last[wave] = my_last;
-    __syncthreads();
-    for (int w = 0; w < kVerifyWaves; ++w) {
-      my_found = found[w] < my_found ? found[w] : my_found;
-      my_last = last[w] > my_last ? last[w] : my_last;
-    }
-    token = my_found != INT64_MAX ? my_found : my_last;
+  if (wave == 0) {
+    const int32_t token = total > 0.0 ? draw(rows, sums, units, p.n, total, static_cast<double>(p.sample_u[b]), lane) : -1;
+    answer(p, b, d, token, lane);
   }
-  for (int j = threadIdx.x; j <= p.drafts; j += kVerifyThreads)
-    p.out_tokens[b * (p.drafts + 1) + j] =
-        j < d.next ? p.tokens[b * p.drafts + j] : (j == d.next ? static_cast<int32_t>(token) : -1);
-  if (threadIdx.x == 0) p.out_accepted[b] = d.next;
+}
+
+// One workgroup per sequence.
+template <int DT>
+__global__ __launch_bounds__(kVerifyThreads) void verify_kernel(VerifyParams p) {
+  __shared__ double sums[kVerifyLdsUnits];
+  const int64_t b = p.unit0 + blockIdx.x;
+  const Verdict d = judge<DT>(p, b, threadIdx.x & 63);
+  draw_alone<DT>(p, b, d, Rows<DT>(p, b, d), sums);
+}
+
+// Few sequences: one workgroup per (sequence, slice of units) leaves the units' sums in the
+// workspace, then one workgroup per sequence draws.
+template <int DT>
+__global__ __launch_bounds__(kVerifyThreads) void verify_sums_kernel(VerifyParams p) {
+  const int64_t at = p.unit0 + blockIdx.x;
+  const int64_t b = at / p.slices;
+  const int sl = static_cast<int>(at - b * p.slices);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const Verdict d = judge<DT>(p, b, lane);
+  const Rows<DT> rows(p, b, d);
+  const int64_t units = (p.n + kVerifyUnit<DT> - 1) / kVerifyUnit<DT>;
+  const int64_t lo = sl * p.slice, hi = lo + p.slice < units ? lo + p.slice : units;
+  if (sl == 0 && threadIdx.x == 0) p.verdicts[b] = make_int2(d.len | d.next << 16, d.token);
+  for (int64_t i = lo + wave; i < hi; i += kVerifyWaves) {
+    const double s = rows.sum(i * kVerifyUnit<DT>, p.n, lane);
+    if (lane == 0) p.part[b * units + i] = s;
+  }
+}
+
+template <int DT>
+__global__ __launch_bounds__(kVerifyThreads) void verify_draw_kernel(VerifyParams p) {
+  __shared__ double near[kVerifyLdsUnits];
+  const int64_t b = p.unit0 + blockIdx.x;
+  const int lane = threadIdx.x & 63;
+  const int units = static_cast<int>((p.n + kVerifyUnit<DT> - 1) / kVerifyUnit<DT>);
+  double* const sums = p.part + b * units;
+  const int2 v = p.verdicts[b];
+  const Verdict d = {v.x & 0xFFFF, v.x >> 16, v.y};
+  const Rows<DT> rows(p, b, d);
+  const bool fits = units <= kVerifyLdsUnits;
+  if (fits) {
+    for (int i = threadIdx.x; i < units; i += kVerifyThreads) near[i] = sums[i];
+    __syncthreads();
+  }
+  const double total = fits ? sum_units(near, units, lane) : sum_units(sums, units, lane);
+  if (!(total > 0.0)) {  // (the same in every wave)
+    __syncthreads();
+    draw_alone<DT>(p, b, d, rows, sums);
+  } else if (threadIdx.x < 64) {
+    const double share = static_cast<double>(p.sample_u[b]);
+    answer(p, b, d, fits ? draw(rows, near, units, p.n, total, share, lane)
+                         : draw(rows, sums, units, p.n, total, share, lane), lane);
+  }
 }
 
 template <int DT>
 hipError_t verify_dt(const VerifyParams& p, hipStream_t s) {
+  if (p.slices == 0) return launch_units(verify_kernel<DT>, p, p.batch, kVerifyThreads, s);
   const hipError_t e = launch_units(verify_sums_kernel<DT>, p, p.batch * p.slices, kVerifyThreads, s);
-  return e != hipSuccess ? e : launch_units(verify_pick_kernel<DT>, p, p.batch, kVerifyThreads, s);
+  return e != hipSuccess ? e : launch_units(verify_draw_kernel<DT>, p, p.batch, kVerifyThreads, s);
 }
 
 }  // namespace
 
-RowCut cut_verify(int64_t batch, int64_t n) { return cut_softmax(batch, n); }
+// No slices (one workgroup per sequence, one launch) while a row is short or the sequences fill
+// the card by themselves; else slices of whole units.
+VerifyCut cut_verify(int64_t batch, int64_t n, int dtype) {
+  const int64_t unit = dtype == DS_BF16 ? kVerifyUnit<DS_BF16> : kVerifyUnit<DS_FP32>;
+  const int64_t units = (n + unit - 1) / unit;
+  if (units <= 32 || (batch >= 64 && units <= kVerifyLdsUnits)) return {0, 0, 0};
+  const int64_t want = batch >= kCus ? 1 : (kCus + batch - 1) / (batch < 1 ? 1 : batch);
+  int64_t slice = (units + want - 1) / want;
+  slice = (slice + kVerifyWaves - 1) / kVerifyWaves * kVerifyWaves;
+  return {slice, static_cast<int32_t>((units + slice - 1) / slice),
+          static_cast<size_t>(batch) * (units * sizeof(double) + sizeof(int2))};
+}
 
-hipError_t launch_verify(int dtype, const VerifyParams& p, hipStream_t s) {
+hipError_t launch_verify(int dtype, VerifyParams p, hipStream_t s) {
+  const int64_t unit = dtype == DS_BF16 ? kVerifyUnit<DS_BF16> : kVerifyUnit<DS_FP32>;
+  if (p.slices) p.verdicts = reinterpret_cast<int2*>(p.part + p.batch * ((p.n + unit - 1) / unit));
   return dtype == DS_BF16 ? verify_dt<DS_BF16>(p, s) : verify_dt<DS_FP32>(p, s);
 }
 
