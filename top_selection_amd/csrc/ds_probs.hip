@@ -145,6 +145,178 @@ __global__ __launch_bounds__(kSoftWaves * 64) void softmax_write_kernel(SoftmaxP
   }
 }
 
+// One workgroup per row, which it reads from memory once where it can: each thread keeps R
+// vectors in registers and LV in LDS, and only what is past them is read again for the output.
+// Vector j of thread t holds elements (j * THREADS + t) * N on.
+template <int DT, int OT, int THREADS, int R, int LV>
+__global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
+  using E = Elem<DT>;
+  using O = Elem<OT>;
+  using T = typename E::T;
+  constexpr int N = E::kPer16, kWaves = THREADS / 64;
+  constexpr int64_t kStep = static_cast<int64_t>(THREADS) * N;
+  using V = Vec<DT, N>;
+  using W = Vec<OT, N>;
+  typedef typename V::type VT;
+  __shared__ __attribute__((aligned(16))) VT kept[LV ? LV * THREADS : 1];
+  __shared__ float of_wave[kWaves];
+  __shared__ int64_t first_of_wave[kWaves];
+  const int64_t r = p.unit0 + blockIdx.x;
+  const T* x = static_cast<const T*>(p.x) + r * p.row_stride;
+  typename O::T* out = static_cast<typename O::T*>(p.out) + r * p.out_stride;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  bool greedy;
+  const float scale = row_scale(p.temperature, r, &greedy);
+  const T none = DT == DS_BF16 ? T(0xFF80) : T(kNegInf);  // -inf past the row's end
+  const auto load = [&](int64_t i) {
+    VT v;
+    if (i + N <= p.n) {
+      v = *reinterpret_cast<const typename V::unaligned*>(x + i);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = i + j < p.n ? x[i + j] : none;
+    }
+    return v;
+  };
+  const auto most = [](float m, VT v) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) m = fmaxf(m, E::widen(v[j]));
+    return m;
+  };
+  const int64_t mine = static_cast<int64_t>(threadIdx.x) * N;
+  VT reg[R];
+#pragma unroll
+  for (int j = 0; j < R; ++j) reg[j] = load(j * kStep + mine);
+  float m = kNegInf, z = 0.0f;
+  int64_t at = R * kStep + mine;
+  if constexpr (LV > 0) {
+    VT ahead[LV];
+#pragma unroll
+    for (int j = 0; j < LV; ++j) ahead[j] = load(at + j * kStep);
+#pragma unroll
+    for (int j = 0; j < LV; ++j) {
+      kept[j * THREADS + threadIdx.x] = ahead[j];
+      m = most(m, ahead[j]);
+    }
+    at += LV * kStep;
+  }
+  // what is past the kept vectors: the running maximum and sum, four vectors at a time
+  const int64_t past = at;
+  for (; at - mine < p.n; at += 4 * kStep) {
+    VT v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = load(at + j * kStep);
+    float top = m;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = most(top, v[j]);
+    if (top != kNegInf) {
+      z *= soft_exp(m, top, scale);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < N; ++i) z += soft_exp(E::widen(v[j][i]), top, scale);
+    }
+    m = top;
+  }
+  const float own = m;
+#pragma unroll
+  for (int j = 0; j < R; ++j) m = most(m, reg[j]);
+  m = wave_max(m);
+  if (lane == 0) of_wave[wave] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) m = fmaxf(m, of_wave[w]);
+  __syncthreads();
+  const bool empty = m == kNegInf;
+  float inv = 0.0f;
+  int64_t hot = -1;  // a greedy row's element
+  if (greedy && !empty) {
+    int64_t first = p.n;
+    const auto look = [&](VT v, int64_t i) {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (E::widen(v[j]) == m && i + j < first) first = i + j;
+    };
+#pragma unroll
+    for (int j = 0; j < R; ++j) look(reg[j], j * kStep + mine);
+    if constexpr (LV > 0) {
+      for (int j = 0; j < LV; ++j) look(kept[j * THREADS + threadIdx.x], (R + j) * kStep + mine);
+    }
+    for (int64_t i = past; i < p.n && i < first; i += kStep) look(load(i), i);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+      const int64_t b = __shfl_xor(first, o);
+      first = b < first ? b : first;
+    }
+    if (lane == 0) first_of_wave[wave] = first;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) first = first_of_wave[w] < first ? first_of_wave[w] : first;
+    hot = first;
+  } else if (!empty) {
+    z *= own == kNegInf ? 0.0f : soft_exp(own, m, scale);
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float e = soft_exp(E::widen(reg[j][i]), m, scale);
+        z += e;
+        if constexpr (DT == DS_FP32) reg[j][i] = e;  // (bf16 has no room for it)
+      }
+    if constexpr (LV > 0) {
+#pragma unroll
+      for (int j = 0; j < LV; ++j) {
+        VT v = kept[j * THREADS + threadIdx.x];
+#pragma unroll
+        for (int i = 0; i < N; ++i) z += soft_exp(E::widen(v[i]), m, scale);
+      }
+    }
+    z = wave_sum(z);
+    if (lane == 0) of_wave[wave] = z;
+    __syncthreads();
+    z = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) z += of_wave[w];
+    inv = 1.0f / z;
+  }
+  const bool shut = greedy || empty;
+  const auto store = [&](int64_t i, const float* v) {
+    if (i + N <= p.n) {
+      typename W::type q;
+#pragma unroll
+      for (int j = 0; j < N; ++j) q[j] = O::narrow(v[j]);
+      *reinterpret_cast<typename W::unaligned*>(out + i) = q;
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (i + j < p.n) out[i + j] = O::narrow(v[j]);
+    }
+  };
+  const auto finish = [&](int64_t i, VT v, bool done) {  // done: v holds exp already
+    float q[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      q[j] = shut ? (i + j == hot ? 1.0f : 0.0f) : (done ? E::widen(v[j]) : soft_exp(E::widen(v[j]), m, scale)) * inv;
+    store(i, q);
+  };
+#pragma unroll
+  for (int j = 0; j < R; ++j)
+    if (j * kStep < p.n) finish(j * kStep + mine, reg[j], DT == DS_FP32);
+  if constexpr (LV > 0) {
+#pragma unroll
+    for (int j = 0; j < LV; ++j)
+      if ((R + j) * kStep < p.n) finish((R + j) * kStep + mine, kept[j * THREADS + threadIdx.x], false);
+  }
+  for (int64_t i = past; i - mine < p.n; i += 4 * kStep) {
+    VT v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = shut ? VT(0) : load(i + j * kStep);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j * kStep - mine < p.n) finish(i + j * kStep, v[j], false);
+  }
+}
+
 // One workgroup per (row, slice of the output): every workgroup of a row computes the list's
 // probabilities (at most 4096 entries, in double: the prefix's end is exact), clears its
 // slice and writes the entries that fall in it.
@@ -261,24 +433,39 @@ __global__ __launch_bounds__(kListThreads) void list_softmax_kernel(ListSoftmaxP
 
 }  // namespace
 
-RowCut cut_softmax(int64_t rows, int64_t n) {
-  constexpr int64_t step = kSoftWaves * 64 * 8;
+static RowCut cut_rows(int64_t rows, int64_t n) {
   if (rows < 1) rows = 1;
+  constexpr int64_t step = kSoftWaves * 64 * 8;
   const int64_t most = (n + step - 1) / step, want = (kCus * 4 + rows - 1) / rows;
   const int64_t slices = want < 1 ? 1 : (want > most ? most : want);
   const int64_t slice = ((n + slices - 1) / slices + step - 1) / step * step;
   return {slice, static_cast<int32_t>((n + slice - 1) / slice)};
 }
 
-RowCut cut_list_softmax(int64_t rows, int64_t n) { return cut_softmax(rows, n); }
+// No slices (one workgroup per row, one launch) while a row is short or the rows fill the card
+// by themselves; else slices and two launches.
+RowCut cut_softmax(int64_t rows, int64_t n) {
+  if (n <= 32768 || rows >= 128) return {0, 0};
+  return cut_rows(rows, n);
+}
+
+RowCut cut_list_softmax(int64_t rows, int64_t n) { return cut_rows(rows, n); }
+
+template <int DT, int OT>
+static hipError_t softmax_out(const SoftmaxParams& p, hipStream_t s) {
+  if (p.slices == 0) {
+    constexpr int64_t kSmall = 256 * 8 * Elem<DT>::kPer16;
+    if (p.n <= kSmall) return launch_units(softmax_row_kernel<DT, OT, 256, 8, 0>, p, p.rows, 256, s);
+    return launch_units(softmax_row_kernel<DT, OT, 1024, DT == DS_BF16 ? 12 : 16, DT == DS_BF16 ? 4 : 8>, p, p.rows, 1024, s);
+  }
+  const int64_t units = p.rows * p.slices;
+  const hipError_t e = launch_units(softmax_stats_kernel<DT>, p, units, kSoftWaves * 64, s);
+  return e != hipSuccess ? e : launch_units(softmax_write_kernel<DT, OT>, p, units, kSoftWaves * 64, s);
+}
 
 template <int DT>
 static hipError_t softmax_dt(int out_dtype, const SoftmaxParams& p, hipStream_t s) {
-  const int64_t units = p.rows * p.slices;
-  const hipError_t e = launch_units(softmax_stats_kernel<DT>, p, units, kSoftWaves * 64, s);
-  if (e != hipSuccess) return e;
-  return out_dtype == DS_BF16 ? launch_units(softmax_write_kernel<DT, DS_BF16>, p, units, kSoftWaves * 64, s)
-                              : launch_units(softmax_write_kernel<DT, DS_FP32>, p, units, kSoftWaves * 64, s);
+  return out_dtype == DS_BF16 ? softmax_out<DT, DS_BF16>(p, s) : softmax_out<DT, DS_FP32>(p, s);
 }
 
 hipError_t launch_softmax(int dtype, int out_dtype, const SoftmaxParams& p, hipStream_t s) {
