@@ -145,16 +145,19 @@ __global__ __launch_bounds__(kSoftWaves * 64) void softmax_write_kernel(SoftmaxP
   }
 }
 
-// One workgroup per row, which it reads from memory once where it can: each thread keeps R
-// vectors in registers and LV in LDS, and only what is past them is read again for the output.
-// Vector j of thread t holds elements (j * THREADS + t) * N on.
+// One workgroup per row of at least N elements, which it reads from memory once where it can:
+// each thread keeps R vectors in registers and LV in LDS, and only what is past them is read
+// again for the output. Vector j of thread t holds elements (j * THREADS + t) * N on; a vector
+// that would pass the row's end is moved back to end there (no branches around loads and
+// stores: what it holds twice changes no maximum, is left out of the sum, and is written
+// twice with the same value).
 template <int DT, int OT, int THREADS, int R, int LV>
 __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
   using E = Elem<DT>;
   using O = Elem<OT>;
   using T = typename E::T;
   constexpr int N = E::kPer16, kWaves = THREADS / 64;
-  constexpr int64_t kStep = static_cast<int64_t>(THREADS) * N;
+  constexpr uint32_t kStep = THREADS * N, kKept = (R + LV) * kStep;
   using V = Vec<DT, N>;
   using W = Vec<OT, N>;
   typedef typename V::type VT;
@@ -167,58 +170,69 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   bool greedy;
   const float scale = row_scale(p.temperature, r, &greedy);
-  const T none = DT == DS_BF16 ? T(0xFF80) : T(kNegInf);  // -inf past the row's end
-  const auto load = [&](int64_t i) {
-    VT v;
-    if (i + N <= p.n) {
-      v = *reinterpret_cast<const typename V::unaligned*>(x + i);
-    } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j) v[j] = i + j < p.n ? x[i + j] : none;
-    }
-    return v;
-  };
+  // the kept vectors lie within 32 bits of the row's start
+  const uint32_t n = p.n < 2 * static_cast<int64_t>(kKept) ? static_cast<uint32_t>(p.n) : 2 * kKept;
+  uint32_t mine = threadIdx.x * N;
+  const auto place = [&](uint32_t j) { return j * kStep + mine < n - N ? j * kStep + mine : n - N; };
+  const auto load = [&](auto i) { return *reinterpret_cast<const typename V::unaligned*>(x + i); };
   const auto most = [](float m, VT v) {
 #pragma unroll
     for (int j = 0; j < N; ++j) m = fmaxf(m, E::widen(v[j]));
     return m;
   };
-  const int64_t mine = static_cast<int64_t>(threadIdx.x) * N;
   VT reg[R];
-#pragma unroll
-  for (int j = 0; j < R; ++j) reg[j] = load(j * kStep + mine);
   float m = kNegInf, z = 0.0f;
-  int64_t at = R * kStep + mine;
   if constexpr (LV > 0) {
-    VT ahead[LV];
+    // LDS vectors come first, B at a time: the registers' loads are under way meanwhile
+    constexpr int B = LV % 4 == 0 ? 4 : 3;
+    static_assert(LV % B == 0);
+    VT ahead[B];
 #pragma unroll
-    for (int j = 0; j < LV; ++j) ahead[j] = load(at + j * kStep);
+    for (int j = 0; j < B; ++j) ahead[j] = load(place(R + j));
 #pragma unroll
-    for (int j = 0; j < LV; ++j) {
-      kept[j * THREADS + threadIdx.x] = ahead[j];
-      m = most(m, ahead[j]);
+    for (int j = 0; j < R; ++j) reg[j] = load(place(j));
+#pragma unroll
+    for (int b = 0; b < LV; b += B) {
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+        kept[(b + j) * THREADS + threadIdx.x] = ahead[j];
+        m = most(m, ahead[j]);
+        if (b + B < LV) ahead[j] = load(place(R + b + B + j));
+      }
     }
-    at += LV * kStep;
+  } else {
+#pragma unroll
+    for (int j = 0; j < R; ++j) reg[j] = load(place(j));
   }
   // what is past the kept vectors: the running maximum and sum, four vectors at a time
-  const int64_t past = at;
-  for (; at - mine < p.n; at += 4 * kStep) {
+  const int64_t past = kKept + static_cast<int64_t>(mine), end = p.n - N;
+  const auto place64 = [&](int64_t i) { return i < end ? i : end; };
+  const auto sum_of = [&](VT v, int64_t back, float top) {  // back: elements that another vector holds too
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float e = soft_exp(E::widen(v[i]), top, scale);
+      s += i >= back ? e : 0.0f;
+    }
+    return s;
+  };
+  for (int64_t at = past; at - mine < p.n; at += 4 * kStep) {
     VT v[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = load(at + j * kStep);
+    for (int j = 0; j < 4; ++j) v[j] = load(place64(at + j * kStep));
     float top = m;
 #pragma unroll
     for (int j = 0; j < 4; ++j) top = most(top, v[j]);
     if (top != kNegInf) {
       z *= soft_exp(m, top, scale);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < N; ++i) z += soft_exp(E::widen(v[j][i]), top, scale);
+      for (int j = 0; j < 4; ++j) z += sum_of(v[j], at + j * kStep - place64(at + j * kStep), top);
     }
     m = top;
   }
   const float own = m;
+  // (places are worked out anew in each phase: kept, they would take a register per vector)
+  asm volatile("" : "+v"(mine));
 #pragma unroll
   for (int j = 0; j < R; ++j) m = most(m, reg[j]);
   m = wave_max(m);
@@ -227,93 +241,111 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) m = fmaxf(m, of_wave[w]);
   __syncthreads();
-  const bool empty = m == kNegInf;
-  float inv = 0.0f;
-  int64_t hot = -1;  // a greedy row's element
-  if (greedy && !empty) {
-    int64_t first = p.n;
-    const auto look = [&](VT v, int64_t i) {
+  if (greedy || m == kNegInf) {  // one-hot at the first maximum, or nothing
+    int64_t hot = p.n;
+    if (m != kNegInf) {
+      const auto look = [&](VT v, int64_t a) {
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (E::widen(v[j]) == m && i + j < first) first = i + j;
-    };
+        for (int j = N - 1; j >= 0; --j) hot = E::widen(v[j]) == m && a + j < hot ? a + j : hot;
+      };
 #pragma unroll
-    for (int j = 0; j < R; ++j) look(reg[j], j * kStep + mine);
-    if constexpr (LV > 0) {
-      for (int j = 0; j < LV; ++j) look(kept[j * THREADS + threadIdx.x], (R + j) * kStep + mine);
-    }
-    for (int64_t i = past; i < p.n && i < first; i += kStep) look(load(i), i);
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-      const int64_t b = __shfl_xor(first, o);
-      first = b < first ? b : first;
-    }
-    if (lane == 0) first_of_wave[wave] = first;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) first = first_of_wave[w] < first ? first_of_wave[w] : first;
-    hot = first;
-  } else if (!empty) {
-    z *= own == kNegInf ? 0.0f : soft_exp(own, m, scale);
-#pragma unroll
-    for (int j = 0; j < R; ++j)
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float e = soft_exp(E::widen(reg[j][i]), m, scale);
-        z += e;
-        if constexpr (DT == DS_FP32) reg[j][i] = e;  // (bf16 has no room for it)
+      for (int j = 0; j < R; ++j) look(reg[j], place(j));
+      if constexpr (LV > 0) {
+        for (int j = 0; j < LV; ++j) look(kept[j * THREADS + threadIdx.x], place(R + j));
       }
-    if constexpr (LV > 0) {
+      for (int64_t i = past; i - mine < p.n && hot == p.n; i += 4 * kStep) {
+        VT v[4];
 #pragma unroll
-      for (int j = 0; j < LV; ++j) {
-        VT v = kept[j * THREADS + threadIdx.x];
+        for (int j = 0; j < 4; ++j) v[j] = load(place64(i + j * kStep));
 #pragma unroll
-        for (int i = 0; i < N; ++i) z += soft_exp(E::widen(v[i]), m, scale);
+        for (int j = 0; j < 4; ++j) look(v[j], place64(i + j * kStep));
       }
-    }
-    z = wave_sum(z);
-    if (lane == 0) of_wave[wave] = z;
-    __syncthreads();
-    z = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) z += of_wave[w];
-    inv = 1.0f / z;
+      for (int o = 32; o > 0; o >>= 1) {
+        const int64_t b = __shfl_xor(hot, o);
+        hot = b < hot ? b : hot;
+      }
+      if (lane == 0) first_of_wave[wave] = hot;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) hot = first_of_wave[w] < hot ? first_of_wave[w] : hot;
+    }
+    for (int64_t i = mine; i < p.n; i += kStep) {
+      const int64_t a = place64(i);
+      typename W::type o;
+#pragma unroll
+      for (int j = 0; j < N; ++j) o[j] = O::narrow(a + j == hot ? 1.0f : 0.0f);
+      *reinterpret_cast<typename W::unaligned*>(out + a) = o;
+    }
+    return;
   }
-  const bool shut = greedy || empty;
-  const auto store = [&](int64_t i, const float* v) {
-    if (i + N <= p.n) {
-      typename W::type q;
+  z *= own == kNegInf ? 0.0f : soft_exp(own, m, scale);
 #pragma unroll
-      for (int j = 0; j < N; ++j) q[j] = O::narrow(v[j]);
-      *reinterpret_cast<typename W::unaligned*>(out + i) = q;
+  for (int j = 0; j < R; ++j) {
+    const bool whole = (j + 1) * kStep <= n;
+    if constexpr (DT == DS_FP32) {  // the registers hold exp from here on (bf16 has no room for it)
+#pragma unroll
+      for (int i = 0; i < N; ++i) reg[j][i] = soft_exp(reg[j][i], m, scale);
+      if (whole) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) z += reg[j][i];
+      } else {
+        const uint32_t back = j * kStep + mine - place(j);
+#pragma unroll
+        for (int i = 0; i < N; ++i) z += i >= back ? reg[j][i] : 0.0f;
+      }
     } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (i + j < p.n) out[i + j] = O::narrow(v[j]);
+      z += sum_of(reg[j], whole ? 0 : j * kStep + mine - place(j), m);
     }
-  };
-  const auto finish = [&](int64_t i, VT v, bool done) {  // done: v holds exp already
-    float q[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      q[j] = shut ? (i + j == hot ? 1.0f : 0.0f) : (done ? E::widen(v[j]) : soft_exp(E::widen(v[j]), m, scale)) * inv;
-    store(i, q);
-  };
-#pragma unroll
-  for (int j = 0; j < R; ++j)
-    if (j * kStep < p.n) finish(j * kStep + mine, reg[j], DT == DS_FP32);
+    __builtin_amdgcn_sched_barrier(0);  // vector by vector: more at a time takes more registers than there are
+  }
   if constexpr (LV > 0) {
 #pragma unroll
     for (int j = 0; j < LV; ++j)
-      if ((R + j) * kStep < p.n) finish((R + j) * kStep + mine, kept[j * THREADS + threadIdx.x], false);
+      z += sum_of(kept[j * THREADS + threadIdx.x], (R + j) * kStep + mine - place(R + j), m);
   }
-  for (int64_t i = past; i - mine < p.n; i += 4 * kStep) {
+  z = wave_sum(z);
+  if (lane == 0) of_wave[wave] = z;
+  __syncthreads();
+  z = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) z += of_wave[w];
+  const float inv = 1.0f / z;
+  asm volatile("" : "+v"(mine));
+  const auto store = [&](auto i, const float* q) {
+    typename W::type o;
+#pragma unroll
+    for (int j = 0; j < N; ++j) o[j] = O::narrow(q[j]);
+    *reinterpret_cast<typename W::unaligned*>(out + i) = o;
+  };
+#pragma unroll
+  for (int j = 0; j < R; ++j)
+    if (j * kStep < n) {
+      float q[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        q[i] = (DT == DS_FP32 ? E::widen(reg[j][i]) : soft_exp(E::widen(reg[j][i]), m, scale)) * inv;
+      store(place(j), q);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  const auto finish = [&](auto i, VT v) {
+    float q[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) q[j] = soft_exp(E::widen(v[j]), m, scale) * inv;
+    store(i, q);
+  };
+  if constexpr (LV > 0) {
+#pragma unroll
+    for (int j = 0; j < LV; ++j)
+      if ((R + j) * kStep < n) finish(place(R + j), kept[j * THREADS + threadIdx.x]);
+  }
+  for (int64_t at = past; at - mine < p.n; at += 4 * kStep) {
     VT v[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = shut ? VT(0) : load(i + j * kStep);
+    for (int j = 0; j < 4; ++j) v[j] = load(place64(at + j * kStep));
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (i + j * kStep - mine < p.n) finish(i + j * kStep, v[j], false);
+      if (at + j * kStep - mine < p.n) finish(place64(at + j * kStep), v[j]);
   }
 }
 
@@ -445,7 +477,7 @@ static RowCut cut_rows(int64_t rows, int64_t n) {
 // No slices (one workgroup per row, one launch) while a row is short or the rows fill the card
 // by themselves; else slices and two launches.
 RowCut cut_softmax(int64_t rows, int64_t n) {
-  if (n <= 32768 || rows >= 128) return {0, 0};
+  if (n >= 8 && (n <= 32768 || rows >= 128)) return {0, 0};  // (a row kernel's vectors hold up to 8)
   return cut_rows(rows, n);
 }
 
@@ -456,7 +488,7 @@ static hipError_t softmax_out(const SoftmaxParams& p, hipStream_t s) {
   if (p.slices == 0) {
     constexpr int64_t kSmall = 256 * 8 * Elem<DT>::kPer16;
     if (p.n <= kSmall) return launch_units(softmax_row_kernel<DT, OT, 256, 8, 0>, p, p.rows, 256, s);
-    return launch_units(softmax_row_kernel<DT, OT, 1024, DT == DS_BF16 ? 12 : 16, DT == DS_BF16 ? 4 : 8>, p, p.rows, 1024, s);
+    return launch_units(softmax_row_kernel<DT, OT, 1024, DT == DS_BF16 ? 8 : 20, DT == DS_BF16 ? 8 : 9>, p, p.rows, 1024, s);
   }
   const int64_t units = p.rows * p.slices;
   const hipError_t e = launch_units(softmax_stats_kernel<DT>, p, units, kSoftWaves * 64, s);
