@@ -377,6 +377,20 @@ __global__ __launch_bounds__(kListThreads) void list_softmax_kernel(ListSoftmaxP
   const int64_t r = unit / p.slices;
   const int sl = static_cast<int>(unit - r * p.slices);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  // the zeros first: they are on their way while the list is worked on
+  const int64_t lo = sl * p.slice, hi = lo + p.slice < p.n ? lo + p.slice : p.n;
+  typename O::T* out = static_cast<typename O::T*>(p.out) + r * p.out_stride;
+  constexpr int N = O::kPer16;
+  using W = Vec<OT, N>;
+  if (p.out) {
+    for (int64_t i = lo + static_cast<int64_t>(threadIdx.x) * N; i < hi; i += kListThreads * N) {
+      if (i + N <= hi) {
+        *reinterpret_cast<typename W::unaligned*>(out + i) = typename W::type(0);
+      } else {
+        for (int j = 0; i + j < hi; ++j) out[i + j] = O::narrow(0.0f);
+      }
+    }
+  }
   const typename E::T* vals = static_cast<const typename E::T*>(p.vals) + r * p.k;
   const int32_t* idx = p.idx + r * p.k;
   const float t = p.temperature ? p.temperature[r] : 1.0f;
@@ -446,17 +460,6 @@ __global__ __launch_bounds__(kListThreads) void list_softmax_kernel(ListSoftmaxP
       if (j < per && base + j < p.k) p.out_list[r * p.k + base + j] = static_cast<float>(e[j] * inv);
   }
   if (!p.out) return;
-  const int64_t lo = sl * p.slice, hi = lo + p.slice < p.n ? lo + p.slice : p.n;
-  typename O::T* out = static_cast<typename O::T*>(p.out) + r * p.out_stride;
-  constexpr int N = O::kPer16;
-  using W = Vec<OT, N>;
-  for (int64_t i = lo + static_cast<int64_t>(threadIdx.x) * N; i < hi; i += kListThreads * N) {
-    if (i + N <= hi) {
-      *reinterpret_cast<typename W::unaligned*>(out + i) = typename W::type(0);
-    } else {
-      for (int j = 0; i + j < hi; ++j) out[i + j] = O::narrow(0.0f);
-    }
-  }
   __syncthreads();  // the zeros are written before the entries go over them
 #pragma unroll
   for (int j = 0; j < kPer; ++j)
