@@ -556,67 +556,167 @@ __global__ __launch_bounds__(kRouteWaves * 64, V == 32 && KP == 16 ? 3 : 4) void
   }
 }
 
-// One wave per row, expert e in lane e % 64; each slot is given to its expert by comparing
-// indices, so no index is ever used as an address.
-template <int DT, int SCORE, int V>
-__global__ __launch_bounds__(kRouteWaves * 64) void route_grad_kernel(RouteGradParams p) {
+// ------------------------------------------------------------------------------ the gradient
+// A wave keeps a tile of rows in LDS, all zero between turns: slots are added at their
+// experts, lanes read the tile in memory's order and the slots clear what they added. Indices
+// are checked before they are used as places.
+constexpr int kGradTile = 2048;  // floats of a wave's tile
+
+// The chosen experts' gradients only (all others are zero): KL lanes a row, slot j in lane
+// j % KL; x is read at the chosen experts.
+//   slot j adds c_j = ds_j * ds/dx at its expert, with f_j = scale * g_j and, renormalised,
+//   ds_j = (f_j - sum f s / S) / S. The softmax renormalised is a softmax over the chosen
+//   experts alone: it needs no other logits, s is exp(x - the chosen ones' maximum).
+template <int DT, int SCORE, int KL>
+__global__ __launch_bounds__(kRouteWaves * 64) void route_grad_chosen_kernel(RouteGradParams p) {
   using E = Elem<DT>;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const typename E::T* x = static_cast<const typename E::T*>(p.x);
-  typename E::T* out = static_cast<typename E::T*>(p.out);
+  using T = typename E::T;
+  constexpr int N = E::kPer16, LEVELS = __builtin_ctz(KL);
+  __shared__ __attribute__((aligned(16))) float tiles[kRouteWaves][kGradTile];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, slot = lane % KL;
+  float* const tile = tiles[wave];
+  const T* x = static_cast<const T*>(p.x);
+  T* out = static_cast<T*>(p.out);
+  const int per_row = (p.experts + N - 1) / N, pitch = per_row * N;  // vectors of a row; floats of its tile
+  int rows = kGradTile / pitch;
+  rows = rows > 64 / KL ? 64 / KL : rows;
+  const float inv_per_row = 1.0f / static_cast<float>(per_row);
+#pragma unroll
+  for (int i = 0; i < kGradTile; i += 256) *reinterpret_cast<float4*>(tile + i + lane * 4) = make_float4(0, 0, 0, 0);
+  wave_sync();
+  for (int64_t r0 = (static_cast<int64_t>(blockIdx.x) * kRouteWaves + wave) * rows; r0 < p.rows;
+       r0 += static_cast<int64_t>(gridDim.x) * kRouteWaves * rows) {
+    const int here = p.rows - r0 < rows ? static_cast<int>(p.rows - r0) : rows;
+    const int row = lane / KL;
+    const bool live = row < here && slot < p.k;
+    int e = -1;
+    float f = 0.0f, v = kNegInf;
+    if (live) {
+      const int64_t at = (r0 + row) * p.k + slot;
+      e = p.idx[at];
+      f = p.grad[at] * p.scale;
+      if (e < 0 || e >= p.experts) e = -1;
+      if (e >= 0) v = E::widen(x[(r0 + row) * p.row_stride + e]);
+    }
+    f = e >= 0 ? f : 0.0f;
+    float s, slope;
+    if constexpr (SCORE == DS_SCORE_SOFTMAX) {
+      const float m = row_reduce<LEVELS>(v, [](float a, float b) { return larger(a, b); });
+      s = v == kNegInf ? 0.0f : v == m ? 1.0f : __builtin_amdgcn_exp2f((v - m) * kLog2E);
+      slope = s;
+    } else {
+      s = 1.0f / (1.0f + __builtin_amdgcn_exp2f(v * -kLog2E));
+      slope = s * (1.0f - s);
+    }
+    float d = f;
+    if (p.renorm) {
+      const float S = row_reduce<LEVELS>(s, plus<float>), fs = row_reduce<LEVELS>(f * s, plus<float>);
+      d = S > 0.0f ? (f - fs / S) / S : 0.0f;
+    }
+    const int place = e >= 0 ? row * pitch + e : -1;
+    if (place >= 0) atomicAdd(tile + place, d * slope);
+    wave_sync();
+    for (int i = lane; i < here * per_row; i += 64) {
+      const int of = static_cast<int>((static_cast<float>(i) + 0.5f) * inv_per_row), at = (i - of * per_row) * N;
+      const float* from = tile + of * pitch + at;
+      T* to = out + (r0 + of) * p.out_stride + at;
+      if (at + N <= p.experts) {
+        typename Vec<DT, N>::type q;
+#pragma unroll
+        for (int j = 0; j < N; ++j) q[j] = E::narrow(from[j]);
+        *reinterpret_cast<typename Vec<DT, N>::unaligned*>(to) = q;
+      } else {
+        for (int j = 0; at + j < p.experts; ++j) to[j] = E::narrow(from[j]);
+      }
+    }
+    wave_sync();
+    if (place >= 0) tile[place] = 0.0f;
+    wave_sync();
+  }
+}
+
+// The softmax without renormalisation has a gradient at every expert: one wave per row, V
+// vectors of N consecutive experts a lane.
+template <int DT, int V>
+__global__ __launch_bounds__(kRouteWaves * 64) void route_grad_softmax_kernel(RouteGradParams p) {
+  using E = Elem<DT>;
+  using T = typename E::T;
+  constexpr int N = E::kPer16;
+  typedef typename Vec<DT, N>::type VT;
+  __shared__ __attribute__((aligned(16))) float tiles[kRouteWaves][V * 64 * N];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  float* const tile = tiles[wave];
+  const T* x = static_cast<const T*>(p.x);
+  T* out = static_cast<T*>(p.out);
+#pragma unroll
+  for (int i = 0; i < V * 64 * N; i += 256)
+    *reinterpret_cast<float4*>(tile + i + lane * 4) = make_float4(0, 0, 0, 0);
+  wave_sync();
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRouteWaves + wave; r < p.rows;
        r += static_cast<int64_t>(gridDim.x) * kRouteWaves) {
-    float xv[V], s[V], h[V], hits[V];
-    float m = -__builtin_huge_valf();
+    int e = -1;
+    float f = 0.0f;
+    if (lane < p.k) {
+      e = p.idx[r * p.k + lane];
+      f = p.grad[r * p.k + lane] * p.scale;
+      if (e < 0 || e >= p.experts) e = -1;
+    }
+    const T* row = x + r * p.row_stride;
+    float s[V][N], m = kNegInf, z = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int e = v * 64 + lane;
-      xv[v] = e < p.experts ? E::widen(x[r * p.row_stride + e]) : -__builtin_huge_valf();
-      m = fmaxf(m, xv[v]);
-      h[v] = hits[v] = 0.0f;
-    }
-    if constexpr (SCORE == DS_SCORE_SOFTMAX) {
-      m = wave_max(m);
-      float z = 0.0f;
+      const int at = (v * 64 + lane) * N;
+      if (at + N <= p.experts) {
+        const VT q = *reinterpret_cast<const typename Vec<DT, N>::unaligned*>(row + at);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        s[v] = xv[v] == -__builtin_huge_valf() ? 0.0f : xv[v] == m ? 1.0f : expf(xv[v] - m);
-        z += s[v];
+        for (int j = 0; j < N; ++j) s[v][j] = E::widen(q[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) s[v][j] = at + j < p.experts ? E::widen(row[at + j]) : kNegInf;
       }
-      z = wave_sum(z);
 #pragma unroll
-      for (int v = 0; v < V; ++v) s[v] = z > 0.0f ? s[v] / z : 0.0f;
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) s[v] = 1.0f / (1.0f + expf(-xv[v]));
+      for (int j = 0; j < N; ++j) m = fmaxf(m, s[v][j]);
     }
-    for (int j = 0; j < p.k; ++j) {
-      const int e = p.idx[r * p.k + j];
-      const float g = p.grad[r * p.k + j] * p.scale;
+    if (e >= 0) atomicAdd(tile + e, f);
+    m = wave_max(m);
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (e == v * 64 + lane) h[v] += g, hits[v] += 1.0f;
-    }
-    if (p.renorm) {
-      float S = 0.0f, hs = 0.0f;
+    for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int v = 0; v < V; ++v) S += hits[v] * s[v], hs += h[v] * s[v];
-      S = wave_sum(S), hs = wave_sum(hs);
+      for (int j = 0; j < N; ++j) {
+        s[v][j] = s[v][j] == kNegInf ? 0.0f : s[v][j] == m ? 1.0f : __builtin_amdgcn_exp2f((s[v][j] - m) * kLog2E);
+        z += s[v][j];
+      }
+    z = wave_sum(z);
+    wave_sync();
+    const float inv = z > 0.0f ? 1.0f / z : 0.0f;
+    float h[V][N], dot = 0.0f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = S > 0.0f ? (h[v] - hits[v] * (hs / S)) / S : 0.0f;
-    }
-    float dot = 0.0f;  // with renormalised weights sum ds s is zero
-    if (SCORE == DS_SCORE_SOFTMAX && !p.renorm) {
+    for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int v = 0; v < V; ++v) dot += h[v] * s[v];
-      dot = wave_sum(dot);
-    }
+      for (int j = 0; j < N; ++j) {
+        h[v][j] = tile[(v * 64 + lane) * N + j];
+        s[v][j] *= inv;
+        dot += h[v][j] * s[v][j];
+      }
+    dot = wave_sum(dot);
+    wave_sync();
+    if (e >= 0) tile[e] = 0.0f;
+    T* to = out + r * p.out_stride;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int e = v * 64 + lane;
-      const float d = SCORE == DS_SCORE_SOFTMAX ? s[v] * (h[v] - dot) : h[v] * s[v] * (1.0f - s[v]);
-      if (e < p.experts) out[r * p.out_stride + e] = E::narrow(d);
+      const int at = (v * 64 + lane) * N;
+      VT q;
+#pragma unroll
+      for (int j = 0; j < N; ++j) q[j] = E::narrow(s[v][j] * (h[v][j] - dot));
+      if (at + N <= p.experts) {
+        *reinterpret_cast<typename Vec<DT, N>::unaligned*>(to + at) = q;
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (at + j < p.experts) to[at + j] = q[j];
+      }
     }
+    wave_sync();
   }
 }
 
@@ -670,15 +770,31 @@ hipError_t route_dt(int score, const RouteParams& p, hipStream_t s) {
   return by_score ? route_mode<DT, DS_SCORE_SIGMOID, kBySigmoid>(p, s) : route_mode<DT, DS_SCORE_SIGMOID, kByLogit>(p, s);
 }
 
-#define DS_ROUTE_V(KERN, DT, SCORE)                                                                              \
-  do {                                                                                                           \
-    const dim3 g(route_grid(p.rows, kRouteWaves, 16)), b(kRouteWaves * 64);                                          \
-    if (p.experts <= 64) hipLaunchKernelGGL((KERN<DT, SCORE, 1>), g, b, 0, s, p);                                \
-    else if (p.experts <= 128) hipLaunchKernelGGL((KERN<DT, SCORE, 2>), g, b, 0, s, p);                          \
-    else if (p.experts <= 256) hipLaunchKernelGGL((KERN<DT, SCORE, 4>), g, b, 0, s, p);                          \
-    else if (p.experts <= 512) hipLaunchKernelGGL((KERN<DT, SCORE, 8>), g, b, 0, s, p);                          \
-    else hipLaunchKernelGGL((KERN<DT, SCORE, 16>), g, b, 0, s, p);                                               \
-  } while (0)
+template <int DT, int SCORE>
+hipError_t grad_chosen(const RouteGradParams& p, hipStream_t s) {
+  const int pitch = (p.experts + Elem<DT>::kPer16 - 1) / Elem<DT>::kPer16 * Elem<DT>::kPer16;
+  const int fit = kGradTile / pitch;
+  const auto go = [&](auto kern, int kl) {
+    const int rows = fit < 64 / kl ? fit : 64 / kl;
+    hipLaunchKernelGGL(kern, dim3(route_grid(p.rows, kRouteWaves * rows, 16)), dim3(kRouteWaves * 64), 0, s, p);
+    return hipGetLastError();
+  };
+  if (p.k <= 2) return go(route_grad_chosen_kernel<DT, SCORE, 2>, 2);
+  if (p.k <= 4) return go(route_grad_chosen_kernel<DT, SCORE, 4>, 4);
+  if (p.k <= 8) return go(route_grad_chosen_kernel<DT, SCORE, 8>, 8);
+  if (p.k <= 16) return go(route_grad_chosen_kernel<DT, SCORE, 16>, 16);
+  return go(route_grad_chosen_kernel<DT, SCORE, 64>, 64);
+}
+
+template <int DT>
+hipError_t grad_softmax(const RouteGradParams& p, hipStream_t s) {
+  constexpr int kOne = 64 * Elem<DT>::kPer16;  // experts of one vector a lane
+  const dim3 g(route_grid(p.rows, kRouteWaves, 16)), b(kRouteWaves * 64);
+  if (p.experts <= kOne) hipLaunchKernelGGL((route_grad_softmax_kernel<DT, 1>), g, b, 0, s, p);
+  else if (p.experts <= 2 * kOne) hipLaunchKernelGGL((route_grad_softmax_kernel<DT, 2>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((route_grad_softmax_kernel<DT, DS_MAX_EXPERTS / kOne>), g, b, 0, s, p);
+  return hipGetLastError();
+}
 
 }  // namespace
 
@@ -687,14 +803,10 @@ hipError_t launch_route(int dtype, int score, const RouteParams& p, hipStream_t 
 }
 
 hipError_t launch_route_grad(int dtype, int score, const RouteGradParams& p, hipStream_t s) {
-  if (dtype == DS_BF16) {
-    if (score == DS_SCORE_SOFTMAX) DS_ROUTE_V(route_grad_kernel, DS_BF16, DS_SCORE_SOFTMAX);
-    else DS_ROUTE_V(route_grad_kernel, DS_BF16, DS_SCORE_SIGMOID);
-  } else {
-    if (score == DS_SCORE_SOFTMAX) DS_ROUTE_V(route_grad_kernel, DS_FP32, DS_SCORE_SOFTMAX);
-    else DS_ROUTE_V(route_grad_kernel, DS_FP32, DS_SCORE_SIGMOID);
-  }
-  return hipGetLastError();
+  if (score == DS_SCORE_SOFTMAX && !p.renorm) return dtype == DS_BF16 ? grad_softmax<DS_BF16>(p, s) : grad_softmax<DS_FP32>(p, s);
+  if (score == DS_SCORE_SOFTMAX)
+    return dtype == DS_BF16 ? grad_chosen<DS_BF16, DS_SCORE_SOFTMAX>(p, s) : grad_chosen<DS_FP32, DS_SCORE_SOFTMAX>(p, s);
+  return dtype == DS_BF16 ? grad_chosen<DS_BF16, DS_SCORE_SIGMOID>(p, s) : grad_chosen<DS_FP32, DS_SCORE_SIGMOID>(p, s);
 }
 
 }  // namespace ds
