@@ -9,6 +9,8 @@ used; in units of u = 2^-24, half a step of fp32):
     a path (at most 300 here), divisions 4 u. Quotients: (50 + 50 + 300 + 4) u < 2^-15.
   * an element d below that range has exp(d) 3 |d| u < 3 e^-1 u of the row's maximum: 2^-22
     of the row's largest value, as an absolute term.
+  * exp below fp32's least normal number, 2^-126, is held as 0; it is multiplied by gradients
+    and scales below 2^6 here: 2^-120, whatever the row's largest value.
   * a result held in bf16 adds half a step, 2^-8 relative (fp32: 2^-24, contained above).
 """
 import numpy as np
@@ -21,7 +23,7 @@ from oracle import rows as orc
 
 pytestmark = pytest.mark.gpu
 
-RTOL, ATOL = 2.0 ** -15, 2.0 ** -22
+RTOL, ATOL, LEAST = 2.0 ** -15, 2.0 ** -22, 2.0 ** -120
 DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
 NEG = float("-inf")
 
@@ -41,7 +43,7 @@ def _close(got, want, label, size=None, bf16=False):
     assert np.isfinite(got).all(), label
     big = np.abs(want) if size is None else size
     top = np.abs(big).max(axis=-1, keepdims=True) if big.size else 0
-    tol = RTOL * big + ATOL * top + (2.0 ** -8 * np.abs(want) if bf16 else 0)
+    tol = RTOL * big + ATOL * top + LEAST + (2.0 ** -8 * np.abs(want) if bf16 else 0)
     bad = np.abs(got - want) > tol
     assert not bad.any(), f"{label}: {bad.sum()} of {bad.size} off, worst {np.max(np.abs(got - want) - tol)}"
 
@@ -164,7 +166,7 @@ def test_route_grad_matches_definition(shape, dtype):
     rows, n, k, groups, tg, top = shape
     for score in (ts.SCORE_SOFTMAX, ts.SCORE_SIGMOID):
         for renorm in (False, True):
-            for kind in ("normal", "masked"):
+            for kind in ("normal", "masked", "far"):
                 x = _logits(3 * n + k, rows, n, DT[dtype], kind)
                 _, idx = ts.ds_route(x, k, score=score, groups=groups, topk_groups=tg, group_top=top)
                 g = torch.randn(rows, k, generator=_gen(n + 1)).cuda()
@@ -175,6 +177,19 @@ def test_route_grad_matches_definition(shape, dtype):
                 # every element is a sum of terms of total magnitude `size`, each with the scores' error
                 _close(dx, want, f"grad {shape} {dtype} {name} renorm={renorm} {kind}", size=4 * size,
                        bf16=dtype == "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_route_far_below_zero(dtype):
+    """Sigmoid scores that fp32 does not hold: weights and gradients are those of their ratios."""
+    x = (_logits(61, 20, 48, torch.float32) - torch.tensor([90.0, 120.0, 300.0, 600.0]).repeat(5)[:, None].cuda()).to(DT[dtype])
+    w, i = _check_route(x, 5, None, "far below", score=ts.SCORE_SIGMOID, renormalize=True, scale=2.0)
+    assert (w.sum(dim=1) - 2).abs().max() < 1e-5
+    g = torch.randn(20, 5, generator=_gen(62)).cuda()
+    dx = ts.ds_route_grad(x, i, g, score=ts.SCORE_SIGMOID, renormalize=True, scale=2.0)
+    want, size = orc.route_grad(_np(x), _np(i), _np(g), "sigmoid", True, 2.0)
+    _close(dx, want, "far below", size=4 * size, bf16=dtype == "bf16")
+    assert np.abs(want).max() > 0.1
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])

@@ -307,36 +307,47 @@ def ds_topk_merge(rows: int, n: int, k: int, dtype: int, seed: int = 0, workspac
 
 
 # ------------------------------------------------------- the operators beside the selection
-def _rows_of(x, what: str):
-    """The (row stride) of the last two dimensions of a device tensor with contiguous rows."""
-    if not x.is_cuda:
-        raise ValueError(f"{what} must be a device tensor")
-    if x.shape[-1] > 1 and x.stride(-1) != 1:
-        raise ValueError(f"rows of {what} must be contiguous (stride(-1) == 1)")
+# These calls are short (small batches of a serving loop), so their checks read each property
+# once and the C functions are looked up once.
+_functions: Dict[str, object] = {}
+_sizes: Dict[tuple, int] = {}
+
+
+def _function(name: str):
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = getattr(lib(), name)
+    return f
 
 
 def _matrix(x, what: str):
     """rows, n, row stride of a 2-D device tensor with contiguous rows."""
     if x.dim() != 2:
         raise ValueError(f"{what} must be 2-D")
-    _rows_of(x, what)
+    if not x.is_cuda:
+        raise ValueError(f"{what} must be a device tensor")
     rows, n = x.shape
-    return rows, n, x.stride(0) if rows > 1 else max(n, 1)
+    stride, one = x.stride()
+    if one != 1 and n > 1:
+        raise ValueError(f"rows of {what} must be contiguous (stride(-1) == 1)")
+    return rows, n, stride if rows > 1 else max(n, 1)
 
 
 def _batch_rows(x, what: str):
     """batch, rows per sequence, n, row stride of a 3-D device tensor whose rows lie evenly apart."""
     if x.dim() != 3:
         raise ValueError(f"{what} must be 3-D")
-    _rows_of(x, what)
+    if not x.is_cuda:
+        raise ValueError(f"{what} must be a device tensor")
     b, m, n = x.shape
+    of_b, of_m, one = x.stride()
+    if one != 1 and n > 1:
+        raise ValueError(f"rows of {what} must be contiguous (stride(-1) == 1)")
     if m > 1:
-        stride = x.stride(1)
-        if b > 1 and x.stride(0) != m * stride:
+        if b > 1 and of_b != m * of_m:
             raise ValueError(f"rows of {what} must lie evenly apart (stride(0) == shape[1] * stride(1))")
-    else:
-        stride = x.stride(0) if b > 1 else n
-    return b, m, n, stride
+        return b, m, n, of_m
+    return b, m, n, of_b if b > 1 else max(n, 1)
 
 
 def _operand(t, what: str, dtype, shape, device):
@@ -348,43 +359,32 @@ def _operand(t, what: str, dtype, shape, device):
     return t.data_ptr()
 
 
-def _call(name: str, device, stream, args) -> None:
+def _call(name: str, device, stream, *args) -> None:
     """Calls the C entry with the stream last, with `device` current (the stream is the given
     one, or torch's current stream on that device)."""
     torch = _torch()
-    if device.index is not None and device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            st = getattr(lib(), name)(*args, _stream_handle(stream, device))
+    index, f = device.index, _function(name)
+    if index is None or index == torch._C._cuda_getDevice():
+        st = f(*args, _stream_handle(stream, device))
     else:
-        st = getattr(lib(), name)(*args, _stream_handle(stream, device))
+        with torch.cuda.device(device):
+            st = f(*args, _stream_handle(stream, device))
     if st != DS_OK:
         raise DSError(st, name)
-
-
-def _scratch(size_of, rows: int, n: int, dt: int, workspace, device, stream):
-    """The call's workspace (kept by the caller until the call has been made), its address and
-    its bytes: the one given, or one of the needed size from torch, which is told about a
-    stream that is not its current one."""
-    if workspace is None:
-        b = ctypes.c_size_t(0)
-        if size_of(rows, n, dt, ctypes.byref(b)) != DS_OK or b.value == 0:  # the call itself reports what is wrong
-            return None, None, 0
-        torch = _torch()
-        workspace = torch.empty(b.value, dtype=torch.uint8, device=device)
-        if stream is not None and stream != torch.cuda.current_stream(device):
-            workspace.record_stream(stream)
-        return workspace, workspace.data_ptr(), b.value
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _workspace_size(name: str, rows: int, n: int, dtype: int) -> int:
-    b = ctypes.c_size_t(0)
-    st = getattr(lib(), name)(rows, n, dtype, ctypes.byref(b))
-    if st != DS_OK:
-        raise DSError(st, name)
-    return int(b.value)
+    key = (name, rows, n, dtype)
+    size = _sizes.get(key)
+    if size is None:
+        b = ctypes.c_size_t(0)
+        st = _function(name)(rows, n, dtype, ctypes.byref(b))
+        if st != DS_OK:
+            raise DSError(st, name)
+        if len(_sizes) >= 4096:
+            _sizes.clear()
+        size = _sizes[key] = int(b.value)
+    return size
 
 
 def ds_softmax_workspace_size(rows: int, n: int, dtype: int) -> int:
@@ -393,6 +393,23 @@ def ds_softmax_workspace_size(rows: int, n: int, dtype: int) -> int:
 
 def ds_verify_workspace_size(batch: int, n: int, dtype: int) -> int:
     return _workspace_size("ds_verify_workspace_size", batch, n, dtype)
+
+
+def _scratch(need: int, workspace, device, stream):
+    """The call's workspace (to be kept until the call has been made), its address and its bytes:
+    the one given, or one of the needed size from torch, which is told about a stream that is
+    not its current one."""
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        torch = _torch()
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        if stream is not None and stream != torch.cuda.current_stream(device):
+            workspace.record_stream(stream)
+        return workspace, workspace.data_ptr(), need
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def ds_route(x, k: int, bias=None, score: int = SCORE_SOFTMAX, groups: int = 1, topk_groups: int = 0,
@@ -407,16 +424,22 @@ def ds_route(x, k: int, bias=None, score: int = SCORE_SOFTMAX, groups: int = 1, 
     torch = _torch()
     rows, n, rs = _matrix(x, "x")
     dt, dev, shape = dtype_code(x), x.device, (rows, k)
-    if weights and out_weights is None:
+    if out_weights is not None:
+        wp = _operand(out_weights, "out_weights", torch.float32, shape, dev)
+    elif weights:
         out_weights = torch.empty(shape, dtype=torch.float32, device=dev)
-    if out_idx is None:
+        wp = out_weights.data_ptr()
+    else:
+        wp = None
+    if out_idx is not None:
+        ip = _operand(out_idx, "out_idx", torch.int32, shape, dev)
+    else:
         out_idx = torch.empty(shape, dtype=torch.int32, device=dev)
+        ip = out_idx.data_ptr()
     cfg = ds_route_config(score, groups, topk_groups, group_top, 1 if renormalize else 0, scale)
-    _call("ds_route", dev, stream,
-          (x.data_ptr(), rows, n, rs, k, dt, _operand(bias, "bias", torch.float32, (n,), dev), ctypes.byref(cfg),
-           _operand(out_weights, "out_weights", torch.float32, shape, dev),
-           _operand(out_idx, "out_idx", torch.int32, shape, dev),
-           _operand(counts, "counts", torch.int32, (n,), dev)))
+    _call("ds_route", dev, stream, x.data_ptr(), rows, n, rs, k, dt,
+          None if bias is None else _operand(bias, "bias", torch.float32, (n,), dev), ctypes.byref(cfg), wp, ip,
+          None if counts is None else _operand(counts, "counts", torch.int32, (n,), dev))
     return out_weights, out_idx
 
 
@@ -429,25 +452,26 @@ def ds_route_grad(x, idx, grad_weights, score: int = SCORE_SOFTMAX, renormalize:
     dt, dev = dtype_code(x), x.device
     if idx.dim() != 2:
         raise ValueError("idx must be 2-D [rows, k]")
-    k = idx.shape[1]
+    shape = (rows, idx.shape[1])
     if out is None:
-        out = torch.empty((rows, n), dtype=x.dtype, device=dev)
-    _, _, os = _matrix(out, "out")
-    if out.dtype != x.dtype or tuple(out.shape) != (rows, n) or out.device != dev:
-        raise ValueError("out must be [rows, experts] of x's dtype on x's device")
+        out, os = torch.empty((rows, n), dtype=x.dtype, device=dev), n
+    else:
+        _, _, os = _matrix(out, "out")
+        if out.dtype != x.dtype or out.shape != (rows, n) or out.device != dev:
+            raise ValueError("out must be [rows, experts] of x's dtype on x's device")
     cfg = ds_route_config(score, 1, 1, 1, 1 if renormalize else 0, scale)
-    _call("ds_route_grad", dev, stream,
-          (x.data_ptr(), rows, n, rs, k, dt, ctypes.byref(cfg), _operand(idx, "idx", torch.int32, (rows, k), dev),
-           _operand(grad_weights, "grad_weights", torch.float32, (rows, k), dev), out.data_ptr(), os))
+    _call("ds_route_grad", dev, stream, x.data_ptr(), rows, n, rs, shape[1], dt, ctypes.byref(cfg),
+          _operand(idx, "idx", torch.int32, shape, dev),
+          _operand(grad_weights, "grad_weights", torch.float32, shape, dev), out.data_ptr(), os)
     return out
 
 
 def _out_rows(out, out_dtype, rows: int, n: int, dev):
     torch = _torch()
     if out is None:
-        out = torch.empty((rows, n), dtype=out_dtype or torch.float32, device=dev)
+        return torch.empty((rows, n), dtype=out_dtype or torch.float32, device=dev), n
     _, _, os = _matrix(out, "out")
-    if tuple(out.shape) != (rows, n) or out.device != dev or (out_dtype is not None and out.dtype != out_dtype):
+    if out.shape != (rows, n) or out.device != dev or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out must be [rows, n] of out_dtype on the inputs' device")
     return out, os
 
@@ -460,10 +484,10 @@ def ds_softmax(x, temperature=None, out_dtype=None, out=None, workspace=None, st
     rows, n, rs = _matrix(x, "x")
     dt, dev = dtype_code(x), x.device
     out, os = _out_rows(out, out_dtype, rows, n, dev)
-    keep, ws, ws_bytes = _scratch(lib().ds_softmax_workspace_size, rows, n, dt, workspace, dev, stream)
-    _call("ds_softmax", dev, stream,
-          (x.data_ptr(), rows, n, rs, dt, _operand(temperature, "temperature", torch.float32, (rows,), dev),
-           out.data_ptr(), os, dtype_code(out), ws, ws_bytes))
+    keep, ws, ws_bytes = _scratch(ds_softmax_workspace_size(rows, n, dt), workspace, dev, stream)
+    _call("ds_softmax", dev, stream, x.data_ptr(), rows, n, rs, dt,
+          None if temperature is None else _operand(temperature, "temperature", torch.float32, (rows,), dev),
+          out.data_ptr(), os, dtype_code(out), ws, ws_bytes)
     return out
 
 
@@ -477,20 +501,21 @@ def ds_topk_softmax(vals, idx, n: int, ks=None, temperature=None, top_p=None, ou
     torch = _torch()
     if vals.dim() != 2 or not vals.is_cuda or not vals.is_contiguous():
         raise ValueError("vals must be a contiguous 2-D device tensor [rows, k]")
-    rows, k = vals.shape
-    dt, dev = dtype_code(vals), vals.device
+    rows, k = shape = vals.shape
+    dt, dev, f32 = dtype_code(vals), vals.device, torch.float32
     if rows_out:
         out, os = _out_rows(out, out_dtype, rows, n, dev)
+        op, odt = out.data_ptr(), dtype_code(out)
     else:
-        out, os = None, n
+        op, os, odt = None, n, FP32
         if out_list is None:
-            out_list = torch.empty((rows, k), dtype=torch.float32, device=dev)
-    f32 = torch.float32
-    _call("ds_topk_softmax", dev, stream,
-          (vals.data_ptr(), _operand(idx, "idx", torch.int32, (rows, k), dev), rows, k, dt,
-           _operand(ks, "ks", torch.int32, (rows,), dev), _operand(temperature, "temperature", f32, (rows,), dev),
-           _operand(top_p, "top_p", f32, (rows,), dev), n, out.data_ptr() if rows_out else None, os,
-           dtype_code(out) if rows_out else FP32, _operand(out_list, "out_list", f32, (rows, k), dev)))
+            out_list = torch.empty(shape, dtype=f32, device=dev)
+    per_row = (rows,)
+    _call("ds_topk_softmax", dev, stream, vals.data_ptr(), _operand(idx, "idx", torch.int32, shape, dev), rows, k, dt,
+          None if ks is None else _operand(ks, "ks", torch.int32, per_row, dev),
+          None if temperature is None else _operand(temperature, "temperature", f32, per_row, dev),
+          None if top_p is None else _operand(top_p, "top_p", f32, per_row, dev), n, op, os, odt,
+          None if out_list is None else _operand(out_list, "out_list", f32, shape, dev))
     return out if rows_out else out_list
 
 
@@ -508,26 +533,31 @@ def ds_verify(target, draft, draft_tokens, accept_u, sample_u, draft_lens=None, 
     dt, dev, K = dtype_code(target), target.device, m - 1
     if K < 0:
         raise ValueError("target must hold at least one row per sequence")
+    if sample_u is None or (K > 0 and (draft_tokens is None or accept_u is None)):
+        raise ValueError("draft_tokens, accept_u and sample_u are needed")
     dp, dstride = None, n
     if draft is not None and K > 0:
         b2, k2, n2, dstride = _batch_rows(draft, "draft")
         if (b2, k2, n2) != (batch, K, n) or draft.dtype != target.dtype or draft.device != dev:
             raise ValueError("draft must be [batch, drafts, n] of target's dtype on its device")
         dp = draft.data_ptr()
+    i32, f32, each, per_seq = torch.int32, torch.float32, (batch, K), (batch,)
     if out_tokens is None:
-        out_tokens = torch.empty((batch, m), dtype=torch.int32, device=dev)
+        out_tokens = torch.empty((batch, m), dtype=i32, device=dev)
+        tp = out_tokens.data_ptr()
+    else:
+        tp = _operand(out_tokens, "out_tokens", i32, (batch, m), dev)
     if out_accepted is None:
-        out_accepted = torch.empty((batch,), dtype=torch.int32, device=dev)
-    if K > 0 and (draft_tokens is None or accept_u is None) or sample_u is None:
-        raise ValueError("draft_tokens, accept_u and sample_u are needed")
-    i32, f32 = torch.int32, torch.float32
-    keep, ws, ws_bytes = _scratch(lib().ds_verify_workspace_size, batch, n, dt, workspace, dev, stream)
-    _call("ds_verify", dev, stream,
-          (target.data_ptr(), ts, dp, dstride, _operand(draft_tokens, "draft_tokens", i32, (batch, K), dev),
-           _operand(draft_lens, "draft_lens", i32, (batch,), dev),
-           _operand(accept_u, "accept_u", f32, (batch, K), dev), _operand(sample_u, "sample_u", f32, (batch,), dev),
-           batch, K, n, dt, _operand(out_tokens, "out_tokens", i32, (batch, m), dev),
-           _operand(out_accepted, "out_accepted", i32, (batch,), dev), ws, ws_bytes))
+        out_accepted = torch.empty(per_seq, dtype=i32, device=dev)
+        ap = out_accepted.data_ptr()
+    else:
+        ap = _operand(out_accepted, "out_accepted", i32, per_seq, dev)
+    keep, ws, ws_bytes = _scratch(ds_verify_workspace_size(batch, n, dt), workspace, dev, stream)
+    _call("ds_verify", dev, stream, target.data_ptr(), ts, dp, dstride,
+          _operand(draft_tokens, "draft_tokens", i32, each, dev),
+          None if draft_lens is None else _operand(draft_lens, "draft_lens", i32, per_seq, dev),
+          _operand(accept_u, "accept_u", f32, each, dev), _operand(sample_u, "sample_u", f32, per_seq, dev),
+          batch, K, n, dt, tp, ap, ws, ws_bytes)
     return out_tokens, out_accepted
 
 

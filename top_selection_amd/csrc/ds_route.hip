@@ -605,8 +605,16 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_grad_chosen_kernel(Rou
       s = v == kNegInf ? 0.0f : v == m ? 1.0f : __builtin_amdgcn_exp2f((v - m) * kLog2E);
       slope = s;
     } else {
-      s = 1.0f / (1.0f + __builtin_amdgcn_exp2f(v * -kLog2E));
-      slope = s * (1.0f - s);
+      // scores far below 1 in units of the largest, which divides out of s / S: with
+      // u = exp(-|x|), s = exp(min(x, 0)) / (1 + u) and 1 - s = exp(min(-x, 0)) / (1 + u)
+      float unit = 0.0f;
+      if (p.renorm) {
+        unit = row_reduce<LEVELS>(v, [](float a, float b) { return larger(a, b); });
+        unit = unit < 0.0f && unit > kNegInf ? unit : 0.0f;
+      }
+      const float part = 1.0f / (1.0f + __builtin_amdgcn_exp2f(fabsf(v) * -kLog2E));
+      s = part * __builtin_amdgcn_exp2f((fminf(v, 0.0f) - unit) * kLog2E);
+      slope = s * part * __builtin_amdgcn_exp2f(fminf(-v, 0.0f) * kLog2E);
     }
     float d = f;
     if (p.renorm) {
