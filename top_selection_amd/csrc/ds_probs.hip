@@ -207,13 +207,13 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
   // what is past the kept vectors: the running maximum and sum, four vectors at a time
   const int64_t past = kKept + static_cast<int64_t>(mine), end = p.n - N;
   const auto place64 = [&](int64_t i) { return i < end ? i : end; };
-  const auto sum_of = [&](VT v, int64_t back, float top) {  // back: elements that another vector holds too
+  // exp((v - top) / t) as exp2(v * scale - top * scale) with the product of the maximum rounded
+  // once: what that is off by is the same factor everywhere and divides out
+  const auto term = [&](T v, float tops) { return __builtin_amdgcn_exp2f(fmaf(E::widen(v), scale, -tops)); };
+  const auto sum_of = [&](VT v, int64_t back, float tops) {  // back: elements that another vector holds too
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float e = soft_exp(E::widen(v[i]), top, scale);
-      s += i >= back ? e : 0.0f;
-    }
+    for (int i = 0; i < N; ++i) s += i >= back ? term(v[i], tops) : 0.0f;
     return s;
   };
   for (int64_t at = past; at - mine < p.n; at += 4 * kStep) {
@@ -224,9 +224,10 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) top = most(top, v[j]);
     if (top != kNegInf) {
-      z *= soft_exp(m, top, scale);
+      const float tops = top * scale;
+      z *= m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m * scale - tops);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) z += sum_of(v[j], at + j * kStep - place64(at + j * kStep), top);
+      for (int j = 0; j < 4; ++j) z += sum_of(v[j], at + j * kStep - place64(at + j * kStep), tops);
     }
     m = top;
   }
@@ -279,13 +280,42 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
     }
     return;
   }
-  z *= own == kNegInf ? 0.0f : soft_exp(own, m, scale);
+  const float ms = m * scale;
+  const auto block_sum = [&](float v) {
+    v = wave_sum(v);
+    if (lane == 0) of_wave[wave] = v;
+    __syncthreads();
+    v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) v += of_wave[w];
+    return v;
+  };
+  if (!(fabsf(ms) < 1e30f)) {  // an infinite maximum or inverse temperature: element by element
+    z = 0.0f;
+    for (int64_t i = mine; i < p.n; i += kStep) {
+      const int64_t a = place64(i);
+      const VT v = load(a);
+#pragma unroll
+      for (int j = 0; j < N; ++j) z += a + j >= i ? soft_exp(E::widen(v[j]), m, scale) : 0.0f;
+    }
+    const float inv = 1.0f / block_sum(z);
+    for (int64_t i = mine; i < p.n; i += kStep) {
+      const int64_t a = place64(i);
+      const VT v = load(a);
+      typename W::type o;
+#pragma unroll
+      for (int j = 0; j < N; ++j) o[j] = O::narrow(soft_exp(E::widen(v[j]), m, scale) * inv);
+      *reinterpret_cast<typename W::unaligned*>(out + a) = o;
+    }
+    return;
+  }
+  z *= own == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(own * scale - ms);
 #pragma unroll
   for (int j = 0; j < R; ++j) {
     const bool whole = (j + 1) * kStep <= n;
     if constexpr (DT == DS_FP32) {  // the registers hold exp from here on (bf16 has no room for it)
 #pragma unroll
-      for (int i = 0; i < N; ++i) reg[j][i] = soft_exp(reg[j][i], m, scale);
+      for (int i = 0; i < N; ++i) reg[j][i] = term(reg[j][i], ms);
       if (whole) {
 #pragma unroll
         for (int i = 0; i < N; ++i) z += reg[j][i];
@@ -294,23 +324,20 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
 #pragma unroll
         for (int i = 0; i < N; ++i) z += i >= back ? reg[j][i] : 0.0f;
       }
+    } else if (whole) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) z += term(reg[j][i], ms);
     } else {
-      z += sum_of(reg[j], whole ? 0 : j * kStep + mine - place(j), m);
+      z += sum_of(reg[j], j * kStep + mine - place(j), ms);
     }
     __builtin_amdgcn_sched_barrier(0);  // vector by vector: more at a time takes more registers than there are
   }
   if constexpr (LV > 0) {
 #pragma unroll
     for (int j = 0; j < LV; ++j)
-      z += sum_of(kept[j * THREADS + threadIdx.x], (R + j) * kStep + mine - place(R + j), m);
+      z += sum_of(kept[j * THREADS + threadIdx.x], (R + j) * kStep + mine - place(R + j), ms);
   }
-  z = wave_sum(z);
-  if (lane == 0) of_wave[wave] = z;
-  __syncthreads();
-  z = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) z += of_wave[w];
-  const float inv = 1.0f / z;
+  const float inv = 1.0f / block_sum(z);
   asm volatile("" : "+v"(mine));
   const auto store = [&](auto i, const float* q) {
     typename W::type o;
@@ -324,14 +351,14 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
       float q[N];
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        q[i] = (DT == DS_FP32 ? E::widen(reg[j][i]) : soft_exp(E::widen(reg[j][i]), m, scale)) * inv;
+        q[i] = (DT == DS_FP32 ? E::widen(reg[j][i]) : term(reg[j][i], ms)) * inv;
       store(place(j), q);
       __builtin_amdgcn_sched_barrier(0);
     }
   const auto finish = [&](auto i, VT v) {
     float q[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) q[j] = soft_exp(E::widen(v[j]), m, scale) * inv;
+    for (int j = 0; j < N; ++j) q[j] = term(v[j], ms) * inv;
     store(i, q);
   };
   if constexpr (LV > 0) {
@@ -480,7 +507,7 @@ static RowCut cut_rows(int64_t rows, int64_t n) {
 // No slices (one workgroup per row, one launch) while a row is short or the rows fill the card
 // by themselves; else slices and two launches.
 RowCut cut_softmax(int64_t rows, int64_t n) {
-  if (n >= 8 && (n <= 32768 || rows >= 128)) return {0, 0};  // (a row kernel's vectors hold up to 8)
+  if (n >= 8 && (n <= 32768 || rows >= 80)) return {0, 0};  // (a row kernel's vectors hold up to 8)
   return cut_rows(rows, n);
 }
 
@@ -489,9 +516,14 @@ RowCut cut_list_softmax(int64_t rows, int64_t n) { return cut_rows(rows, n); }
 template <int DT, int OT>
 static hipError_t softmax_out(const SoftmaxParams& p, hipStream_t s) {
   if (p.slices == 0) {
-    constexpr int64_t kSmall = 256 * 8 * Elem<DT>::kPer16;
-    if (p.n <= kSmall) return launch_units(softmax_row_kernel<DT, OT, 256, 8, 0>, p, p.rows, 256, s);
-    return launch_units(softmax_row_kernel<DT, OT, 1024, DT == DS_BF16 ? 8 : 20, DT == DS_BF16 ? 8 : 9>, p, p.rows, 1024, s);
+    // the fewest vectors a thread that hold the row: those past its end cost as much as others
+    const int64_t vectors = (p.n + Elem<DT>::kPer16 - 1) / Elem<DT>::kPer16;
+    if (vectors <= 256 * 4) return launch_units(softmax_row_kernel<DT, OT, 256, 4, 0>, p, p.rows, 256, s);
+    if (vectors <= 256 * 8) return launch_units(softmax_row_kernel<DT, OT, 256, 8, 0>, p, p.rows, 256, s);
+    if (vectors <= 1024 * 4) return launch_units(softmax_row_kernel<DT, OT, 1024, 4, 0>, p, p.rows, 1024, s);
+    if (vectors <= 1024 * 8) return launch_units(softmax_row_kernel<DT, OT, 1024, 8, 0>, p, p.rows, 1024, s);
+    constexpr bool kTwo = DT == DS_BF16;  // (two bytes an element)
+    return launch_units(softmax_row_kernel<DT, OT, 1024, kTwo ? 8 : 20, kTwo ? 8 : 9>, p, p.rows, 1024, s);
   }
   const int64_t units = p.rows * p.slices;
   const hipError_t e = launch_units(softmax_stats_kernel<DT>, p, units, kSoftWaves * 64, s);
