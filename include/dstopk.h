@@ -351,8 +351,8 @@ typedef struct ds_route_config {
  *   bias         NULL, or [experts] float.
  *   out_weights  [rows, k] float, or NULL.
  *   out_idx      [rows, k] int32, or NULL. Not both NULL.
- *   counts       NULL, or [experts] int32: the number of rows that chose each expert is ADDED
- *                to it (the load that a balancing bias is updated from).
+ *   counts       NULL, or [experts] int32 (out_idx is needed then): the number of rows that
+ *                chose each expert is ADDED to it (the load that a balancing bias is updated from).
  */
 int ds_route(const void* x, int64_t rows, int64_t experts, int64_t row_stride, int k, int dtype, const float* bias,
              const ds_route_config* cfg, float* out_weights, int32_t* out_idx, int32_t* counts, void* stream);

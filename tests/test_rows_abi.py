@@ -78,7 +78,7 @@ def test_constants_and_struct_match_the_header():
 @pytest.mark.parametrize("kw,code", [
     (dict(dtype=2), BAD), (dict(rows=-1), BAD), (dict(experts=0), BAD), (dict(stride=63), BAD), (dict(k=0), BAD),
     (dict(k=65), BAD), (dict(experts=1025), BIG), (dict(experts=512, k=65), BIG), (dict(x=None), BAD),
-    (dict(w=None, idx=None), BAD), (dict(cfg=_cfg(score=2)), BAD), (dict(cfg=_cfg(groups=-1)), BAD),
+    (dict(w=None, idx=None), BAD), (dict(idx=None, counts=FAKE), BAD), (dict(cfg=_cfg(score=2)), BAD), (dict(cfg=_cfg(groups=-1)), BAD),
     (dict(cfg=_cfg(groups=5)), BAD), (dict(cfg=_cfg(groups=4, topk_groups=5)), BAD),
     (dict(cfg=_cfg(groups=16, topk_groups=1)), BAD),  # four experts for k = 6
     (dict(cfg=_cfg(groups=4, topk_groups=2, group_top=3)), BAD), (dict(cfg=_cfg(groups=64, topk_groups=64, group_top=2)), BAD),

@@ -311,6 +311,7 @@ def ds_topk_merge(rows: int, n: int, k: int, dtype: int, seed: int = 0, workspac
 # once and the C functions are looked up once.
 _functions: Dict[str, object] = {}
 _sizes: Dict[tuple, int] = {}
+_codes: Dict[object, int] = {}  # torch dtypes, once one was asked for
 
 
 def _function(name: str):
@@ -318,6 +319,18 @@ def _function(name: str):
     if f is None:
         f = _functions[name] = getattr(lib(), name)
     return f
+
+
+def _code(dtype) -> int:
+    """The element type's code (dtype_code of a tensor's dtype)."""
+    code = _codes.get(dtype)
+    if code is None:
+        torch = _torch()
+        _codes.update({torch.bfloat16: BF16, torch.float32: FP32})
+        code = _codes.get(dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {dtype}; expected torch.bfloat16 or torch.float32")
+    return code
 
 
 def _matrix(x, what: str):
@@ -362,10 +375,11 @@ def _operand(t, what: str, dtype, shape, device):
 def _call(name: str, device, stream, *args) -> None:
     """Calls the C entry with the stream last, with `device` current (the stream is the given
     one, or torch's current stream on that device)."""
+    f = _functions.get(name) or _function(name)
     torch = _torch()
-    index, f = device.index, _function(name)
-    if index is None or index == torch._C._cuda_getDevice():
-        st = f(*args, _stream_handle(stream, device))
+    index = device.index
+    if index == torch._C._cuda_getDevice():
+        st = f(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(device):
             st = f(*args, _stream_handle(stream, device))
@@ -423,7 +437,7 @@ def ds_route(x, k: int, bias=None, score: int = SCORE_SOFTMAX, groups: int = 1, 
     """
     torch = _torch()
     rows, n, rs = _matrix(x, "x")
-    dt, dev, shape = dtype_code(x), x.device, (rows, k)
+    dt, dev, shape = _code(x.dtype), x.device, (rows, k)
     if out_weights is not None:
         wp = _operand(out_weights, "out_weights", torch.float32, shape, dev)
     elif weights:
@@ -449,7 +463,7 @@ def ds_route_grad(x, idx, grad_weights, score: int = SCORE_SOFTMAX, renormalize:
     int32 and the weights' gradient [rows, k] fp32; [rows, experts] of x's dtype."""
     torch = _torch()
     rows, n, rs = _matrix(x, "x")
-    dt, dev = dtype_code(x), x.device
+    dt, dev = _code(x.dtype), x.device
     if idx.dim() != 2:
         raise ValueError("idx must be 2-D [rows, k]")
     shape = (rows, idx.shape[1])
@@ -482,12 +496,12 @@ def ds_softmax(x, temperature=None, out_dtype=None, out=None, workspace=None, st
     first maximum); see include/dstopk.h."""
     torch = _torch()
     rows, n, rs = _matrix(x, "x")
-    dt, dev = dtype_code(x), x.device
+    dt, dev = _code(x.dtype), x.device
     out, os = _out_rows(out, out_dtype, rows, n, dev)
     keep, ws, ws_bytes = _scratch(ds_softmax_workspace_size(rows, n, dt), workspace, dev, stream)
     _call("ds_softmax", dev, stream, x.data_ptr(), rows, n, rs, dt,
           None if temperature is None else _operand(temperature, "temperature", torch.float32, (rows,), dev),
-          out.data_ptr(), os, dtype_code(out), ws, ws_bytes)
+          out.data_ptr(), os, _code(out.dtype), ws, ws_bytes)
     return out
 
 
@@ -502,10 +516,10 @@ def ds_topk_softmax(vals, idx, n: int, ks=None, temperature=None, top_p=None, ou
     if vals.dim() != 2 or not vals.is_cuda or not vals.is_contiguous():
         raise ValueError("vals must be a contiguous 2-D device tensor [rows, k]")
     rows, k = shape = vals.shape
-    dt, dev, f32 = dtype_code(vals), vals.device, torch.float32
+    dt, dev, f32 = _code(vals.dtype), vals.device, torch.float32
     if rows_out:
         out, os = _out_rows(out, out_dtype, rows, n, dev)
-        op, odt = out.data_ptr(), dtype_code(out)
+        op, odt = out.data_ptr(), _code(out.dtype)
     else:
         op, os, odt = None, n, FP32
         if out_list is None:
@@ -530,7 +544,7 @@ def ds_verify(target, draft, draft_tokens, accept_u, sample_u, draft_lens=None, 
     """
     torch = _torch()
     batch, m, n, ts = _batch_rows(target, "target")
-    dt, dev, K = dtype_code(target), target.device, m - 1
+    dt, dev, K = _code(target.dtype), target.device, m - 1
     if K < 0:
         raise ValueError("target must hold at least one row per sequence")
     if sample_u is None or (K > 0 and (draft_tokens is None or accept_u is None)):

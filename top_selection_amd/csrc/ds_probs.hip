@@ -504,10 +504,13 @@ static RowCut cut_rows(int64_t rows, int64_t n) {
   return {slice, static_cast<int32_t>((n + slice - 1) / slice)};
 }
 
-// No slices (one workgroup per row, one launch) while a row is short or the rows fill the card
-// by themselves; else slices and two launches.
-RowCut cut_softmax(int64_t rows, int64_t n) {
-  if (n >= 8 && (n <= 32768 || rows >= 80)) return {0, 0};  // (a row kernel's vectors hold up to 8)
+// No slices (one workgroup per row, one launch) while a row is short or there are many; else
+// slices and two launches. Both sides, in us, called one after the other from the host: 7 rows
+// of 50001 bf16 9.8 and 11.6, 7 of 50001 fp32 11.4 and 12.0 (from a graph 11.6 and 8.2), 64 of
+// 129280 fp32 19.9 and 21.1, 100 of them 24 and 33, one of 16384 fp32 7.8 and 12.
+RowCut cut_softmax(int64_t rows, int64_t n, int dtype) {
+  const int64_t bytes = n * (dtype == DS_BF16 ? 2 : 4);
+  if (n >= 8 && (bytes <= 128 * 1024 || rows >= 48)) return {0, 0};  // (a row kernel's vectors hold up to 8)
   return cut_rows(rows, n);
 }
 

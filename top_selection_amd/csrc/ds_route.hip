@@ -16,7 +16,8 @@ __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > 
 
 // ------------------------------------------------------------------ the exact choice of a row
 // A whole wave chooses for one row with everything that decides in double; expert e is in lane
-// e % 64, room: exact_room(64 V) bytes of LDS, the wave's own. Rows that the fast kernel cannot
+// e % 64, lds: exact_room(64 V) bytes of LDS, the wave's own. groups_kept: 0, or the chosen
+// groups where they are known (group g's bit is g << groups_step). Rows that the fast kernel cannot
 // decide come here, and every row where no fast kernel fits. Out of line: its registers would
 // otherwise count against the fast kernel's, which seldom calls it. It reads the parameters
 // where the launch left them (a kernel's only argument), with scalar loads. A lone wave waits
@@ -48,7 +49,8 @@ __device__ __forceinline__ Top2 from_partner(Top2 v) {
 }
 
 template <int DT, int SCORE, int V>
-__device__ __noinline__ void route_row_exact(const void* params, int64_t row, uint8_t* lds) {
+__device__ __noinline__ void route_row_exact(const void* params, int64_t row, uint8_t* lds, uint64_t groups_kept,
+                                             int groups_step) {
   using E = Elem<DT>;
   typedef const __attribute__((address_space(4))) RouteParams* ScalarParams;
   const ScalarParams p = (ScalarParams)uniform(reinterpret_cast<uint64_t>(params));
@@ -59,7 +61,7 @@ __device__ __noinline__ void route_row_exact(const void* params, int64_t row, ui
   const bool two = p->group_top > 1, renorm = p->renorm != 0;
   const float scale = p->scale;
   float* const out_weights = p->out_weights;
-  int32_t *const out_idx = p->out_idx, *const counts = p->counts;
+  int32_t* const out_idx = p->out_idx;
   // (as LDS addresses: a generic pointer's accesses take longer)
   const auto room = (__attribute__((address_space(3))) double*)reinterpret_cast<double*>(lds);
   const auto room_at = (__attribute__((address_space(3))) int32_t*)(room + 64 * V);
@@ -104,13 +106,15 @@ __device__ __noinline__ void route_row_exact(const void* params, int64_t row, ui
     c[v] = xv[v] == kNegInf ? kNone
            : biases         ? s[v] + static_cast<double>(bias[v])
                             : static_cast<double>(xv[v]);
-  if (limited) {
+  uint64_t keep = uniform(groups_kept);
+  int levels = __builtin_amdgcn_readfirstlane(groups_step);
+  if (limited && keep == 0) {
     wave_sync();
 #pragma unroll
     for (int v = 0; v < V; ++v)
       if (v * 64 + lane < experts) room[v * 64 + lane] = sums && c[v] != kNone ? s[v] : c[v];
     wave_sync();
-    int levels = 6;  // 2^levels lanes share a group
+    levels = 6;  // 2^levels lanes share a group
     while ((64 >> levels) < groups) --levels;
     const int group = lane >> levels, part = lane & ((1 << levels) - 1);
     Top2 top = {kNone, kNone};
@@ -131,11 +135,14 @@ __device__ __noinline__ void route_row_exact(const void* params, int64_t row, ui
         const double other = __shfl(score, (o << levels) & 63);
         rank += (o < groups) & ((other > score) | ((other == score) & (o < group)));
       }
-    const uint64_t keep = __ballot(group < groups && rank < topk_groups);
+    keep = __ballot(group < groups && rank < topk_groups);
+  }
+  if (limited) {
+    const float per_group = 1.0f / static_cast<float>(size);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int e = v * 64 + lane;
-      if (e < experts && !((keep >> ((e / size) << levels)) & 1)) c[v] = kNone;
+      const int g = static_cast<int>((static_cast<float>(v * 64 + lane) + 0.5f) * per_group);
+      if (!((keep >> ((g << levels) & 63)) & 1)) c[v] = kNone;
     }
   }
   // A bound that at least k experts reach, the k-th largest of the lanes' best (everything, if
@@ -147,9 +154,15 @@ __device__ __noinline__ void route_row_exact(const void* params, int64_t row, ui
   wave_sync();
   lane_best[lane] = best;
   wave_sync();
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  const auto four_best = (const __attribute__((address_space(3))) f32x4*)lane_best;
   int above = 0;
-#pragma unroll 16
-  for (int o = 0; o < 64; ++o) above += lane_best[o] > best;
+#pragma unroll
+  for (int o = 0; o < 16; ++o) {
+    const f32x4 q = four_best[o];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) above += q[j] > best;
+  }
   const float bound = -row_reduce<6>(above < k ? -best : kNegInf, [](float a, float b) { return larger(a, b); });
   int listed = 0;
 #pragma unroll
@@ -166,18 +179,21 @@ __device__ __noinline__ void route_row_exact(const void* params, int64_t row, ui
   }
   wave_sync();
   int rank[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) rank[v] = 0;
+#pragma unroll 2
+  for (int o = 0; o < listed; ++o) {
+    const double other = room[o];
+    const int at = room_at[o];
+#pragma unroll
+    for (int v = 0; v < V; ++v) rank[v] += (other > c[v]) | ((other == c[v]) & (at < v * 64 + lane));
+  }
   double total = 0.0;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    rank[v] = k;
     const bool in = c[v] > kNone && static_cast<float>(c[v]) >= bound;
-    if (__any(in)) {
-      int n = 0;
-#pragma unroll 4
-      for (int o = 0; o < listed; ++o) n += (room[o] > c[v]) | ((room[o] == c[v]) & (room_at[o] < v * 64 + lane));
-      rank[v] = in ? n : k;
-      total += rank[v] < k ? s[v] : 0.0;
-    }
+    rank[v] = in ? rank[v] : k;
+    total += rank[v] < k ? s[v] : 0.0;
   }
   total = row_reduce<6>(total, plus<double>);
   const double factor = static_cast<double>(scale);
@@ -187,7 +203,6 @@ __device__ __noinline__ void route_row_exact(const void* params, int64_t row, ui
       const double w = !renorm ? s[v] : total > 0.0 ? s[v] / total : 0.0;
       if (out_weights) out_weights[r * k + rank[v]] = static_cast<float>(w * factor);
       if (out_idx) out_idx[r * k + rank[v]] = v * 64 + lane;
-      if (counts) atomicAdd(counts + v * 64 + lane, 1);
     }
   if (lane >= listed && lane < k) {  // slots that no expert is left for
     if (out_weights) out_weights[r * k + lane] = 0.0f;
@@ -196,13 +211,13 @@ __device__ __noinline__ void route_row_exact(const void* params, int64_t row, ui
   wave_sync();
 }
 
-template <int DT, int SCORE>
+template <int DT, int SCORE, int V>
 __global__ __launch_bounds__(kRouteWaves * 64) void route_exact_kernel(RouteParams p) {
-  __shared__ __attribute__((aligned(16))) uint8_t room[kRouteWaves][exact_room(DS_MAX_EXPERTS)];
+  __shared__ __attribute__((aligned(16))) uint8_t room[kRouteWaves][exact_room(64 * V)];
   const int wave = threadIdx.x >> 6;
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRouteWaves + wave; r < p.rows;
        r += static_cast<int64_t>(gridDim.x) * kRouteWaves)
-    route_row_exact<DT, SCORE, DS_MAX_EXPERTS / 64>(params_of_launch(), r, room[wave]);
+    route_row_exact<DT, SCORE, V>(params_of_launch(), r, room[wave], 0, 0);
 }
 
 // ------------------------------------------------------------------------- the fast kernel
@@ -276,8 +291,13 @@ __device__ __forceinline__ void merge_partner(uint32_t* list, uint32_t& dropped)
   merge_down<KP>(list, o, dropped);
 }
 
+// Waves a SIMD, and workgroups a CU: with 32 experts a lane, three waves' registers hold what
+// four spill (65536 x 256 fp32, k = 8: 26.5 and 29.9 us).
+template <int V, int KP>
+constexpr int kRouteOccupancy = V < 32 ? 4 : KP == 16 ? 2 : 3;
+
 template <int DT, int SCORE, int MODE, int L, int V, int KP>
-__global__ __launch_bounds__(kRouteWaves * 64, V == 32 && KP == 16 ? 3 : 4) void route_kernel(RouteParams p) {
+__global__ __launch_bounds__(kRouteWaves * 64, (kRouteOccupancy<V, KP>)) void route_kernel(RouteParams p) {
   using E = Elem<DT>;
   using T = typename E::T;
   constexpr int N = E::kPer16;
@@ -302,6 +322,10 @@ __global__ __launch_bounds__(kRouteWaves * 64, V == 32 && KP == 16 ? 3 : 4) void
   have = have > p.per_lane ? p.per_lane : have;
   if (group >= p.experts / p.run || have < 0) have = 0;
   const bool full = __ballot(have != V) == 0;
+  uint32_t apart = 0;  // vectors of which a lane holds only a part (or that a row is too short for)
+#pragma unroll
+  for (int v = 0; v < V; v += N)
+    if (p.experts < N || __any(v < have && have < v + N)) apart |= 1u << (v / N);
 
   // c = s + b as a key: (s + b - least b) * per_unit + 1; `steps` holds the bias' part by
   // position, and -inf (key 0) where there is no expert
@@ -354,13 +378,20 @@ __global__ __launch_bounds__(kRouteWaves * 64, V == 32 && KP == 16 ? 3 : 4) void
       int last = have > 0 ? first + have - 1 : 0;  // slots past the lane's experts load its last one
       asm("" : "+v"(last));                        // (not kept as one address per slot)
 #pragma unroll
-      for (int v = 0; v < V; ++v) ahead[v / N][v % N] = row[first + v < last ? first + v : last];
+      for (int v = 0; v < V; v += N) {
+        if (apart >> (v / N) & 1) {
+#pragma unroll
+          for (int j = 0; j < N; ++j) ahead[v / N][j] = row[first + v + j < last ? first + v + j : last];
+        } else {
+          ahead[v / N] = *reinterpret_cast<const typename Vec<DT, N>::unaligned*>(row + (first + v < last ? first + v : 0));
+        }
+      }
     }
   };
   // Turns are taken 64 at a time; lane i keeps which rows of turn i need the exact choice.
   for (int64_t turn0 = first_row; turn0 < p.rows; turn0 += 64 * row_step) {
   fetch(turn0);
-  uint64_t left = 0;
+  uint64_t left = 0, left_kept = 0, left_open = 0;
   int turn = 0;
   for (int64_t r0 = turn0; turn < 64 && r0 < p.rows; r0 += row_step, ++turn) {
     const int64_t r = r0 + lane / L < p.rows ? r0 + lane / L : p.rows - 1;
@@ -450,9 +481,11 @@ __global__ __launch_bounds__(kRouteWaves * 64, V == 32 && KP == 16 ? 3 : 4) void
       merge_down<KP>(list, o, dropped);
     }
     bool close = undecided || (MODE == kByLogit && m == __builtin_huge_valf());
+    bool unsure = false;  // the choice of groups is close
+    uint64_t kept = 0;    // lanes whose group was chosen
     const auto rank_groups = [&](auto level) {  // of the lists of 2^level lanes
       const uint32_t a = list[0] >> IB, b = list[1] >> IB;
-      close |= p.group_top > 1 && a != 0u && b == 0u;  // a sum of one: not comparable in steps
+      unsure |= p.group_top > 1 && a != 0u && b == 0u;  // a sum of one: not comparable in steps
       const uint32_t sum = p.group_top > 1 ? a + b : a;
       const uint32_t mine = (sum << 6) | static_cast<uint32_t>(63 - group);
       int rank = 0;  // (lanes without a group have the smallest keys)
@@ -463,7 +496,9 @@ __global__ __launch_bounds__(kRouteWaves * 64, V == 32 && KP == 16 ? 3 : 4) void
       const auto least = [](uint32_t u, uint32_t w) { return u < w ? u : w; };
       const uint32_t in = row_reduce<LEVELS>(out ? 0xFFFFFFFFu : sum, least);
       const uint32_t over = row_reduce<LEVELS>(out ? sum : 0u, [](uint32_t u, uint32_t w) { return larger(u, w); });
-      close |= over != 0u && static_cast<int>(in - over) <= (p.group_top > 1 ? 2 * kSlack : kSlack);
+      unsure |= over != 0u && static_cast<int>(in - over) <= (p.group_top > 1 ? 2 * kSlack : kSlack);
+      close |= unsure;
+      kept = __ballot(!out);
       dropped = out ? 0u : dropped;
 #pragma unroll
       for (int i = 0; i < KP; ++i) list[i] = out ? 0u : list[i];
@@ -537,23 +572,47 @@ __global__ __launch_bounds__(kRouteWaves * 64, V == 32 && KP == 16 ? 3 : 4) void
       if (mine && !close && j < p.k) {
         if (p.out_weights) p.out_weights[r * p.k + j] = s[t] * factor;
         if (p.out_idx) p.out_idx[r * p.k + j] = at[t];
-        if (p.counts && at[t] >= 0) atomicAdd(p.counts + at[t], 1);
       }
     }
-    const uint64_t rest = __ballot(mine && close && sub == 0);
-    if (lane == turn) left = rest;
+    const uint64_t rest = __ballot(mine && close && sub == 0), open = __ballot(unsure);
+    if (lane == turn) left = rest, left_kept = kept, left_open = open;
   }
   if (__any(left != 0)) {
     for (int t = 0; t < turn; ++t) {
       uint64_t rest = __shfl(left, t);
+      const uint64_t kept = __shfl(left_kept, t), open = __shfl(left_open, t);
       while (rest) {
         const int l = __builtin_ctzll(rest);
         rest &= rest - 1;
-        route_row_exact<DT, SCORE, L * V / 64>(params_of_launch(), turn0 + t * row_step + l / L, room[wave]);
+        constexpr uint64_t kLanes = (uint64_t{1} << L) - 1;
+        const bool known = (open >> l & kLanes) == 0;
+        route_row_exact<DT, SCORE, L * V / 64>(params_of_launch(), turn0 + t * row_step + l / L, room[wave],
+                                               known ? kept >> l & kLanes : 0, p.lanes_log2);
       }
     }
   }
   }
+}
+
+// The experts' loads, from the chosen indices: few workgroups count in LDS and add once an expert
+// each. (Adding from the routing itself, 524288 atomics on 256 counters, took 320 us: an
+// address takes one add every 0.17 us or so from the card's several L2 caches.)
+constexpr int kCountThreads = 1024, kCountGroups = 32;
+
+__global__ __launch_bounds__(kCountThreads) void route_counts_kernel(const int32_t* idx, int64_t n, int32_t* counts,
+                                                                     int32_t experts) {
+  __shared__ int32_t of_expert[DS_MAX_EXPERTS];
+  for (int e = threadIdx.x; e < experts; e += kCountThreads) of_expert[e] = 0;
+  __syncthreads();
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kCountThreads;
+#pragma unroll 4
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kCountThreads + threadIdx.x; i < n; i += step) {
+    const int32_t e = idx[i];
+    if (e >= 0) atomicAdd(&of_expert[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < experts; e += kCountThreads)
+    if (of_expert[e]) atomicAdd(counts + e, of_expert[e]);
 }
 
 // ------------------------------------------------------------------------------ the gradient
@@ -735,10 +794,13 @@ uint32_t route_grid(int64_t rows, int64_t rows_per_group, int64_t per_cu) {
 
 template <int DT, int SCORE, int MODE, int L, int V>
 hipError_t route_shape(const RouteParams& p, hipStream_t s) {
-  const dim3 g(route_grid(p.rows, kRouteWaves * (64 / L), 4)), b(kRouteWaves * 64);
-  if (p.k <= 8) hipLaunchKernelGGL((route_kernel<DT, SCORE, MODE, L, V, 8>), g, b, 0, s, p);
-  else hipLaunchKernelGGL((route_kernel<DT, SCORE, MODE, L, V, 16>), g, b, 0, s, p);
-  return hipGetLastError();
+  const auto go = [&](auto kern, int per_cu) {
+    const dim3 g(route_grid(p.rows, kRouteWaves * (64 / L), per_cu)), b(kRouteWaves * 64);
+    hipLaunchKernelGGL(kern, g, b, 0, s, p);
+    return hipGetLastError();
+  };
+  if (p.k <= 8) return go(route_kernel<DT, SCORE, MODE, L, V, 8>, kRouteOccupancy<V, 8>);
+  return go(route_kernel<DT, SCORE, MODE, L, V, 16>, kRouteOccupancy<V, 16>);
 }
 
 template <int DT, int SCORE, int MODE>
@@ -766,7 +828,9 @@ hipError_t route_mode(RouteParams p, hipStream_t s) {
     }
     return route_shape<DT, SCORE, MODE, 32, 32>(p, s);
   }
-  hipLaunchKernelGGL((route_exact_kernel<DT, SCORE>), dim3(route_grid(p.rows, kRouteWaves, 4)), dim3(kRouteWaves * 64), 0, s, p);
+  const dim3 g(route_grid(p.rows, kRouteWaves, 4)), b(kRouteWaves * 64);
+  if (p.experts <= 256) hipLaunchKernelGGL((route_exact_kernel<DT, SCORE, 4>), g, b, 0, s, p);
+  else hipLaunchKernelGGL((route_exact_kernel<DT, SCORE, DS_MAX_EXPERTS / 64>), g, b, 0, s, p);
   return hipGetLastError();
 }
 
@@ -807,7 +871,12 @@ hipError_t grad_softmax(const RouteGradParams& p, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_route(int dtype, int score, const RouteParams& p, hipStream_t s) {
-  return dtype == DS_BF16 ? route_dt<DS_BF16>(score, p, s) : route_dt<DS_FP32>(score, p, s);
+  const hipError_t e = dtype == DS_BF16 ? route_dt<DS_BF16>(score, p, s) : route_dt<DS_FP32>(score, p, s);
+  if (e != hipSuccess || !p.counts) return e;
+  const int64_t n = p.rows * p.k, need = (n + 4 * kCountThreads - 1) / (4 * kCountThreads);
+  hipLaunchKernelGGL(route_counts_kernel, dim3(static_cast<uint32_t>(need < kCountGroups ? need : kCountGroups)),
+                     dim3(kCountThreads), 0, s, p.out_idx, n, p.counts, p.experts);
+  return hipGetLastError();
 }
 
 hipError_t launch_route_grad(int dtype, int score, const RouteGradParams& p, hipStream_t s) {

@@ -114,7 +114,7 @@ struct RowCut {
   int64_t slice;
   int32_t slices;
 };
-RowCut cut_softmax(int64_t rows, int64_t n);
+RowCut cut_softmax(int64_t rows, int64_t n, int dtype);
 RowCut cut_list_softmax(int64_t rows, int64_t n);
 
 // How sequences are cut for the verification: `slices` workgroups of `slice` units each, and

@@ -55,7 +55,7 @@ int ds_route(const void* x, int64_t rows, int64_t experts, int64_t row_stride, i
   ds_route_config c;
   const int st = check_route(rows, experts, row_stride, k, dtype, cfg, &c);
   if (st != DS_OK || rows == 0) return st;
-  if (!x || (!out_weights && !out_idx)) return DS_ERR_INVALID_ARG;
+  if (!x || (!out_weights && !out_idx) || (counts && !out_idx)) return DS_ERR_INVALID_ARG;
   if (misaligned(x, elem_bytes(dtype)) || misaligned(bias, 4) || misaligned(out_weights, 4) || misaligned(out_idx, 4) ||
       misaligned(counts, 4))
     return DS_ERR_ALIGNMENT;
@@ -109,7 +109,7 @@ int ds_route_grad(const void* x, int64_t rows, int64_t experts, int64_t row_stri
 
 int ds_softmax_workspace_size(int64_t rows, int64_t n, int dtype, size_t* bytes) {
   if (!bytes || !known(dtype) || !rows_ok(rows, n, n)) return DS_ERR_INVALID_ARG;
-  *bytes = softmax_bytes(rows, ds::cut_softmax(rows, n));
+  *bytes = softmax_bytes(rows, ds::cut_softmax(rows, n, dtype));
   return DS_OK;
 }
 
@@ -121,7 +121,7 @@ int ds_softmax(const void* x, int64_t rows, int64_t n, int64_t row_stride, int d
   if (!x || !out) return DS_ERR_INVALID_ARG;
   if (misaligned(x, elem_bytes(dtype)) || misaligned(out, elem_bytes(out_dtype)) || misaligned(temperature, 4))
     return DS_ERR_ALIGNMENT;
-  const ds::RowCut c = ds::cut_softmax(rows, n);
+  const ds::RowCut c = ds::cut_softmax(rows, n, dtype);
   const int st = check_workspace(workspace, ws_bytes, softmax_bytes(rows, c));
   if (st != DS_OK) return st;
   (void)hipGetLastError();
