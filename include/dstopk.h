@@ -396,7 +396,8 @@ int ds_softmax_workspace_size(int64_t rows, int64_t n, int dtype, size_t* bytes)
 
 /*
  * ds_topk_softmax -- ds_softmax restricted to a row's top-k list, as a whole row and as a list.
- *   The list (vals, idx) is ds_topk's: sorted by value, larger first, padded with index -1.
+ *   The list (vals, idx) is ds_topk's: sorted by value, larger first, distinct indices, padded
+ *   with index -1.
  *   Row r uses its first ks[r] entries (clamped to [1, k]); top_p keeps the shortest prefix
  *   of those whose mass reaches top_p[r] of theirs (at least one entry); the kept entries'
  *   probabilities sum to 1. Temperatures and infinities as in ds_softmax. The prefix is

@@ -73,7 +73,8 @@ ROUTES = [  # rows, experts, k, groups, topk_groups, group_top
     (1, 1, 1, 1, 1, 1), (3, 2, 2, 1, 1, 1), (5, 7, 3, 1, 1, 1), (4, 64, 64, 1, 1, 1), (37, 61, 6, 1, 1, 1),
     (33, 256, 8, 8, 4, 2), (64, 160, 6, 8, 3, 1), (9, 63, 5, 3, 2, 2), (17, 384, 9, 1, 1, 1), (6, 1024, 64, 64, 32, 2),
     (5, 1000, 10, 8, 1, 2), (11, 512, 16, 64, 5, 1), (130, 16, 4, 16, 8, 1), (2, 130, 20, 2, 2, 2), (3, 8, 2, 4, 1, 2),
-    (66, 32, 5, 4, 2, 2), (21, 128, 1, 1, 1, 1), (19, 100, 12, 5, 3, 2),
+    (66, 32, 5, 4, 2, 2), (21, 128, 1, 1, 1, 1), (19, 100, 12, 5, 3, 2), (40, 384, 8, 8, 4, 2), (7, 300, 9, 6, 3, 2),
+    (9, 96, 8, 32, 9, 2), (5, 600, 7, 1, 1, 1), (3, 250, 24, 10, 4, 1), (12, 3, 3, 1, 1, 1),
 ]
 
 
@@ -249,6 +250,45 @@ def test_softmax_matches_definition(rows, n, dtype, odt):
             want = orc.softmax(_np(x), None if temp is None else _np(temp))
             assert p.dtype == DT[odt]
             _close(p, want, f"softmax {rows}x{n} {dtype}->{odt} {kind} t={temp is not None}", bf16=odt == "bf16")
+
+
+def test_softmax_extreme_temperatures_spread_or_keep_the_mass():
+    """An infinite temperature is uniform over what is not masked; a NaN one counts as not above 0."""
+    x = torch.randn(3, 20000, generator=_gen(9))
+    x[:, ::4] = NEG
+    t = torch.tensor([float("inf"), float("nan"), 1e30])
+    want = np.where(np.isinf(x.double().numpy()), 0, 1 / 15000)
+    for n in (20000, 40000):  # in one workgroup, in slices
+        y = torch.full((3, n), NEG)
+        y[:, :20000] = x
+        p = _np(ts.ds_softmax(y.cuda(), temperature=t.cuda()))
+        assert np.abs(p[[0, 2], :20000] - want[[0, 2]]).max() < 1e-8 and not p[:, 20000:].any()
+        assert p[1].sum() == 1 and p[1].argmax() == int(x[1].argmax())
+    v, i = x.sort(dim=1, descending=True)
+    q = _np(ts.ds_topk_softmax(v[:, :4000].contiguous().cuda(), i[:, :4000].to(torch.int32).contiguous().cuda(), 20000,
+                               temperature=t.cuda()))
+    assert np.abs(q.max(axis=1) - [1 / 4000, 1, 1 / 4000]).max() < 1e-8
+
+
+def test_more_rows_than_a_launch_takes():
+    """Rows past the workgroups of one launch, and routing past the turns that a wave keeps."""
+    rows = (1 << 22) + 5
+    x = torch.randn(rows, 3, generator=_gen(2)).to(torch.bfloat16).cuda()
+    p = ts.ds_softmax(x)
+    assert (p - torch.softmax(x.float(), dim=1)).abs().max() < 1e-6
+    v, i = ts.ds_topk_softmax, torch.arange(3, dtype=torch.int32, device="cuda").repeat(rows, 1)
+    s = x.float().sort(dim=1, descending=True)
+    assert torch.equal(v(s[0].to(torch.bfloat16), s[1].to(torch.int32), 3) > 0, p > 0)
+    got, acc = ts.ds_verify(p.view(rows, 1, 3), None, None, None, torch.zeros(rows, device="cuda"))
+    assert not got.any() and not acc.any()  # the first element that has mass
+    y = torch.randn(rows, 8, generator=_gen(3)).cuda()
+    y[-4000::3, 5] = y[-4000::3, 2]  # ties: decided in double
+    bias = torch.tensor([0.1, 0.0, 0.2, -0.1, 0.05, 0.2, 0.0, 0.0]).cuda()
+    w, e = ts.ds_route(y, 2, bias=bias, score=ts.SCORE_SIGMOID, renormalize=True)
+    pick = torch.cat([torch.arange(0, rows, 9001), torch.arange(rows - 4000, rows)])
+    ww, we = orc.route(_np(y[pick.cuda()]), 2, _np(bias), score="sigmoid", renormalize=True)
+    assert np.array_equal(_np(e[pick.cuda()]), we)
+    _close(w[pick.cuda()], ww, "many turns")
 
 
 @pytest.mark.parametrize("off", [0, 1, 3])

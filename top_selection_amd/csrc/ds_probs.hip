@@ -33,7 +33,7 @@ __device__ __forceinline__ float2 wave_xor(float2 v, int o) {
 __device__ __forceinline__ float row_scale(const float* temperature, int64_t r, bool* greedy) {
   const float t = temperature ? temperature[r] : 1.0f;
   *greedy = !(t > 0.0f);
-  return *greedy ? 0.0f : kLog2E / t;
+  return *greedy ? 0.0f : fmaxf(kLog2E / t, 1e-37f);  // (above 0 at an infinite temperature: -inf keeps no mass)
 }
 
 // One workgroup per (row, slice): the slice's maximum and sum.
@@ -420,8 +420,8 @@ __global__ __launch_bounds__(kListThreads) void list_softmax_kernel(ListSoftmaxP
   }
   const typename E::T* vals = static_cast<const typename E::T*>(p.vals) + r * p.k;
   const int32_t* idx = p.idx + r * p.k;
-  const float t = p.temperature ? p.temperature[r] : 1.0f;
-  const bool greedy = !(t > 0.0f);
+  const float t = p.temperature ? fminf(p.temperature[r], 1e37f) : 1.0f;
+  const bool greedy = p.temperature && !(p.temperature[r] > 0.0f);
   int used = p.ks ? p.ks[r] : p.k;
   used = used < 1 ? 1 : (used > p.k ? p.k : used);
   const int per = (p.k + kListThreads - 1) / kListThreads;

@@ -106,8 +106,9 @@ hipError_t launch_verify(int dtype, VerifyParams p, hipStream_t s);
 // The compute units that a launch is sized for (MI355X).
 constexpr int64_t kCus = 256;
 
-// The most workgroups of a launch; longer work is launched in turns (`unit0` on).
-constexpr int64_t kMaxUnits = 1 << 22;
+// The most workgroups of a launch (of at most 1024 threads: a grid holds fewer than 2^32);
+// longer work is launched in turns (`unit0` on).
+constexpr int64_t kMaxUnits = 1 << 21;
 
 // How a row of n elements is cut: `slices` workgroups of `slice` elements each.
 struct RowCut {
