@@ -343,7 +343,8 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
     typename W::type o;
 #pragma unroll
     for (int j = 0; j < N; ++j) o[j] = O::narrow(q[j]);
-    *reinterpret_cast<typename W::unaligned*>(out + i) = o;
+    // (past the caches, which keep more of the logits: 50.1 -> 48.8 us for 256 x 129280 fp32)
+    __builtin_nontemporal_store(o, reinterpret_cast<typename W::unaligned*>(out + i));
   };
 #pragma unroll
   for (int j = 0; j < R; ++j)

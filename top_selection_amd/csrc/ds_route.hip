@@ -619,7 +619,7 @@ __global__ __launch_bounds__(kCountThreads) void route_counts_kernel(const int32
 // A wave keeps a tile of rows in LDS, all zero between turns: slots are added at their
 // experts, lanes read the tile in memory's order and the slots clear what they added. Indices
 // are checked before they are used as places.
-constexpr int kGradTile = 2048;  // floats of a wave's tile
+constexpr int kGradTile = 1024;  // floats of a wave's tile (twice as many: 17.0 -> 17.6 us for 65536 x 256 fp32)
 
 // The chosen experts' gradients only (all others are zero): KL lanes a row, slot j in lane
 // j % KL; x is read at the chosen experts.
@@ -691,7 +691,8 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_grad_chosen_kernel(Rou
         typename Vec<DT, N>::type q;
 #pragma unroll
         for (int j = 0; j < N; ++j) q[j] = E::narrow(from[j]);
-        *reinterpret_cast<typename Vec<DT, N>::unaligned*>(to) = q;
+        // (past the caches: 19.2 -> 17.4 us for 65536 x 256 fp32, 25.6 -> 17.9 from a graph)
+        __builtin_nontemporal_store(q, reinterpret_cast<typename Vec<DT, N>::unaligned*>(to));
       } else {
         for (int j = 0; at + j < p.experts; ++j) to[j] = E::narrow(from[j]);
       }

@@ -12,6 +12,7 @@ constexpr int kVerifyLoads = 4;  // 16-byte loads of each row that a lane has in
 // found from the units' sums and by reading one unit again.
 template <int DT>
 constexpr int kVerifyUnit = 64 * Elem<DT>::kPer16 * kVerifyLoads;  // 1024 fp32 or 2048 bf16 elements
+constexpr int kVerifyShort = 32;       // units of a row that counts as short
 constexpr int kVerifyLdsUnits = 2048;  // units of a row that one workgroup draws from alone
 
 // What the acceptance tests of a sequence decide; the same in every lane.
@@ -66,21 +67,30 @@ struct Rows {
     without = refused && !v.draft ? d.token : -1;
   }
 
+  // kOnce: past the caches, for rows that are long and read once (256 x 129280 fp32 45 -> 41 us;
+  // short rows are better kept for the draw, 48 x 32003 bf16 10.8 and 11.4 us).
+  template <bool kOnce>
+  static __device__ __forceinline__ typename V::type load(const T* from) {
+    const auto at = reinterpret_cast<const typename V::unaligned*>(from);
+    if constexpr (kOnce) return __builtin_nontemporal_load(at);
+    else return *at;
+  }
+
   // The masses of the lane's elements of a unit, in vectors `step` elements apart from the
   // lane's first, unit + lane * first on. Elements past n have none. The difference of two fp32 is
   // taken in double: it is the sums' terms that must not be rounded to fp32.
-  template <int kFirst, int kStep>
+  template <int kFirst, int kStep, bool kOnce = false>
   __device__ __forceinline__ void masses(int64_t unit, int64_t n, int lane, double (&m)[kVerifyLoads][N]) const {
     typename V::type pv[kVerifyLoads], qv[kVerifyLoads];
     const int64_t at = unit + lane * kFirst;
     if (unit + kVerifyUnit<DT> <= n) {
 #pragma unroll
       for (int u = 0; u < kVerifyLoads; ++u)
-        pv[u] = *reinterpret_cast<const typename V::unaligned*>(p + at + u * kStep);
+        pv[u] = load<kOnce>(p + at + u * kStep);
       if (q) {
 #pragma unroll
         for (int u = 0; u < kVerifyLoads; ++u)
-          qv[u] = *reinterpret_cast<const typename V::unaligned*>(q + at + u * kStep);
+          qv[u] = load<kOnce>(q + at + u * kStep);
       }
     } else {
 #pragma unroll
@@ -109,9 +119,10 @@ struct Rows {
       }
   }
 
+  template <bool kOnce>
   __device__ __forceinline__ double sum(int64_t unit, int64_t n, int lane) const {
     double m[kVerifyLoads][N], t = 0.0;
-    masses<N, 64 * N>(unit, n, lane, m);  // in memory's order
+    masses<N, 64 * N, kOnce>(unit, n, lane, m);  // in memory's order
 #pragma unroll
     for (int u = 0; u < kVerifyLoads; ++u)
 #pragma unroll
@@ -214,9 +225,16 @@ __device__ __forceinline__ void draw_alone(const VerifyParams& p, int64_t b, Ver
   const int units = static_cast<int>((p.n + kVerifyUnit<DT> - 1) / kVerifyUnit<DT>);
   double total = 0.0;
   for (int turn = 0; turn < 2; ++turn) {
-    for (int i = wave; i < units; i += kVerifyWaves) {
-      const double s = rows.sum(static_cast<int64_t>(i) * kVerifyUnit<DT>, p.n, lane);
-      if (lane == 0) sums[i] = s;
+    if (units > kVerifyShort) {
+      for (int i = wave; i < units; i += kVerifyWaves) {
+        const double s = rows.template sum<true>(static_cast<int64_t>(i) * kVerifyUnit<DT>, p.n, lane);
+        if (lane == 0) sums[i] = s;
+      }
+    } else {
+      for (int i = wave; i < units; i += kVerifyWaves) {
+        const double s = rows.template sum<false>(static_cast<int64_t>(i) * kVerifyUnit<DT>, p.n, lane);
+        if (lane == 0) sums[i] = s;
+      }
     }
     __syncthreads();
     total = sum_units(sums, units, lane);
@@ -254,7 +272,7 @@ __global__ __launch_bounds__(kVerifyThreads) void verify_sums_kernel(VerifyParam
   const int64_t lo = sl * p.slice, hi = lo + p.slice < units ? lo + p.slice : units;
   if (sl == 0 && threadIdx.x == 0) p.verdicts[b] = make_int2(d.len | d.next << 16, d.token);
   for (int64_t i = lo + wave; i < hi; i += kVerifyWaves) {
-    const double s = rows.sum(i * kVerifyUnit<DT>, p.n, lane);
+    const double s = rows.template sum<false>(i * kVerifyUnit<DT>, p.n, lane);
     if (lane == 0) p.part[b * units + i] = s;
   }
 }
@@ -295,11 +313,13 @@ hipError_t verify_dt(const VerifyParams& p, hipStream_t s) {
 }  // namespace
 
 // No slices (one workgroup per sequence, one launch) while a row is short or the sequences fill
-// the card by themselves; else slices of whole units.
+// the card by themselves; else slices of whole units. Both sides: one sequence of 129280 fp32 in
+// one workgroup 18 us, in slices 8.7 (15 and 18 from the host, which then waits for neither);
+// 256 sequences 41 and 49 us.
 VerifyCut cut_verify(int64_t batch, int64_t n, int dtype) {
   const int64_t unit = dtype == DS_BF16 ? kVerifyUnit<DS_BF16> : kVerifyUnit<DS_FP32>;
   const int64_t units = (n + unit - 1) / unit;
-  if (units <= 32 || (batch >= 64 && units <= kVerifyLdsUnits)) return {0, 0, 0};
+  if (units <= kVerifyShort || (batch >= 64 && units <= kVerifyLdsUnits)) return {0, 0, 0};
   const int64_t want = batch >= kCus ? 1 : (kCus + batch - 1) / (batch < 1 ? 1 : batch);
   int64_t slice = (units + want - 1) / want;
   slice = (slice + kVerifyWaves - 1) / kVerifyWaves * kVerifyWaves;
