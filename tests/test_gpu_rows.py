@@ -252,6 +252,20 @@ def test_softmax_matches_definition(rows, n, dtype, odt):
             _close(p, want, f"softmax {rows}x{n} {dtype}->{odt} {kind} t={temp is not None}", bf16=odt == "bf16")
 
 
+@pytest.mark.parametrize("rows,n", [(50, 130001), (48, 140003), (49, 40000)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_softmax_long_rows(rows, n, dtype):
+    """Rows past what a workgroup holds on chip, with and without a temperature."""
+    t = 0.5 + torch.rand(rows, generator=_gen(rows))
+    t[1::5] = 0.0
+    t[2] = 1e-40
+    for kind in ("normal", "inf", "masked", "ties"):
+        x = _logits(n, rows, n, DT[dtype], kind)
+        p = ts.ds_softmax(x, temperature=t.cuda())
+        want = orc.softmax(_np(x), _np(t))
+        _close(p, want, f"softmax {rows}x{n} {dtype} {kind}")
+
+
 def test_softmax_extreme_temperatures_spread_or_keep_the_mass():
     """An infinite temperature is uniform over what is not masked; a NaN one counts as not above 0."""
     x = torch.randn(3, 20000, generator=_gen(9))
@@ -336,6 +350,29 @@ def test_list_softmax_matches_definition(rows, n, k, dtype, odt):
         _close(only, orc.list_softmax(_np(vals), _np(idx), n)[1], "list only")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_list_softmax_many_long_rows(dtype):
+    """Rows whose clearing takes longer than their list."""
+    rows, n, k = 520, 66001, 40
+    x = _logits(12, rows, 400, DT[dtype], "ties")
+    vals, at = x.sort(dim=1, descending=True, stable=True)
+    vals = vals[:, :k].contiguous()
+    idx = (at[:, :k] * 165 + torch.arange(rows, device="cuda")[:, None] % 165).to(torch.int32).contiguous()
+    g = _gen(4)
+    ks = torch.randint(1, k + 1, (rows,), generator=g, dtype=torch.int32)
+    t, top_p = 0.5 + torch.rand(rows, generator=g), torch.rand(rows, generator=g)
+    t[::7] = 0.0
+    idx[5, 3:] = -1
+    lists = torch.empty(rows, k, device="cuda")
+    p = ts.ds_topk_softmax(vals, idx, n, ks=ks.cuda(), temperature=t.cuda(), top_p=top_p.cuda(), out_dtype=DT[dtype],
+                           out_list=lists)
+    _, want = orc.list_softmax(_np(vals), _np(idx), n, _np(ks), _np(t), _np(top_p))
+    _close(lists, want, "long rows")
+    got = torch.gather(p.float(), 1, idx.clamp(min=0).long())
+    _close(torch.where(idx < 0, 0, got), want, "long rows", bf16=dtype == "bf16")
+    assert ((p != 0).sum(dim=1).cpu() == torch.from_numpy((want > 0).sum(axis=1))).all()
+
+
 def test_list_softmax_padding_and_ragged_rows():
     """ds_topk_ex's padding (index -1, a NaN pattern as value) has no mass; an empty list gives zeros."""
     x = torch.randn(4, 1000, generator=_gen(1)).cuda()
@@ -374,7 +411,8 @@ def _check_verify(target, draft, tokens, u, v, lens=None, label=""):
 
 
 @pytest.mark.parametrize("batch,K,n", [(1, 0, 1), (1, 1, 2), (3, 2, 17), (2, 3, 4096), (5, 1, 12289), (40, 4, 1000),
-                                       (1, 64, 300), (3, 7, 32003), (300, 2, 257), (2, 2, 129280)])
+                                       (1, 64, 300), (3, 7, 32003), (300, 2, 257), (2, 2, 129280),
+                                       (66, 1, 70001)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_verify_matches_definition(batch, K, n, dtype):
     for kind in ("probs", "sparse"):

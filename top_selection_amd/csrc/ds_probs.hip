@@ -377,129 +377,153 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
   }
 }
 
-// One workgroup per (row, slice of the output): every workgroup of a row computes the list's
-// probabilities (at most 4096 entries, in double: the prefix's end is exact), clears its
-// slice and writes the entries that fall in it.
+// One workgroup per (row, slice of the output): every workgroup of a row works out the list's
+// probabilities (in double: the prefix's end is exact), clears its slice and writes the
+// entries that fall in it. Where a slice takes longer to clear than a short list takes one wave,
+// one wave works on the list while the others clear (LW = 1: a wave's loads wait for its own
+// earlier stores, so that all doing both took 22 us where the clearing of 256 x 129280 fp32
+// takes 17.4; this way 19.0). Elsewhere all waves share the list and clear after it (one list
+// of 512: 5.8 us, by one wave 7.4).
 constexpr int kListWaves = 8;
 constexpr int kListThreads = kListWaves * 64;
+constexpr int kOneWaveList = 512;
+constexpr int64_t kOneWaveBytes = 128 * 1024;
 
-template <class T>
-__device__ __forceinline__ T block_sum(T v, T* of_wave) {  // of_wave: kListWaves words of LDS
-  v = wave_sum(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) of_wave[threadIdx.x >> 6] = v;
-  __syncthreads();
-  T t = 0;
-  for (int w = 0; w < kListWaves; ++w) t += of_wave[w];
-  return t;
-}
-
-template <int DT, int OT>
+template <int DT, int OT, int LW>
 __global__ __launch_bounds__(kListThreads) void list_softmax_kernel(ListSoftmaxParams p) {
   using E = Elem<DT>;
   using O = Elem<OT>;
-  constexpr int kPer = DS_MAX_K / kListThreads;  // entries per thread, consecutive
-  __shared__ double of_wave[kListWaves];
-  __shared__ int first_of_wave[kListWaves];
+  constexpr int kPer = (LW == 1 ? kOneWaveList : DS_MAX_K) / (LW * 64);  // entries per thread, consecutive
+  __shared__ double of_wave[LW];
+  __shared__ int first_of_wave[LW];
   const int64_t unit = p.unit0 + blockIdx.x;
   const int64_t r = unit / p.slices;
   const int sl = static_cast<int>(unit - r * p.slices);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  // the zeros first: they are on their way while the list is worked on
   const int64_t lo = sl * p.slice, hi = lo + p.slice < p.n ? lo + p.slice : p.n;
   typename O::T* out = static_cast<typename O::T*>(p.out) + r * p.out_stride;
   constexpr int N = O::kPer16;
   using W = Vec<OT, N>;
-  if (p.out) {
-    for (int64_t i = lo + static_cast<int64_t>(threadIdx.x) * N; i < hi; i += kListThreads * N) {
+  const auto clear = [&](int thread, int threads) {
+    for (int64_t i = lo + static_cast<int64_t>(thread) * N; i < hi; i += threads * N) {
       if (i + N <= hi) {
         *reinterpret_cast<typename W::unaligned*>(out + i) = typename W::type(0);
       } else {
         for (int j = 0; i + j < hi; ++j) out[i + j] = O::narrow(0.0f);
       }
     }
-  }
-  const typename E::T* vals = static_cast<const typename E::T*>(p.vals) + r * p.k;
-  const int32_t* idx = p.idx + r * p.k;
-  const float t = p.temperature ? fminf(p.temperature[r], 1e37f) : 1.0f;
-  const bool greedy = p.temperature && !(p.temperature[r] > 0.0f);
-  int used = p.ks ? p.ks[r] : p.k;
-  used = used < 1 ? 1 : (used > p.k ? p.k : used);
-  const int per = (p.k + kListThreads - 1) / kListThreads;
-  const int base = threadIdx.x * per;
-  float v[kPer];
-  int at[kPer];
-  int first = p.k;  // the first entry that names an element: the list's maximum
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int i = base + j;
-    const bool live = j < per && i < used;
-    at[j] = live ? idx[i] : -1;
-    v[j] = live ? E::widen(vals[i]) : 0.0f;
-    if (at[j] < 0 || at[j] >= p.n) at[j] = -1;
-    if (at[j] >= 0 && first == p.k) first = i;
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const int b = __shfl_xor(first, o);
-    first = b < first ? b : first;
-  }
-  if (lane == 0) first_of_wave[wave] = first;
-  __syncthreads();
-  for (int w = 0; w < kListWaves; ++w) first = first_of_wave[w] < first ? first_of_wave[w] : first;
-  const float m = first < p.k ? E::widen(vals[first]) : kNegInf;
-  double e[kPer];
-  double mine = 0.0;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const bool live = at[j] >= 0 && m != kNegInf && (!greedy || base + j == first);
-    e[j] = !live ? 0.0
-           : v[j] == m ? 1.0
-                       : exp((static_cast<double>(v[j]) - static_cast<double>(m)) / static_cast<double>(t));
-    mine += e[j];
-  }
-  double total = block_sum(mine, of_wave);
-  if (p.top_p) {
-    // the mass before each entry: the waves before this one, the lanes before this one, then
-    // this thread's own entries
-    double before = mine;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const double b = __shfl_up(before, o);
-      if (lane >= o) before += b;
+  };
+  // sums and minima over the waves that have the list
+  const auto all_sum = [&](double v) {
+    v = wave_sum(v);
+    if constexpr (LW > 1) {
+      __syncthreads();
+      if (lane == 0) of_wave[wave] = v;
+      __syncthreads();
+      v = 0.0;
+      for (int w = 0; w < LW; ++w) v += of_wave[w];
     }
-    before -= mine;
-    for (int w = 0; w < wave; ++w) before += of_wave[w];
-    const double most = static_cast<double>(p.top_p[r]) * total;
-    mine = 0.0;
+    return v;
+  };
+  double e[kPer];
+  int at[kPer];
+  double inv = 0.0;
+  const int per = (p.k + LW * 64 - 1) / (LW * 64);
+  const int base = threadIdx.x * per;
+  if (LW > 1 || wave == 0) {
+    const typename E::T* vals = static_cast<const typename E::T*>(p.vals) + r * p.k;
+    const int32_t* idx = p.idx + r * p.k;
+    const float t = p.temperature ? fminf(p.temperature[r], 1e37f) : 1.0f;
+    const bool greedy = p.temperature && !(p.temperature[r] > 0.0f);
+    const float top_p = p.top_p ? p.top_p[r] : 0.0f;
+    int used = p.ks ? p.ks[r] : p.k;
+    used = used < 1 ? 1 : (used > p.k ? p.k : used);
+    float v[kPer];
+    int first = p.k;  // the first entry that names an element: the list's maximum
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const double q = e[j];
-      if (!(before < most) && base + j != first) e[j] = 0.0;
-      before += q;
+      const int i = base + j;
+      const bool held = j < per && i < p.k;
+      at[j] = held ? idx[i] : -1;
+      v[j] = held ? E::widen(vals[i]) : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (base + j >= used || at[j] < 0 || at[j] >= p.n) at[j] = -1;
+      if (at[j] >= 0 && first == p.k) first = base + j;
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+      const int b = __shfl_xor(first, o);
+      first = b < first ? b : first;
+    }
+    if constexpr (LW > 1) {
+      if (lane == 0) first_of_wave[wave] = first;
+      __syncthreads();
+      for (int w = 0; w < LW; ++w) first = first_of_wave[w] < first ? first_of_wave[w] : first;
+    }
+    const float m = first < p.k ? E::widen(vals[first]) : kNegInf;
+    double mine = 0.0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const bool live = at[j] >= 0 && m != kNegInf && (!greedy || base + j == first);
+      e[j] = 0.0;
+      if (j < per)  // (the same in every thread)
+        e[j] = !live ? 0.0
+               : v[j] == m ? 1.0
+                           : exp((static_cast<double>(v[j]) - static_cast<double>(m)) / static_cast<double>(t));
       mine += e[j];
     }
-    total = block_sum(mine, of_wave);
-  }
-  const double inv = total > 0.0 ? 1.0 / total : 0.0;
-  if (p.out_list && sl == 0) {
+    double total = all_sum(mine);
+    if (p.top_p) {
+      // the mass before each entry: the waves before this one, the lanes before this one, then
+      // this thread's own entries
+      double before = mine;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (j < per && base + j < p.k) p.out_list[r * p.k + base + j] = static_cast<float>(e[j] * inv);
+      for (int o = 1; o < 64; o <<= 1) {
+        const double b = __shfl_up(before, o);
+        if (lane >= o) before += b;
+      }
+      before -= mine;
+      if constexpr (LW > 1) {
+        for (int w = 0; w < wave; ++w) before += of_wave[w];
+      }
+      const double most = static_cast<double>(top_p) * total;
+      mine = 0.0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const double q = e[j];
+        if (!(before < most) && base + j != first) e[j] = 0.0;
+        before += q;
+        mine += e[j];
+      }
+      total = all_sum(mine);
+    }
+    inv = total > 0.0 ? 1.0 / total : 0.0;
+    if (p.out_list && sl == 0) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (j < per && base + j < p.k) p.out_list[r * p.k + base + j] = static_cast<float>(e[j] * inv);
+    }
+    if (LW > 1 && p.out) clear(threadIdx.x, kListThreads);
+  } else if (p.out) {
+    clear(threadIdx.x - 64, kListThreads - 64);
   }
   if (!p.out) return;
   __syncthreads();  // the zeros are written before the entries go over them
+  if (LW > 1 || wave == 0) {
 #pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (at[j] >= lo && at[j] < hi && e[j] > 0.0) out[at[j]] = O::narrow(static_cast<float>(e[j] * inv));
+    for (int j = 0; j < kPer; ++j)
+      if (at[j] >= lo && at[j] < hi && e[j] > 0.0) out[at[j]] = O::narrow(static_cast<float>(e[j] * inv));
+  }
 }
 
 }  // namespace
 
-static RowCut cut_rows(int64_t rows, int64_t n) {
+static RowCut cut_rows(int64_t rows, int64_t n, int64_t per_cu) {
   if (rows < 1) rows = 1;
   constexpr int64_t step = kSoftWaves * 64 * 8;
-  const int64_t most = (n + step - 1) / step, want = (kCus * 4 + rows - 1) / rows;
+  const int64_t most = (n + step - 1) / step, want = (kCus * per_cu + rows - 1) / rows;
   const int64_t slices = want < 1 ? 1 : (want > most ? most : want);
   const int64_t slice = ((n + slices - 1) / slices + step - 1) / step * step;
   return {slice, static_cast<int32_t>((n + slice - 1) / slice)};
@@ -512,10 +536,12 @@ static RowCut cut_rows(int64_t rows, int64_t n) {
 RowCut cut_softmax(int64_t rows, int64_t n, int dtype) {
   const int64_t bytes = n * (dtype == DS_BF16 ? 2 : 4);
   if (n >= 8 && (bytes <= 128 * 1024 || rows >= 48)) return {0, 0};  // (a row kernel's vectors hold up to 8)
-  return cut_rows(rows, n);
+  return cut_rows(rows, n, 4);
 }
 
-RowCut cut_list_softmax(int64_t rows, int64_t n) { return cut_rows(rows, n); }
+// Two workgroups a CU: each of a row's repeats the list (256 lists of 512 over 129280 fp32: one 19.6,
+// two 19.0, four 23.4 us).
+RowCut cut_list_softmax(int64_t rows, int64_t n) { return cut_rows(rows, n, 2); }
 
 template <int DT, int OT>
 static hipError_t softmax_out(const SoftmaxParams& p, hipStream_t s) {
@@ -543,13 +569,17 @@ hipError_t launch_softmax(int dtype, int out_dtype, const SoftmaxParams& p, hipS
   return dtype == DS_BF16 ? softmax_dt<DS_BF16>(out_dtype, p, s) : softmax_dt<DS_FP32>(out_dtype, p, s);
 }
 
-hipError_t launch_list_softmax(int dtype, int out_dtype, const ListSoftmaxParams& p, hipStream_t s) {
+template <int DT, int OT>
+static hipError_t list_softmax_out(const ListSoftmaxParams& p, hipStream_t s) {
   const int64_t units = p.rows * p.slices;
-  if (dtype == DS_BF16)
-    return out_dtype == DS_BF16 ? launch_units(list_softmax_kernel<DS_BF16, DS_BF16>, p, units, kListThreads, s)
-                                : launch_units(list_softmax_kernel<DS_BF16, DS_FP32>, p, units, kListThreads, s);
-  return out_dtype == DS_BF16 ? launch_units(list_softmax_kernel<DS_FP32, DS_BF16>, p, units, kListThreads, s)
-                              : launch_units(list_softmax_kernel<DS_FP32, DS_FP32>, p, units, kListThreads, s);
+  const bool one = p.out && p.k <= kOneWaveList && p.slice * static_cast<int64_t>(sizeof(typename Elem<OT>::T)) >= kOneWaveBytes;
+  return one ? launch_units(list_softmax_kernel<DT, OT, 1>, p, units, kListThreads, s)
+                             : launch_units(list_softmax_kernel<DT, OT, kListWaves>, p, units, kListThreads, s);
+}
+
+hipError_t launch_list_softmax(int dtype, int out_dtype, const ListSoftmaxParams& p, hipStream_t s) {
+  if (dtype == DS_BF16) return out_dtype == DS_BF16 ? list_softmax_out<DS_BF16, DS_BF16>(p, s) : list_softmax_out<DS_BF16, DS_FP32>(p, s);
+  return out_dtype == DS_BF16 ? list_softmax_out<DS_FP32, DS_BF16>(p, s) : list_softmax_out<DS_FP32, DS_FP32>(p, s);
 }
 
 }  // namespace ds
