@@ -115,6 +115,27 @@ def test_route_near_ties_are_decided_exactly(score, n, k, groups, tg, top):
                  renormalize=True)
 
 
+@pytest.mark.parametrize("scale", [0.002, 0.2, 1.0, 2.0, 6.0, 20.0])
+def test_route_constant_bias_and_tied_bf16_logits(scale):
+    """One bias for all and bf16 logits, of which many are equal: around zero, where different
+    logits give closer scores than fp32 tells apart, and where the sigmoid saturates."""
+    x = (scale * torch.randn(150, 256, generator=_gen(int(10 * scale)))).to(torch.bfloat16)
+    x[::5] = x[::5].abs()
+    for bias in (None, torch.zeros(256), torch.full((256,), -0.375)):
+        for groups, tg, top in ((8, 4, 2), (1, 1, 1), (8, 3, 1)):
+            _check_route(x.cuda(), 8, bias, f"flat {scale} {bias is None} {groups}", score=ts.SCORE_SIGMOID, groups=groups,
+                         topk_groups=tg, group_top=top, renormalize=True)
+
+
+@pytest.mark.parametrize("score", [ts.SCORE_SOFTMAX, ts.SCORE_SIGMOID])
+def test_route_large_biases(score):
+    """Biases beside which scores lose bits even in double, and ranges that no key holds."""
+    x = _logits(17, 30, 100, torch.bfloat16)
+    r = torch.randn(100, generator=_gen(18))
+    for bias in (torch.full((100,), 1e12), 1e9 + 64 * r.round(), 1e6 * r, 1e20 * r, 3e38 * r.clamp(-1, 1), -1e12 + 0 * r):
+        _check_route(x, 7, bias, f"large {float(bias[0])}", score=score, groups=5, topk_groups=3, group_top=2)
+
+
 def test_route_zero_bias_and_equal_logits_give_the_smaller_expert():
     x = torch.zeros(5, 200, device="cuda", dtype=torch.bfloat16)
     x[1] = 3.0
@@ -576,10 +597,15 @@ def test_streams_and_repeats_give_the_same_bits():
         with torch.cuda.stream(s2):
             got2.append(_everything(d2))
     p = ts.ds_softmax(d1["logits"], temperature=d1["t"], stream=s1)
+    dx = ts.ds_route_grad(d1["x"], w1[1], d1["g"], score=ts.SCORE_SIGMOID, renormalize=True, stream=s2)
+    w, _ = ts.ds_route(d1["x"], 6, bias=d1["bias"], score=ts.SCORE_SIGMOID, groups=8, topk_groups=4, group_top=2,
+                       renormalize=True, stream=s1)
+    l = ts.ds_topk_softmax(d1["vals"], d1["idx"], 30011, top_p=d1["top_p"], stream=s2)
     t, _ = ts.ds_verify(w1[3].view(2, 3, 30011), None, d1["tokens"], d1["u"], d1["v"], stream=s2)
     torch.cuda.synchronize()
     t2, _ = ts.ds_verify(w1[3].view(2, 3, 30011), None, d1["tokens"], d1["u"], d1["v"])
     assert torch.equal(p, w1[3]) and torch.equal(t, t2)
+    assert torch.equal(w, w1[0]) and torch.equal(dx, w1[2]) and torch.equal(l, w1[4])
     for got, want in ((got1, w1), (got2, w2)):
         for outs in got:
             for a, b in zip(outs, want):

@@ -37,7 +37,7 @@ def _route_grad(x=FAKE, rows=4, experts=64, stride=None, k=6, dtype=ts.BF16, cfg
                                   experts if gstride is None else gstride, None)
 
 
-def _softmax(x=FAKE, rows=4, n=1000, stride=None, dtype=ts.BF16, t=None, out=FAKE, ostride=None, odtype=ts.FP32,
+def _softmax(x=FAKE, rows=4, n=1000, stride=None, dtype=ts.BF16, t=None, out=2 * FAKE, ostride=None, odtype=ts.FP32,
              ws=FAKE, ws_bytes=1 << 40):
     return ts.lib().ds_softmax(x, rows, n, n if stride is None else stride, dtype, t, out,
                                n if ostride is None else ostride, odtype, ws, ws_bytes, None)
@@ -104,6 +104,7 @@ def test_route_grad_refusals(kw, code):
     (dict(dtype=2), BAD), (dict(odtype=-1), BAD), (dict(rows=-1), BAD), (dict(n=0), BAD), (dict(n=1 << 31), BAD),
     (dict(stride=999), BAD), (dict(ostride=999), BAD), (dict(x=None), BAD), (dict(out=None), BAD),
     (dict(x=FAKE + 1), ALIGN), (dict(out=FAKE + 2), ALIGN), (dict(t=FAKE + 2), ALIGN),
+    (dict(x=FAKE, out=FAKE), BAD),  # in place
 ])
 def test_softmax_refusals(kw, code):
     assert _softmax(**kw) == code

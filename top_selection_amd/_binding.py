@@ -409,17 +409,23 @@ def ds_verify_workspace_size(batch: int, n: int, dtype: int) -> int:
     return _workspace_size("ds_verify_workspace_size", batch, n, dtype)
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor for work on `stream` (torch's current one if None): memory that torch's allocator
+    hands out is free for the stream it is asked for on, and for no other."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _scratch(need: int, workspace, device, stream):
     """The call's workspace (to be kept until the call has been made), its address and its bytes:
-    the one given, or one of the needed size from torch, which is told about a stream that is
-    not its current one."""
+    the one given, or a new one of the needed size."""
     if workspace is None:
         if need == 0:
             return None, None, 0
-        torch = _torch()
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream is not None and stream != torch.cuda.current_stream(device):
-            workspace.record_stream(stream)
+        workspace = _empty((need,), _torch().uint8, device, stream)
         return workspace, workspace.data_ptr(), need
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
@@ -441,14 +447,14 @@ def ds_route(x, k: int, bias=None, score: int = SCORE_SOFTMAX, groups: int = 1, 
     if out_weights is not None:
         wp = _operand(out_weights, "out_weights", torch.float32, shape, dev)
     elif weights:
-        out_weights = torch.empty(shape, dtype=torch.float32, device=dev)
+        out_weights = _empty(shape, torch.float32, dev, stream)
         wp = out_weights.data_ptr()
     else:
         wp = None
     if out_idx is not None:
         ip = _operand(out_idx, "out_idx", torch.int32, shape, dev)
     else:
-        out_idx = torch.empty(shape, dtype=torch.int32, device=dev)
+        out_idx = _empty(shape, torch.int32, dev, stream)
         ip = out_idx.data_ptr()
     cfg = ds_route_config(score, groups, topk_groups, group_top, 1 if renormalize else 0, scale)
     _call("ds_route", dev, stream, x.data_ptr(), rows, n, rs, k, dt,
@@ -468,7 +474,7 @@ def ds_route_grad(x, idx, grad_weights, score: int = SCORE_SOFTMAX, renormalize:
         raise ValueError("idx must be 2-D [rows, k]")
     shape = (rows, idx.shape[1])
     if out is None:
-        out, os = torch.empty((rows, n), dtype=x.dtype, device=dev), n
+        out, os = _empty((rows, n), x.dtype, dev, stream), n
     else:
         _, _, os = _matrix(out, "out")
         if out.dtype != x.dtype or out.shape != (rows, n) or out.device != dev:
@@ -480,10 +486,10 @@ def ds_route_grad(x, idx, grad_weights, score: int = SCORE_SOFTMAX, renormalize:
     return out
 
 
-def _out_rows(out, out_dtype, rows: int, n: int, dev):
+def _out_rows(out, out_dtype, rows: int, n: int, dev, stream):
     torch = _torch()
     if out is None:
-        return torch.empty((rows, n), dtype=out_dtype or torch.float32, device=dev), n
+        return _empty((rows, n), out_dtype or torch.float32, dev, stream), n
     _, _, os = _matrix(out, "out")
     if out.shape != (rows, n) or out.device != dev or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out must be [rows, n] of out_dtype on the inputs' device")
@@ -497,7 +503,7 @@ def ds_softmax(x, temperature=None, out_dtype=None, out=None, workspace=None, st
     torch = _torch()
     rows, n, rs = _matrix(x, "x")
     dt, dev = _code(x.dtype), x.device
-    out, os = _out_rows(out, out_dtype, rows, n, dev)
+    out, os = _out_rows(out, out_dtype, rows, n, dev, stream)
     keep, ws, ws_bytes = _scratch(ds_softmax_workspace_size(rows, n, dt), workspace, dev, stream)
     _call("ds_softmax", dev, stream, x.data_ptr(), rows, n, rs, dt,
           None if temperature is None else _operand(temperature, "temperature", torch.float32, (rows,), dev),
@@ -518,12 +524,12 @@ def ds_topk_softmax(vals, idx, n: int, ks=None, temperature=None, top_p=None, ou
     rows, k = shape = vals.shape
     dt, dev, f32 = _code(vals.dtype), vals.device, torch.float32
     if rows_out:
-        out, os = _out_rows(out, out_dtype, rows, n, dev)
+        out, os = _out_rows(out, out_dtype, rows, n, dev, stream)
         op, odt = out.data_ptr(), _code(out.dtype)
     else:
         op, os, odt = None, n, FP32
         if out_list is None:
-            out_list = torch.empty(shape, dtype=f32, device=dev)
+            out_list = _empty(shape, f32, dev, stream)
     per_row = (rows,)
     _call("ds_topk_softmax", dev, stream, vals.data_ptr(), _operand(idx, "idx", torch.int32, shape, dev), rows, k, dt,
           None if ks is None else _operand(ks, "ks", torch.int32, per_row, dev),
@@ -557,12 +563,12 @@ def ds_verify(target, draft, draft_tokens, accept_u, sample_u, draft_lens=None, 
         dp = draft.data_ptr()
     i32, f32, each, per_seq = torch.int32, torch.float32, (batch, K), (batch,)
     if out_tokens is None:
-        out_tokens = torch.empty((batch, m), dtype=i32, device=dev)
+        out_tokens = _empty((batch, m), i32, dev, stream)
         tp = out_tokens.data_ptr()
     else:
         tp = _operand(out_tokens, "out_tokens", i32, (batch, m), dev)
     if out_accepted is None:
-        out_accepted = torch.empty(per_seq, dtype=i32, device=dev)
+        out_accepted = _empty(per_seq, i32, dev, stream)
         ap = out_accepted.data_ptr()
     else:
         ap = _operand(out_accepted, "out_accepted", i32, per_seq, dev)

@@ -331,6 +331,7 @@ __global__ __launch_bounds__(kRouteWaves * 64, (kRouteOccupancy<V, KP>)) void ro
   // position, and -inf (key 0) where there is no expert
   float per_unit = kTop;
   bool undecided = false;  // no key can hold the biases' range
+  bool flat = false;       // the order is that of bf16 logits through a sigmoid, whatever the bias
   if constexpr (kSteps) {
     float lo = 0.0f, hi = 0.0f;
     if (p.bias) {
@@ -343,8 +344,10 @@ __global__ __launch_bounds__(kRouteWaves * 64, (kRouteOccupancy<V, KP>)) void ro
       hi = wave_max(hi);
       lo = -wave_max(-lo);
     }
+    flat = MODE == kBySigmoid && DT == DS_BF16 && lo == hi;
     const float range = hi - lo + 1.0f;
-    undecided = !(range < 1e30f);
+    // (beyond, the sums' own rounding to double would count, and at last the keys' range)
+    undecided = !(fmaxf(fabsf(lo), fabsf(hi)) <= 1e6f);
     per_unit = kTop / range;
     for (int i = threadIdx.x; i < L * V; i += kRouteWaves * 64) {
       const int of = i / V, v = i % V, run_at = (of & ((1 << p.lanes_log2) - 1)) * p.per_lane + v;
@@ -519,9 +522,18 @@ __global__ __launch_bounds__(kRouteWaves * 64, (kRouteOccupancy<V, KP>)) void ro
 #pragma unroll
       for (int i = 0; i + 1 < KP; ++i) gap = list[i] - list[i + 1] < gap ? list[i] - list[i + 1] : gap;
       if (__any(gap < kNear)) {  // (or there is nothing at these places)
-        close |= (list[KP - 1] - dropped < kNear) & (dropped >= kFirst);
+        bool near = (list[KP - 1] - dropped < kNear) & (dropped >= kFirst);
 #pragma unroll
-        for (int i = 0; i + 1 < KP; ++i) close |= (list[i] - list[i + 1] < kNear) & (list[i + 1] >= kFirst);
+        for (int i = 0; i + 1 < KP; ++i) near |= (list[i] - list[i + 1] < kNear) & (list[i + 1] >= kFirst);
+        // Equal bf16 logits are common, and with one bias for all (zeros, before any balancing) they
+        // tie. Between 2^-8 and 8 different ones give scores at least 7e-6 apart, 30 steps of the
+        // coarsest keys: there only equal logits are near, and the smaller expert is right.
+        if (flat) {
+          const uint32_t high = static_cast<uint32_t>(fmaf(0.99966465f, per_unit, 1.0f)) << IB,
+                         low = static_cast<uint32_t>(fmaf(0.50097656f, per_unit, 2.0f)) << IB;
+          near &= !(list[0] < high && dropped >= low);
+        }
+        close |= near;
       }
     }
     close = row_reduce<LEVELS>(close ? 1u : 0u, [](uint32_t a, uint32_t b) { return a | b; }) != 0u;

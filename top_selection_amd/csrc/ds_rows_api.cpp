@@ -118,7 +118,7 @@ int ds_softmax(const void* x, int64_t rows, int64_t n, int64_t row_stride, int d
   if (!known(dtype) || !known(out_dtype)) return DS_ERR_INVALID_ARG;
   if (!rows_ok(rows, n, row_stride) || !rows_ok(rows, n, out_stride)) return DS_ERR_INVALID_ARG;
   if (rows == 0) return DS_OK;
-  if (!x || !out) return DS_ERR_INVALID_ARG;
+  if (!x || !out || x == out) return DS_ERR_INVALID_ARG;
   if (misaligned(x, elem_bytes(dtype)) || misaligned(out, elem_bytes(out_dtype)) || misaligned(temperature, 4))
     return DS_ERR_ALIGNMENT;
   const ds::RowCut c = ds::cut_softmax(rows, n, dtype);
