@@ -163,7 +163,7 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
   typedef typename V::type VT;
   __shared__ __attribute__((aligned(16))) VT kept[LV ? LV * THREADS : 1];
   __shared__ float of_wave[kWaves];
-  __shared__ int64_t first_of_wave[kWaves];
+  __shared__ uint32_t first_of_wave[kWaves];
   const int64_t r = p.unit0 + blockIdx.x;
   const T* x = static_cast<const T*>(p.x) + r * p.row_stride;
   typename O::T* out = static_cast<typename O::T*>(p.out) + r * p.out_stride;
@@ -242,30 +242,30 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) m = fmaxf(m, of_wave[w]);
   __syncthreads();
-  if (greedy || m == kNegInf) {  // one-hot at the first maximum, or nothing
-    int64_t hot = p.n;
+  if (greedy || m == kNegInf) {  // one-hot at the first maximum, or nothing (n fits 31 bits)
+    uint32_t hot = 0xFFFFFFFFu;
     if (m != kNegInf) {
-      const auto look = [&](VT v, int64_t a) {
+      const auto look = [&](VT v, uint32_t a) {
+        uint32_t in = N;
 #pragma unroll
-        for (int j = N - 1; j >= 0; --j) hot = E::widen(v[j]) == m && a + j < hot ? a + j : hot;
+        for (int j = N - 1; j >= 0; --j) in = E::widen(v[j]) == m ? j : in;
+        hot = in < N && a + in < hot ? a + in : hot;
       };
 #pragma unroll
-      for (int j = 0; j < R; ++j) look(reg[j], place(j));
+      for (int j = 0; j < R; ++j)
+        if (j * kStep < n) look(reg[j], place(j));
       if constexpr (LV > 0) {
-        for (int j = 0; j < LV; ++j) look(kept[j * THREADS + threadIdx.x], place(R + j));
+        for (int j = 0; j < LV; ++j)
+          if ((R + j) * kStep < n) look(kept[j * THREADS + threadIdx.x], place(R + j));
       }
-      for (int64_t i = past; i - mine < p.n && hot == p.n; i += 4 * kStep) {
+      for (int64_t i = past; i - mine < p.n && hot == 0xFFFFFFFFu; i += 4 * kStep) {
         VT v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = load(place64(i + j * kStep));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) look(v[j], place64(i + j * kStep));
+        for (int j = 0; j < 4; ++j) look(v[j], static_cast<uint32_t>(place64(i + j * kStep)));
       }
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) {
-        const int64_t b = __shfl_xor(hot, o);
-        hot = b < hot ? b : hot;
-      }
+      hot = row_reduce<6>(hot, [](uint32_t u, uint32_t w) { return u < w ? u : w; });
       if (lane == 0) first_of_wave[wave] = hot;
       __syncthreads();
 #pragma unroll
@@ -273,9 +273,10 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
     }
     for (int64_t i = mine; i < p.n; i += kStep) {
       const int64_t a = place64(i);
+      const uint32_t in = hot - static_cast<uint32_t>(a);
       typename W::type o;
 #pragma unroll
-      for (int j = 0; j < N; ++j) o[j] = O::narrow(a + j == hot ? 1.0f : 0.0f);
+      for (int j = 0; j < N; ++j) o[j] = O::narrow(in == static_cast<uint32_t>(j) ? 1.0f : 0.0f);
       *reinterpret_cast<typename W::unaligned*>(out + a) = o;
     }
     return;
@@ -343,8 +344,11 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
     typename W::type o;
 #pragma unroll
     for (int j = 0; j < N; ++j) o[j] = O::narrow(q[j]);
-    // (past the caches, which keep more of the logits: 50.1 -> 48.8 us for 256 x 129280 fp32)
-    __builtin_nontemporal_store(o, reinterpret_cast<typename W::unaligned*>(out + i));
+    const auto to = reinterpret_cast<typename W::unaligned*>(out + i);
+    // past the caches, which keep more of the logits (50.1 -> 48.8 us for 256 x 129280 fp32), where a
+    // store writes whole lines (two stores of bf16 to fp32 share one: 26.9 -> 32.3 us at 128 rows)
+    if constexpr (sizeof(o) <= 16) __builtin_nontemporal_store(o, to);
+    else *to = o;
   };
 #pragma unroll
   for (int j = 0; j < R; ++j)
