@@ -477,6 +477,40 @@ def test_verify_samples_the_target_rows_when_nothing_is_drafted():
     assert np.abs(count - N * _np(p)).max() <= 2 and not _np(acc).any()
 
 
+@pytest.mark.parametrize("batch", [64, 128, 129])
+def test_verify_of_many_long_rows(batch):
+    """Either side of the number of sequences that a workgroup each is enough for."""
+    n, K = 33001, 1
+    target, draft, tokens, u, v = _verify_inputs(batch, batch, K, n, torch.float32)
+    _check_verify(target, draft, tokens, u, v, None, f"verify {batch}")
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 7, 8, 9, 15, 17, 1023, 1024, 1025, 1027, 1031, 2047, 2048, 2049, 2055,
+                               4097, 33001])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_verify_draws_each_place(n, dtype):
+    """Equal masses, and numbers that aim at the middle of an element's share: (i + 1/2) of n shares
+    is half a share (2^-17 of all, at the least) from the next element, the number is rounded by 2^-25
+    and the sums by n 2^-53 of all. With a
+    refused certain draft t the same over the other elements."""
+    near = sorted({i for c in (0, 1024, 2048, n // 2, n) for i in range(c - 18, c + 18) if 0 <= i < n})
+    at = torch.tensor(near)
+    B = len(near)
+    target = torch.full((1, 1, n), 2.0 ** -10, dtype=DT[dtype]).expand(B, 1, n)
+    v = ((at.double() + 0.5) / n).float()
+    got, acc = ts.ds_verify(target.contiguous().cuda(), None, None, None, v.cuda())
+    assert _np(got)[:, 0].tolist() == near and not _np(acc).any()
+    if n == 1:
+        return
+    for t in (0, n // 2, n - 1):
+        others = at[at < n - 1]
+        target = torch.full((1, 1, 1), 2.0 ** -10, dtype=DT[dtype]).expand(len(others), 2, n).contiguous()
+        tokens = torch.full((len(others), 1), t, dtype=torch.int32)
+        v = ((others.double() + 0.5) / (n - 1)).float()
+        got, acc = ts.ds_verify(target.cuda(), None, tokens.cuda(), torch.ones(len(others), 1).cuda(), v.cuda())
+        assert _np(got)[:, 0].tolist() == [i + (i >= t) for i in others.tolist()] and not _np(acc).any()
+
+
 def test_verify_strided_inputs():
     target, draft, tokens, u, v = _verify_inputs(9, 4, 3, 1001, torch.float32)
     wide = torch.zeros(4, 4, 1103)

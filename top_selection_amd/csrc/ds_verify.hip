@@ -67,8 +67,8 @@ struct Rows {
     without = refused && !v.draft ? d.token : -1;
   }
 
-  // kOnce: past the caches, for rows that are long and read once (256 x 129280 fp32 45 -> 41 us;
-  // short rows are better kept for the draw, 48 x 32003 bf16 10.8 and 11.4 us).
+  // kOnce: past the caches, for rows that are long and read once (256 x 129280 fp32 42.5 -> 37.9 us;
+  // short rows are better kept for the draw, 48 x 32003 bf16 7.6 and 8.5 us).
   template <bool kOnce>
   static __device__ __forceinline__ typename V::type load(const T* from) {
     const auto at = reinterpret_cast<const typename V::unaligned*>(from);
@@ -76,58 +76,65 @@ struct Rows {
     else return *at;
   }
 
-  // The masses of the lane's elements of a unit, in vectors `step` elements apart from the
-  // lane's first, unit + lane * first on. Elements past n have none. The difference of two fp32 is
-  // taken in double: it is the sums' terms that must not be rounded to fp32.
+  // The mass of element i; none past the end. The difference of two fp32 is taken in double: the
+  // sums' terms must not be rounded.
+  __device__ __forceinline__ double mass(int64_t i, int64_t n) const {
+    if (i >= n || i == without) return 0.0;
+    const double d = E::widen(p[i]);
+    return fmax(d - (q ? static_cast<double>(E::widen(q[i])) : 0.0), 0.0);
+  }
+
+  // The mass of the lane's elements of a unit: vectors `step` elements apart, the lanes' first ones
+  // `first` apart. A vector that would pass the row's end is moved back to end there, and what it
+  // then holds a second time is left out: loads one by one under guards, for the last unit alone,
+  // made that unit's wave the last. And few instructions, as a wave runs them once or twice and
+  // has to fetch them: without a draft row q is 0, not a case of its own, and the draw looks at
+  // one run's elements in as many lanes. From 27 to 14 KB of code in all (bf16): 48 x 32003 10.9 ->
+  // 7.7 us, one sequence of 129280 fp32 8.8 -> 7.4, 256 of them 41 -> 37.9.
   template <int kFirst, int kStep, bool kOnce = false>
-  __device__ __forceinline__ void masses(int64_t unit, int64_t n, int lane, double (&m)[kVerifyLoads][N]) const {
-    typename V::type pv[kVerifyLoads], qv[kVerifyLoads];
-    const int64_t at = unit + lane * kFirst;
-    if (unit + kVerifyUnit<DT> <= n) {
-#pragma unroll
-      for (int u = 0; u < kVerifyLoads; ++u)
-        pv[u] = load<kOnce>(p + at + u * kStep);
-      if (q) {
-#pragma unroll
-        for (int u = 0; u < kVerifyLoads; ++u)
-          qv[u] = load<kOnce>(q + at + u * kStep);
+  __device__ __forceinline__ double share(int64_t unit, int64_t n, int lane) const {
+    double t = 0.0;
+    if (n < N) {  // a row shorter than a vector
+      if (lane == 0) {
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) t += mass(i, n);
       }
-    } else {
-#pragma unroll
-      for (int u = 0; u < kVerifyLoads; ++u)
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const int64_t i = at + u * kStep + j;
-          pv[u][j] = i < n ? p[i] : T(0);
-          if (q) qv[u][j] = i < n ? q[i] : T(0);
-        }
+      return t;
     }
-    const int64_t gone = without - at;  // where the lane would hold the element without mass
-    const int skip = gone >= 0 && gone < kVerifyUnit<DT> ? static_cast<int>(gone) : -1;
+    const int most = unit + kVerifyUnit<DT> <= n ? kVerifyUnit<DT> : static_cast<int>(n - unit) - N;
+    const int64_t left = without - unit;
+    const int gone = left >= 0 && left < kVerifyUnit<DT> ? static_cast<int>(left) : -1;
+    typename V::type pv[kVerifyLoads], qv[kVerifyLoads] = {};
+    int at[kVerifyLoads];
+#pragma unroll
+    for (int u = 0; u < kVerifyLoads; ++u) {
+      at[u] = lane * kFirst + u * kStep < most ? lane * kFirst + u * kStep : most;
+      pv[u] = load<kOnce>(p + unit + at[u]);
+    }
+    if (q) {
+#pragma unroll
+      for (int u = 0; u < kVerifyLoads; ++u) qv[u] = load<kOnce>(q + unit + at[u]);
+    }
+    if (gone >= 0 || most < kVerifyUnit<DT>) {  // (the same in every lane)
+#pragma unroll
+      for (int u = 0; u < kVerifyLoads; ++u) {
+        const int twice = lane * kFirst + u * kStep - at[u], none = gone < 0 ? -1 : gone - at[u];
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (j < twice || j == none) pv[u][j] = T(0);
+      }
+    }
 #pragma unroll
     for (int u = 0; u < kVerifyLoads; ++u)
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        double d = static_cast<double>(E::widen(pv[u][j]));
-        if (q) {
-          d -= static_cast<double>(E::widen(qv[u][j]));
-          d = fmax(d, 0.0);
-        } else if (without >= 0) {
-          d = skip == u * kStep + j ? 0.0 : d;
-        }
-        m[u][j] = d;
-      }
+      for (int j = 0; j < N; ++j)
+        t += fmax(static_cast<double>(E::widen(pv[u][j])) - static_cast<double>(E::widen(qv[u][j])), 0.0);
+    return t;
   }
 
   template <bool kOnce>
   __device__ __forceinline__ double sum(int64_t unit, int64_t n, int lane) const {
-    double m[kVerifyLoads][N], t = 0.0;
-    masses<N, 64 * N, kOnce>(unit, n, lane, m);  // in memory's order
-#pragma unroll
-    for (int u = 0; u < kVerifyLoads; ++u)
-#pragma unroll
-      for (int j = 0; j < N; ++j) t += m[u][j];
-    return wave_sum(t);
+    return wave_sum(share<N, 64 * N, kOnce>(unit, n, lane));  // in memory's order
   }
 };
 
@@ -179,29 +186,18 @@ __device__ __forceinline__ int32_t draw(const Rows<DT>& rows, const double* sums
     if (past) break;
     start = of_lane(end, 63);
   }
-  // within the unit each lane takes a run of elements
-  double m[kVerifyLoads][N];
-  const int64_t first = static_cast<int64_t>(unit) * kVerifyUnit<DT>;
-  rows.template masses<kRun, N>(first, n, lane, m);
-  double s = 0.0;
-#pragma unroll
-  for (int u = 0; u < kVerifyLoads; ++u)
-#pragma unroll
-    for (int j = 0; j < N; ++j) s += m[u][j];
-  double sum = before + (scan_lanes(s) - s);
-  int hit = -1, with = -1;
-#pragma unroll
-  for (int u = 0; u < kVerifyLoads; ++u)
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      sum += m[u][j];
-      const bool some = m[u][j] > 0.0;
-      with = some ? u * N + j : with;
-      hit = some && hit < 0 && sum > point ? u * N + j : hit;
-    }
-  const uint64_t hits = __ballot(hit >= 0), withs = __ballot(with >= 0);
-  const int l = hits ? __builtin_ctzll(hits) : 63 - __builtin_clzll(withs | 1);
-  return static_cast<int32_t>(first + l * kRun + __builtin_amdgcn_readlane(hits ? hit : with, l));
+  // within the unit each lane takes a run of elements, and then each an element of the run that
+  // the point falls in; the last lane or element with mass where by rounding none is past it
+  int64_t first = static_cast<int64_t>(unit) * kVerifyUnit<DT>;
+  const auto pass = [&](double m) {
+    const double end = before + scan_lanes(m);
+    const uint64_t some = __ballot(m > 0.0), past = some & __ballot(end > point);
+    const int l = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(some | 1);
+    before = of_lane(end, l) - of_lane(m, l);
+    return l;
+  };
+  first += pass(rows.template share<kRun, N>(first, n, lane)) * kRun;
+  return static_cast<int32_t>(first + pass(lane < kRun ? rows.mass(first + lane, n) : 0.0));
 }
 
 // The sum of the units' masses, in every lane of every wave.
@@ -313,13 +309,13 @@ hipError_t verify_dt(const VerifyParams& p, hipStream_t s) {
 }  // namespace
 
 // No slices (one workgroup per sequence, one launch) while a row is short or the sequences fill
-// the card by themselves; else slices of whole units. Both sides: one sequence of 129280 fp32 in
-// one workgroup 18 us, in slices 8.7 (15 and 18 from the host, which then waits for neither);
-// 256 sequences 41 and 49 us.
+// half the card by themselves; else slices of whole units. Both sides, fp32, drafts of 3: one
+// sequence of 129280 in one workgroup 12.8 us, in slices 7.4; 64 sequences 28 and 18, 128 32 and 26,
+// 192 35 and 40, 256 41 and 50.
 VerifyCut cut_verify(int64_t batch, int64_t n, int dtype) {
   const int64_t unit = dtype == DS_BF16 ? kVerifyUnit<DS_BF16> : kVerifyUnit<DS_FP32>;
   const int64_t units = (n + unit - 1) / unit;
-  if (units <= kVerifyShort || (batch >= 64 && units <= kVerifyLdsUnits)) return {0, 0, 0};
+  if (units <= kVerifyShort || (batch > kCus / 2 && units <= kVerifyLdsUnits)) return {0, 0, 0};
   const int64_t want = batch >= kCus ? 1 : (kCus + batch - 1) / (batch < 1 ? 1 : batch);
   int64_t slice = (units + want - 1) / want;
   slice = (slice + kVerifyWaves - 1) / kVerifyWaves * kVerifyWaves;
