@@ -287,6 +287,21 @@ def test_softmax_long_rows(rows, n, dtype):
         _close(p, want, f"softmax {rows}x{n} {dtype} {kind}")
 
 
+@pytest.mark.parametrize("rows", [1, 8, 9, 17, 32, 33, 47])
+@pytest.mark.parametrize("n,dtype", [(8193, "fp32"), (16385, "fp32"), (32001, "fp32"), (16387, "bf16"), (50005, "bf16")])
+def test_softmax_few_rows(rows, n, dtype):
+    """Rows that several workgroups work out, each for its part of the output, and those that one does."""
+    t = 0.5 + torch.rand(rows, generator=_gen(rows))
+    t[1::4] = 0.0
+    t[2::7] = 1e-40
+    for kind in ("normal", "inf", "masked", "ties"):
+        x = _logits(n + rows, rows, n, DT[dtype], kind)
+        out = torch.full((rows, n + 6), 7.0, device="cuda")
+        ts.ds_softmax(x, temperature=t.cuda(), out=out[:, 3:n + 3])
+        _close(out[:, 3:n + 3], orc.softmax(_np(x), _np(t)), f"softmax {rows}x{n} {dtype} {kind}")
+        assert (out[:, :3] == 7).all() and (out[:, n + 3:] == 7).all()
+
+
 def test_softmax_extreme_temperatures_spread_or_keep_the_mass():
     """An infinite temperature is uniform over what is not masked; a NaN one counts as not above 0."""
     x = torch.randn(3, 20000, generator=_gen(9))

@@ -145,12 +145,13 @@ __global__ __launch_bounds__(kSoftWaves * 64) void softmax_write_kernel(SoftmaxP
   }
 }
 
-// One workgroup per row of at least N elements, which it reads from memory once where it can:
+// A workgroup per row of at least N elements, which it reads from memory once where it can:
 // each thread keeps R vectors in registers and LV in LDS, and only what is past them is read
 // again for the output. Vector j of thread t holds elements (j * THREADS + t) * N on; a vector
 // that would pass the row's end is moved back to end there (no branches around loads and
 // stores: what it holds twice changes no maximum, is left out of the sum, and is written
-// twice with the same value).
+// twice with the same value). 2^together workgroups may work out the same row and write each
+// their part of the vectors.
 template <int DT, int OT, int THREADS, int R, int LV>
 __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
   using E = Elem<DT>;
@@ -164,7 +165,9 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
   __shared__ __attribute__((aligned(16))) VT kept[LV ? LV * THREADS : 1];
   __shared__ float of_wave[kWaves];
   __shared__ uint32_t first_of_wave[kWaves];
-  const int64_t r = p.unit0 + blockIdx.x;
+  const int64_t r = (p.unit0 + blockIdx.x) >> p.together;
+  const int part = (p.unit0 + blockIdx.x) & ((1 << p.together) - 1);
+  const auto ours = [&](int j) { return ((j ^ part) & ((1 << p.together) - 1)) == 0; };
   const T* x = static_cast<const T*>(p.x) + r * p.row_stride;
   typename O::T* out = static_cast<typename O::T*>(p.out) + r * p.out_stride;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -271,7 +274,7 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) hot = first_of_wave[w] < hot ? first_of_wave[w] : hot;
     }
-    for (int64_t i = mine; i < p.n; i += kStep) {
+    for (int64_t i = mine + part * static_cast<int64_t>(kStep); i < p.n; i += static_cast<int64_t>(kStep) << p.together) {
       const int64_t a = place64(i);
       const uint32_t in = hot - static_cast<uint32_t>(a);
       typename W::type o;
@@ -300,7 +303,7 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
       for (int j = 0; j < N; ++j) z += a + j >= i ? soft_exp(E::widen(v[j]), m, scale) : 0.0f;
     }
     const float inv = 1.0f / block_sum(z);
-    for (int64_t i = mine; i < p.n; i += kStep) {
+    for (int64_t i = mine + part * static_cast<int64_t>(kStep); i < p.n; i += static_cast<int64_t>(kStep) << p.together) {
       const int64_t a = place64(i);
       const VT v = load(a);
       typename W::type o;
@@ -352,7 +355,7 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
   };
 #pragma unroll
   for (int j = 0; j < R; ++j)
-    if (j * kStep < n) {
+    if (j * kStep < n && ours(j)) {
       float q[N];
 #pragma unroll
       for (int i = 0; i < N; ++i)
@@ -535,7 +538,7 @@ static RowCut cut_rows(int64_t rows, int64_t n, int64_t per_cu) {
 
 // No slices (one workgroup per row, one launch) while a row is short or there are many; else
 // slices and two launches. Both sides, in us, called one after the other from the host: 7 rows
-// of 50001 bf16 9.8 and 11.6, 7 of 50001 fp32 11.4 and 12.0 (from a graph 11.6 and 8.2), 64 of
+// of 50001 bf16 7.9 and 11.6, 7 of 50001 fp32 11.4 and 12.0 (from a graph 11.6 and 8.2), 64 of
 // 129280 fp32 19.9 and 21.1, 100 of them 24 and 33, one of 16384 fp32 7.8 and 12.
 RowCut cut_softmax(int64_t rows, int64_t n, int dtype) {
   const int64_t bytes = n * (dtype == DS_BF16 ? 2 : 4);
@@ -548,14 +551,20 @@ RowCut cut_softmax(int64_t rows, int64_t n, int dtype) {
 RowCut cut_list_softmax(int64_t rows, int64_t n) { return cut_rows(rows, n, 2); }
 
 template <int DT, int OT>
-static hipError_t softmax_out(const SoftmaxParams& p, hipStream_t s) {
+static hipError_t softmax_out(SoftmaxParams p, hipStream_t s) {
   if (p.slices == 0) {
     // the fewest vectors a thread that hold the row: those past its end cost as much as others
     const int64_t vectors = (p.n + Elem<DT>::kPer16 - 1) / Elem<DT>::kPer16;
     if (vectors <= 256 * 4) return launch_units(softmax_row_kernel<DT, OT, 256, 4, 0>, p, p.rows, 256, s);
     if (vectors <= 256 * 8) return launch_units(softmax_row_kernel<DT, OT, 256, 8, 0>, p, p.rows, 256, s);
-    if (vectors <= 1024 * 4) return launch_units(softmax_row_kernel<DT, OT, 1024, 4, 0>, p, p.rows, 1024, s);
-    if (vectors <= 1024 * 8) return launch_units(softmax_row_kernel<DT, OT, 1024, 8, 0>, p, p.rows, 1024, s);
+    // few rows: several workgroups per row, each with its share of the stores and of the second
+    // exponentials, but not so many that reading each row that often costs more (8 workgroups for
+    // each of 7 rows of 50001 bf16 10.0 -> 7.9 us; 2 for 32 of 32000 fp32 change nothing, 4 take
+    // 7.0 us for 5.9)
+    if (vectors <= 1024 * 8)
+      while (p.together < 3 && p.rows << (p.together + 1) <= kCus / 4) ++p.together;
+    if (vectors <= 1024 * 4) return launch_units(softmax_row_kernel<DT, OT, 1024, 4, 0>, p, p.rows << p.together, 1024, s);
+    if (vectors <= 1024 * 8) return launch_units(softmax_row_kernel<DT, OT, 1024, 8, 0>, p, p.rows << p.together, 1024, s);
     constexpr bool kTwo = DT == DS_BF16;  // (two bytes an element)
     return launch_units(softmax_row_kernel<DT, OT, 1024, kTwo ? 8 : 20, kTwo ? 8 : 9>, p, p.rows, 1024, s);
   }

@@ -57,6 +57,7 @@ struct SoftmaxParams {
   int32_t slices;  // workgroups per row
   int64_t unit0;   // (row, slice) of a launch's first workgroup, set by the launcher
   float2* part;    // [rows][slices]: (maximum, sum of exp against it)
+  int32_t together;  // no slices: log2 of the workgroups per row, set by the launcher
 };
 
 struct ListSoftmaxParams {
