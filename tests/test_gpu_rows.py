@@ -287,6 +287,15 @@ def test_softmax_long_rows(rows, n, dtype):
         _close(p, want, f"softmax {rows}x{n} {dtype} {kind}")
 
 
+@pytest.mark.parametrize("rows,n", [(50, 130001), (48, 300007), (3, 140003), (2, 30001)])
+def test_softmax_far_from_zero(rows, n):
+    """Logits whose common part is thousands of times their spread: it takes no part in the result."""
+    t = 0.3 + torch.rand(rows, generator=_gen(rows))
+    for shift in (-3000.0, 3000.0):
+        x = (shift + torch.randn(rows, n, generator=_gen(n))).cuda()
+        _close(ts.ds_softmax(x, temperature=t.cuda()), orc.softmax(_np(x), _np(t)), f"softmax {rows}x{n} {shift}")
+
+
 @pytest.mark.parametrize("rows", [1, 8, 9, 17, 32, 33, 47])
 @pytest.mark.parametrize("n,dtype", [(8193, "fp32"), (16385, "fp32"), (32001, "fp32"), (16387, "bf16"), (50005, "bf16")])
 def test_softmax_few_rows(rows, n, dtype):

@@ -211,7 +211,13 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
   const int64_t past = kKept + static_cast<int64_t>(mine), end = p.n - N;
   const auto place64 = [&](int64_t i) { return i < end ? i : end; };
   // exp((v - top) / t) as exp2(v * scale - top * scale) with the product of the maximum rounded
-  // once: what that is off by is the same factor everywhere and divides out
+  // once: what that is off by is the same factor everywhere and divides out. (That product is kept
+  // from being fused into a difference, where it would not be rounded.)
+  const auto rounded = [&](float v) {
+    float q = v * scale;
+    asm("" : "+v"(q));
+    return q;
+  };
   const auto term = [&](T v, float tops) { return __builtin_amdgcn_exp2f(fmaf(E::widen(v), scale, -tops)); };
   const auto sum_of = [&](VT v, int64_t back, float tops) {  // back: elements that another vector holds too
     float s = 0.0f;
@@ -227,8 +233,8 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) top = most(top, v[j]);
     if (top != kNegInf) {
-      const float tops = top * scale;
-      z *= m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m * scale - tops);
+      const float tops = rounded(top);
+      z *= m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(rounded(m) - tops);
 #pragma unroll
       for (int j = 0; j < 4; ++j) z += sum_of(v[j], at + j * kStep - place64(at + j * kStep), tops);
     }
@@ -284,7 +290,7 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
     }
     return;
   }
-  const float ms = m * scale;
+  const float ms = rounded(m);
   const auto block_sum = [&](float v) {
     v = wave_sum(v);
     if (lane == 0) of_wave[wave] = v;
@@ -313,7 +319,7 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
     }
     return;
   }
-  z *= own == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(own * scale - ms);
+  z *= own == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(rounded(own) - ms);
 #pragma unroll
   for (int j = 0; j < R; ++j) {
     const bool whole = (j + 1) * kStep <= n;
