@@ -340,7 +340,8 @@ typedef struct ds_route_config {
  *   expert is scale * s_e, divided by the sum of the chosen s when `renormalize` is set: the
  *   bias moves the choice only.
  * The order is exact: c is evaluated in double precision, and without a bias the order is
- * that of the logits themselves; equal scores go to the smaller group and expert.
+ * that of the logits themselves; equal scores go to the smaller group and expert. (Sums of different
+ * terms that are equal as real numbers, s_a + b_a = s_b + b_b, are as double rounds them.)
  * An expert whose logit or bias is -inf is masked: it is never chosen and, with a logit of
  * -inf, takes no part in the softmax. A group's score counts its unmasked experts, and a group
  * without any is chosen after all others. Slots that no expert is left for hold index -1 and
