@@ -210,14 +210,8 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
   // what is past the kept vectors: the running maximum and sum, four vectors at a time
   const int64_t past = kKept + static_cast<int64_t>(mine), end = p.n - N;
   const auto place64 = [&](int64_t i) { return i < end ? i : end; };
-  // exp((v - top) / t) as exp2(v * scale - top * scale) with the product of the maximum rounded
-  // once: what that is off by is the same factor everywhere and divides out. (That product is kept
-  // from being fused into a difference, where it would not be rounded.)
-  const auto rounded = [&](float v) {
-    float q = v * scale;
-    asm("" : "+v"(q));
-    return q;
-  };
+  // exp((v - top) / t) as exp2(v * scale - tops), tops = top * scale rounded once: what that is off by is
+  // the same factor everywhere and divides out
   const auto term = [&](T v, float tops) { return __builtin_amdgcn_exp2f(fmaf(E::widen(v), scale, -tops)); };
   const auto sum_of = [&](VT v, int64_t back, float tops) {  // back: elements that another vector holds too
     float s = 0.0f;
@@ -225,6 +219,9 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
     for (int i = 0; i < N; ++i) s += i >= back ? term(v[i], tops) : 0.0f;
     return s;
   };
+  // A thread's running maximum may be any finite number (a mask), of which no product can be
+  // rounded harmlessly: here the difference is taken first. (Infinite maxima and inverse
+  // temperatures make NaN here; their rows are summed again below.)
   for (int64_t at = past; at - mine < p.n; at += 4 * kStep) {
     VT v[4];
 #pragma unroll
@@ -233,10 +230,16 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) top = most(top, v[j]);
     if (top != kNegInf) {
-      const float tops = rounded(top);
-      z *= m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(rounded(m) - tops);
+      z *= __builtin_amdgcn_exp2f((m - top) * scale);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) z += sum_of(v[j], at + j * kStep - place64(at + j * kStep), tops);
+      for (int j = 0; j < 4; ++j) {
+        const int64_t back = at + j * kStep - place64(at + j * kStep);
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          s += i >= back ? __builtin_amdgcn_exp2f((E::widen(v[j][i]) - top) * scale) : 0.0f;
+        z += s;
+      }
     }
     m = top;
   }
@@ -290,7 +293,7 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
     }
     return;
   }
-  const float ms = rounded(m);
+  const float ms = m * scale;
   const auto block_sum = [&](float v) {
     v = wave_sum(v);
     if (lane == 0) of_wave[wave] = v;
@@ -319,7 +322,7 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
     }
     return;
   }
-  z *= own == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(rounded(own) - ms);
+  z *= __builtin_amdgcn_exp2f(fmaf(own, scale, -ms));  // to what `term` gives
 #pragma unroll
   for (int j = 0; j < R; ++j) {
     const bool whole = (j + 1) * kStep <= n;
