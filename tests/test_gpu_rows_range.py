@@ -36,3 +36,41 @@ def test_softmax_finite_masks(dtype, shape, mask):
     for temp in (None, t):
         p = ts.ds_softmax(x.cuda(), temperature=None if temp is None else temp.cuda())
         _close(p, orc.softmax(_np(x), None if temp is None else _np(temp)), f"softmax {shape} {dtype} {mask} {temp is None}")
+
+
+def _softmax(x, t):
+    """The definition with an infinite temperature as the limit: no mass at -inf, else as much at any logit."""
+    x, t = _np(x), np.broadcast_to(np.asarray(t, np.float64), len(x))[:, None]
+    m = x.max(axis=1, keepdims=True)
+    with np.errstate(over="ignore", invalid="ignore"):
+        e = np.where(x == -np.inf, 0.0, np.exp(np.where(x == m, 0.0, x - m) / t))
+    return e / np.maximum(e.sum(axis=1, keepdims=True), 1e-300)
+
+
+@pytest.mark.parametrize("dtype,shape", EACH)
+def test_softmax_small_temperatures(dtype, shape):
+    """Temperatures by decades from 1e-4 to 1e-30: the mass moves to the maxima."""
+    rows, n = shape
+    for first in ((4, 13, 22) if rows < 27 else (4,)):
+        t = torch.tensor([10.0 ** -(first + r % (9 if rows < 27 else 27)) for r in range(rows)])
+        x = 10 + 4 * torch.randn(rows, n, generator=_gen(n + first))
+        x[1::2] -= 50  # maxima on both sides of zero
+        x = x.to(DT[dtype])
+        x[:, n - 2] = x.max(dim=1)[0]  # a tie
+        p = ts.ds_softmax(x.cuda(), temperature=t.cuda())
+        _close(p, _softmax(x, _np(t)), f"softmax {shape} {dtype} t from 1e-{first}")
+
+
+@pytest.mark.parametrize("dtype,shape", EACH)
+def test_softmax_logits_far_from_zero(dtype, shape):
+    """Rows whose logits are all near one number of either sign, from 1e9 to 1e37, a few steps of their type
+    apart, at temperature 1 and at one of about a step; and rows of a mask alone."""
+    rows, n = shape
+    step = 2.0 ** (-7 if dtype == "bf16" else -22)
+    base = torch.tensor([(-1.0) ** r * 10.0 ** (9 + 3.5 * (r % 9)) for r in range(rows)])
+    x = (base[:, None] * (1 + step * torch.randint(0, 3, (rows, n), generator=_gen(n)))).to(DT[dtype])
+    x[3] = -1e10
+    x[4] = torch.finfo(DT[dtype]).min
+    for t in (torch.ones(rows), base.abs() * step):
+        p = ts.ds_softmax(x.cuda(), temperature=t.cuda())
+        _close(p, _softmax(x, _np(t)), f"softmax {shape} {dtype} t[0]={float(t[0])}")

@@ -211,7 +211,9 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
   const int64_t past = kKept + static_cast<int64_t>(mine), end = p.n - N;
   const auto place64 = [&](int64_t i) { return i < end ? i : end; };
   // exp((v - top) / t) as exp2(v * scale - tops), tops = top * scale rounded once: what that is off by is
-  // the same factor everywhere and divides out
+  // the same factor everywhere and divides out. Below 2^28 (kFar) it is off by at most 8, a factor that
+  // takes no term or sum out of fp32's range; larger products are not used.
+  constexpr float kFar = 0x1p28f;
   const auto term = [&](T v, float tops) { return __builtin_amdgcn_exp2f(fmaf(E::widen(v), scale, -tops)); };
   const auto sum_of = [&](VT v, int64_t back, float tops) {  // back: elements that another vector holds too
     float s = 0.0f;
@@ -303,7 +305,7 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
     for (int w = 0; w < kWaves; ++w) v += of_wave[w];
     return v;
   };
-  if (!(fabsf(ms) < 1e30f)) {  // an infinite maximum or inverse temperature: element by element
+  if (!(fabsf(ms) < kFar)) {  // far logits, tiny temperatures, infinities: differences, element by element
     z = 0.0f;
     for (int64_t i = mine; i < p.n; i += kStep) {
       const int64_t a = place64(i);
