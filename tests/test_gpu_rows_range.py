@@ -74,3 +74,29 @@ def test_softmax_logits_far_from_zero(dtype, shape):
     for t in (torch.ones(rows), base.abs() * step):
         p = ts.ds_softmax(x.cuda(), temperature=t.cuda())
         _close(p, _softmax(x, _np(t)), f"softmax {shape} {dtype} t[0]={float(t[0])}")
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("n,k,groups,tg,top", [(100, 7, 5, 3, 2), (256, 8, 8, 4, 2), (64, 6, 4, 2, 1)])
+def test_route_groups_beside_large_biases(score, n, k, groups, tg, top):
+    """Biases beside which scores vanish, in sums as in single ones: groups tie in double and the smaller ones are
+    chosen; ranges of biases that fp32 does not hold."""
+    x = (1.5 * torch.randn(40, n, generator=_gen(n))).cuda()
+    size = n // groups
+    ends = torch.zeros(n)
+    ends[-size:] = 3e38
+    ends[:size] = -3e38
+    near = 3e38 * (1 - 2.0 ** -20 * torch.rand(n, generator=_gen(k)))
+    near[:size] = -3e38
+    one = torch.zeros(n)
+    one[size] = -3e38
+    one[-1] = 3e38
+    for label, bias in (("1e12", torch.full((n,), 1e12)), ("1e15", torch.full((n,), 1e15)), ("1e20", torch.full((n,), 1e20)),
+                        ("-1e17", torch.full((n,), -1e17)), ("ends", ends), ("near", near), ("one", one)):
+        for dtype in DT.values():
+            kw = dict(groups=groups, topk_groups=tg, group_top=top, renormalize=True)
+            code = ts.SCORE_SIGMOID if score == "sigmoid" else ts.SCORE_SOFTMAX
+            w, i = ts.ds_route(x.to(dtype), k, bias=bias.cuda(), score=code, **kw)
+            ww, wi = orc.route(_np(x.to(dtype)), k, _np(bias), score, **kw)
+            assert np.array_equal(_np(i), wi), f"{label} {dtype}"
+            _close(w, ww, f"{label} {dtype}")

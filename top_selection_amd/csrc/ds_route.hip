@@ -484,7 +484,7 @@ __global__ __launch_bounds__(kRouteWaves * 64, (kRouteOccupancy<V, KP>)) void ro
       merge_down<KP>(list, o, dropped);
     }
     bool close = undecided || (MODE == kByLogit && m == __builtin_huge_valf());
-    bool unsure = false;  // the choice of groups is close
+    bool unsure = undecided;  // the choice of groups is close, or not to be taken from keys at all
     uint64_t kept = 0;    // lanes whose group was chosen
     const auto rank_groups = [&](auto level) {  // of the lists of 2^level lanes
       const uint32_t a = list[0] >> IB, b = list[1] >> IB;
