@@ -100,3 +100,40 @@ def test_route_groups_beside_large_biases(score, n, k, groups, tg, top):
             ww, wi = orc.route(_np(x.to(dtype)), k, _np(bias), score, **kw)
             assert np.array_equal(_np(i), wi), f"{label} {dtype}"
             _close(w, ww, f"{label} {dtype}")
+
+
+@pytest.mark.parametrize("dtype,shape", EACH)
+def test_softmax_large_temperatures(dtype, shape):
+    """Temperatures up to infinity against logits up to the type's ends: what is finite keeps its share."""
+    rows, n = shape
+    top = torch.finfo(DT[dtype]).max
+    x = torch.randn(rows, n, generator=_gen(n))
+    x[1::3] *= 2e37
+    x[2::3, ::5] = -top
+    x[3::6, 1::7] = top
+    x[4::6, 2::7] = -np.inf
+    x = x.clamp(-top, top).to(DT[dtype])
+    x[4::6, 2::7] = -np.inf
+    t = torch.tensor([(float("inf"), 3e38, 1.2e38, 1e38, 2e37, 1e36, 1e30)[r % 7] for r in range(rows)])
+    p = ts.ds_softmax(x.cuda(), temperature=t.cuda())
+    _close(p, _softmax(x, _np(t)), f"softmax {shape} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,n,k", [(21, 5000, 300), (21, 5000, 1000), (260, 70001, 64)])
+def test_list_softmax_large_temperatures(dtype, rows, n, k):
+    top = torch.finfo(DT[dtype]).max
+    x = 1e37 * torch.randn(rows, k, generator=_gen(k))
+    x[:, ::5] = -top
+    x[1::3, ::7] = top
+    x = x.clamp(-top, top).to(DT[dtype])
+    x[2::3, 3::4] = -np.inf
+    vals, at = x.sort(dim=1, descending=True, stable=True)
+    t = torch.tensor([(float("inf"), 3e38, 1.2e38, 1e38, 2e37, 1e36, 1.0)[r % 7] for r in range(rows)])
+    idx = (at * (n // k)).to(torch.int32)
+    lists = torch.empty(rows, k, device="cuda")
+    p = ts.ds_topk_softmax(vals.cuda(), idx.cuda(), n, temperature=t.cuda(), out_list=lists)
+    want = _softmax(vals, _np(t))
+    _close(lists, want, f"list {dtype}")
+    _close(p.gather(1, idx.cuda().long()), want, f"rows {dtype}")
+    assert (p != 0).sum().item() == (lists != 0).sum().item()

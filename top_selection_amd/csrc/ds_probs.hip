@@ -8,9 +8,14 @@ constexpr int kSoftWaves = 8;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLog2E = 1.44269504088896341f;
 
+// (v - m) * scale by way of half the difference: of two finite numbers that does not overflow.
+__device__ __forceinline__ float apart(float v, float m, float scale) {
+  return fmaf(v, 0.5f, m * -0.5f) * (scale + scale);
+}
+
 // exp((v - m) / t) with scale = log2(e) / t; exactly 1 at the maximum, infinities included.
 __device__ __forceinline__ float soft_exp(float v, float m, float scale) {
-  return v == m ? 1.0f : __builtin_amdgcn_exp2f((v - m) * scale);
+  return v == m ? 1.0f : __builtin_amdgcn_exp2f(apart(v, m, scale));
 }
 
 // (maximum, sum) of two parts of a row. A part without any mass is (-inf, 0).
@@ -33,7 +38,9 @@ __device__ __forceinline__ float2 wave_xor(float2 v, int o) {
 __device__ __forceinline__ float row_scale(const float* temperature, int64_t r, bool* greedy) {
   const float t = temperature ? temperature[r] : 1.0f;
   *greedy = !(t > 0.0f);
-  return *greedy ? 0.0f : fmaxf(kLog2E / t, 1e-37f);  // (above 0 at an infinite temperature: -inf keeps no mass)
+  // at an infinite temperature fp32's least number: -inf keeps no mass, and the largest difference there is
+  // moves an exponent by 1e-6
+  return *greedy ? 0.0f : fmaxf(kLog2E / t, __uint_as_float(1u));
 }
 
 // One workgroup per (row, slice): the slice's maximum and sum.
@@ -232,14 +239,14 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) top = most(top, v[j]);
     if (top != kNegInf) {
-      z *= __builtin_amdgcn_exp2f((m - top) * scale);
+      z *= __builtin_amdgcn_exp2f(apart(m, top, scale));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int64_t back = at + j * kStep - place64(at + j * kStep);
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          s += i >= back ? __builtin_amdgcn_exp2f((E::widen(v[j][i]) - top) * scale) : 0.0f;
+          s += i >= back ? __builtin_amdgcn_exp2f(apart(E::widen(v[j][i]), top, scale)) : 0.0f;
         z += s;
       }
     }
@@ -451,7 +458,7 @@ __global__ __launch_bounds__(kListThreads) void list_softmax_kernel(ListSoftmaxP
   if (LW > 1 || wave == 0) {
     const typename E::T* vals = static_cast<const typename E::T*>(p.vals) + r * p.k;
     const int32_t* idx = p.idx + r * p.k;
-    const float t = p.temperature ? fminf(p.temperature[r], 1e37f) : 1.0f;
+    const float t = p.temperature ? p.temperature[r] : 1.0f;
     const bool greedy = p.temperature && !(p.temperature[r] > 0.0f);
     const float top_p = p.top_p ? p.top_p[r] : 0.0f;
     int used = p.ks ? p.ks[r] : p.k;
@@ -487,7 +494,7 @@ __global__ __launch_bounds__(kListThreads) void list_softmax_kernel(ListSoftmaxP
       const bool live = at[j] >= 0 && m != kNegInf && (!greedy || base + j == first);
       e[j] = 0.0;
       if (j < per)  // (the same in every thread)
-        e[j] = !live ? 0.0
+        e[j] = !live || v[j] == kNegInf ? 0.0  // (at an infinite temperature too)
                : v[j] == m ? 1.0
                            : exp((static_cast<double>(v[j]) - static_cast<double>(m)) / static_cast<double>(t));
       mine += e[j];
