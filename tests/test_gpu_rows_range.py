@@ -137,3 +137,16 @@ def test_list_softmax_large_temperatures(dtype, rows, n, k):
     _close(lists, want, f"list {dtype}")
     _close(p.gather(1, idx.cuda().long()), want, f"rows {dtype}")
     assert (p != 0).sum().item() == (lists != 0).sum().item()
+
+
+@pytest.mark.parametrize("dtype,shape", EACH)
+def test_softmax_equal_logits_have_equal_probabilities(dtype, shape):
+    """A row's probabilities are a function of its logits that never falls: one sum divides all of them."""
+    rows, n = shape
+    t = 0.3 + torch.rand(rows, generator=_gen(rows))
+    x = torch.randn(rows, n, generator=_gen(n))
+    x = ((x * 8).round() / 8).to(DT[dtype]).cuda()
+    s, order = x.sort(dim=1)
+    p = ts.ds_softmax(x, temperature=t.cuda()).gather(1, order)
+    assert (p[:, 1:] >= p[:, :-1]).all()
+    assert torch.equal(p[:, 1:] == p[:, :-1], s[:, 1:] == s[:, :-1])

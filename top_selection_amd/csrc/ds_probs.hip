@@ -122,6 +122,9 @@ __global__ __launch_bounds__(kSoftWaves * 64) void softmax_write_kernel(SoftmaxP
     const float2 b = wave_xor(a, o);
     a = greedy ? first_join(a, b) : soft_join(a, b, scale);
   }
+  // (the lanes' joins round differently: one lane's sum is everyone's)
+  a.x = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(a.x)));
+  a.y = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(a.y)));
   const bool empty = a.x == kNegInf;
   const int64_t first = greedy && !empty ? static_cast<int64_t>(__float_as_uint(a.y)) : -1;
   const float inv = greedy || empty ? 0.0f : 1.0f / a.y;
