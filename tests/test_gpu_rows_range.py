@@ -150,3 +150,18 @@ def test_softmax_equal_logits_have_equal_probabilities(dtype, shape):
     p = ts.ds_softmax(x, temperature=t.cuda()).gather(1, order)
     assert (p[:, 1:] >= p[:, :-1]).all()
     assert torch.equal(p[:, 1:] == p[:, :-1], s[:, 1:] == s[:, :-1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,n", [(48, 1 << 25), (47, 1 << 26)])
+def test_softmax_sums_of_very_long_rows(rows, n, dtype):
+    """Rows of two values, so that every thread adds thousands of equal terms below its maximum's: one by one
+    in fp32 they would all be rounded to one side. (In one workgroup, in slices.)"""
+    c = -(torch.arange(rows) + 1) / 32  # exact in both types
+    x = c.to(DT[dtype]).cuda()[:, None].repeat(1, n)
+    x.view(rows, -1, 1 << 19)[:, :, :8192] = 0.0
+    p = ts.ds_softmax(x)
+    del x
+    e, ones = np.exp(_np(c)), (n >> 19) * 8192
+    total = ones + (n - ones) * e
+    _close(p[:, [0, 8192, n - 1]], np.stack([1 / total, e / total, e / total], axis=1), f"softmax {rows}x{n} {dtype}")

@@ -57,6 +57,7 @@ __global__ __launch_bounds__(kSoftWaves * 64) void softmax_stats_kernel(SoftmaxP
   const float scale = row_scale(p.temperature, r, &greedy);
   constexpr int N = E::kPer16;
   float2 a = make_float2(kNegInf, greedy ? __uint_as_float(0xFFFFFFFFu) : 0.0f);
+  double sum = 0.0;  // a thread's terms may be thousands: equal ones added in fp32 are all rounded to one side
   for (int64_t i = lo + static_cast<int64_t>(threadIdx.x) * N; i < hi; i += kSoftWaves * 64 * N) {
     float v[N];
     if (i + N <= hi) {
@@ -76,13 +77,15 @@ __global__ __launch_bounds__(kSoftWaves * 64) void softmax_stats_kernel(SoftmaxP
 #pragma unroll
       for (int j = 0; j < N; ++j) m = fmaxf(m, v[j]);
       if (m != kNegInf) {
-        float z = a.y * soft_exp(a.x, m, scale);
+        float z = 0.0f;
 #pragma unroll
         for (int j = 0; j < N; ++j) z += soft_exp(v[j], m, scale);
-        a = make_float2(m, z);
+        sum = sum * static_cast<double>(soft_exp(a.x, m, scale)) + static_cast<double>(z);
+        a.x = m;
       }
     }
   }
+  if (!greedy) a.y = static_cast<float>(sum);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
     const float2 b = wave_xor(a, o);
@@ -234,6 +237,9 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
   // A thread's running maximum may be any finite number (a mask), of which no product can be
   // rounded harmlessly: here the difference is taken first. (Infinite maxima and inverse
   // temperatures make NaN here; their rows are summed again below.)
+  // The sum is kept in double: a thread of a very long row has thousands of terms, and equal ones
+  // added in fp32 are all rounded to one side.
+  double past_sum = 0.0;
   for (int64_t at = past; at - mine < p.n; at += 4 * kStep) {
     VT v[4];
 #pragma unroll
@@ -242,20 +248,19 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) top = most(top, v[j]);
     if (top != kNegInf) {
-      z *= __builtin_amdgcn_exp2f(apart(m, top, scale));
+      float s = 0.0f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int64_t back = at + j * kStep - place64(at + j * kStep);
-        float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i)
           s += i >= back ? __builtin_amdgcn_exp2f(apart(E::widen(v[j][i]), top, scale)) : 0.0f;
-        z += s;
       }
+      past_sum = past_sum * static_cast<double>(__builtin_amdgcn_exp2f(apart(m, top, scale))) + static_cast<double>(s);
     }
     m = top;
   }
-  const float own = m;
+  const float own = m, own_sum = static_cast<float>(past_sum);
   // (places are worked out anew in each phase: kept, they would take a register per vector)
   asm volatile("" : "+v"(mine));
 #pragma unroll
@@ -316,14 +321,16 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
     return v;
   };
   if (!(fabsf(ms) < kFar)) {  // far logits, tiny temperatures, infinities: differences, element by element
-    z = 0.0f;
+    double sum = 0.0;
     for (int64_t i = mine; i < p.n; i += kStep) {
       const int64_t a = place64(i);
       const VT v = load(a);
+      float s = 0.0f;
 #pragma unroll
-      for (int j = 0; j < N; ++j) z += a + j >= i ? soft_exp(E::widen(v[j]), m, scale) : 0.0f;
+      for (int j = 0; j < N; ++j) s += a + j >= i ? soft_exp(E::widen(v[j]), m, scale) : 0.0f;
+      sum += static_cast<double>(s);
     }
-    const float inv = 1.0f / block_sum(z);
+    const float inv = 1.0f / block_sum(static_cast<float>(sum));
     for (int64_t i = mine + part * static_cast<int64_t>(kStep); i < p.n; i += static_cast<int64_t>(kStep) << p.together) {
       const int64_t a = place64(i);
       const VT v = load(a);
@@ -334,7 +341,6 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
     }
     return;
   }
-  z *= __builtin_amdgcn_exp2f(fmaf(own, scale, -ms));  // to what `term` gives
 #pragma unroll
   for (int j = 0; j < R; ++j) {
     const bool whole = (j + 1) * kStep <= n;
@@ -362,6 +368,7 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
     for (int j = 0; j < LV; ++j)
       z += sum_of(kept[j * THREADS + threadIdx.x], (R + j) * kStep + mine - place(R + j), ms);
   }
+  z += own_sum * __builtin_amdgcn_exp2f(fmaf(own, scale, -ms));  // to what `term` gives
   const float inv = 1.0f / block_sum(z);
   asm volatile("" : "+v"(mine));
   const auto store = [&](auto i, const float* q) {
