@@ -165,3 +165,25 @@ def test_softmax_sums_of_very_long_rows(rows, n, dtype):
     e, ones = np.exp(_np(c)), (n >> 19) * 8192
     total = ones + (n - ones) * e
     _close(p[:, [0, 8192, n - 1]], np.stack([1 / total, e / total, e / total], axis=1), f"softmax {rows}x{n} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_scales_past_the_scores(dtype, score):
+    """Renormalised weights whose scale divided by the scores' sum is past fp32 (the weights are not)."""
+    x = torch.randn(20, 48, generator=_gen(7))
+    bias = None
+    if score == "sigmoid":
+        x -= torch.tensor([20.0, 40.0, 60.0, 66.0]).repeat(5)[:, None]
+    else:  # the experts with mass are masked by their biases
+        x[:, :8] += torch.tensor([20.0, 40.0, 60.0, 66.0]).repeat(5)[:, None]
+        bias = torch.zeros(48)
+        bias[:8] = -np.inf
+    x = x.to(DT[dtype])
+    for scale in (1.0, 1e12, 3e38, -1e30, 1e-30):
+        w, i = ts.ds_route(x.cuda(), 5, bias=None if bias is None else bias.cuda(), score=ts.SCORE_SIGMOID if score == "sigmoid" else ts.SCORE_SOFTMAX,
+                           renormalize=True, scale=scale)
+        scale = float(np.float32(scale))
+        ww, wi = orc.route(_np(x), 5, None if bias is None else _np(bias), score, renormalize=True)
+        assert np.array_equal(_np(i), wi)
+        _close(w.double() / scale, ww, f"scale {scale}")

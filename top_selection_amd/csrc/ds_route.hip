@@ -1,4 +1,5 @@
 // Routing to experts and its gradient.
+#include <cmath>
 #include <type_traits>
 
 #include "ds_rows_device.h"
@@ -824,7 +825,10 @@ hipError_t route_mode(RouteParams p, hipStream_t s) {
   p.run = p.experts / groups;
   int need = 1;
   while (need < groups) need *= 2;
-  for (int lanes = 8; lanes <= 32 && p.k <= 16; lanes *= 2) {
+  // (a k that no list holds is left to the exact kernel; and scales past 1e8: the weights are
+  // s * (scale / total) with totals down to 1e-30, and the quotient would leave fp32)
+  const bool fast = p.k <= 16 && !(p.renorm && std::fabs(p.scale) > 1e8f);
+  for (int lanes = 8; lanes <= 32 && fast; lanes *= 2) {
     if (lanes < need) continue;
     const int of_group = lanes / need;
     p.per_lane = (p.run + of_group - 1) / of_group;
