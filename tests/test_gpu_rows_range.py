@@ -187,3 +187,16 @@ def test_route_scales_past_the_scores(dtype, score):
         ww, wi = orc.route(_np(x), 5, None if bias is None else _np(bias), score, renormalize=True)
         assert np.array_equal(_np(i), wi)
         _close(w.double() / scale, ww, f"scale {scale}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("k", [6, 700])
+def test_top_p_of_one_keeps_every_entry(dtype, k):
+    """The prefix that holds all of the mass is the list, entries below a double's step of it included."""
+    vals = torch.cat([torch.tensor([3.0, 2.0, -37.0, -40.0, -60.0]), -70 - torch.arange(k - 5) / 64]).to(DT[dtype])
+    vals = vals.repeat(4, 1).cuda()
+    idx = torch.arange(k, dtype=torch.int32, device="cuda").repeat(4, 1)
+    ks = torch.tensor([k, 5, 3, 1], dtype=torch.int32, device="cuda")
+    top_p = torch.tensor([1.0, 1.0, 1.5, 1.0], device="cuda")
+    got, want = (ts.ds_topk_softmax(vals, idx, 1000, ks=ks, top_p=q, rows_out=False) for q in (top_p, None))
+    assert torch.equal(got, want) and (got > 0).sum(dim=1).tolist() == ks.tolist()

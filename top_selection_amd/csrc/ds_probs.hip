@@ -523,7 +523,8 @@ __global__ __launch_bounds__(kListThreads) void list_softmax_kernel(ListSoftmaxP
       if constexpr (LW > 1) {
         for (int w = 0; w < wave; ++w) before += of_wave[w];
       }
-      const double most = static_cast<double>(top_p) * total;
+      // (all of the mass is in the whole list only, also where a double no longer shows an entry's share)
+      const double most = top_p >= 1.0f ? __builtin_huge_val() : static_cast<double>(top_p) * total;
       mine = 0.0;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
