@@ -387,7 +387,8 @@ int ds_route_grad(const void* x, int64_t rows, int64_t experts, int64_t row_stri
  * has probability 0, a row of -inf alone gives zeros, and +inf logits share the mass evenly.
  *   x            [rows, n] of dtype, 1 <= n <= 2^31 - 1.
  *   temperature  NULL (1 everywhere), or [rows] float on the device.
- *   out          [rows, n] of out_dtype, rows out_stride elements apart; does not overlap x.
+ *   out          [rows, n] of out_dtype, rows out_stride elements apart. Its rows share no memory
+ *                with x's (DS_ERR_INVALID_ARG; they may lie among them, as columns of one matrix do).
  *   workspace    ds_softmax_workspace_size bytes, 8-byte aligned (NULL when that is 0). Its
  *                contents on entry do not matter; calls that share it must not overlap in time.
  */

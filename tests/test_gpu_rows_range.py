@@ -200,3 +200,14 @@ def test_top_p_of_one_keeps_every_entry(dtype, k):
     top_p = torch.tensor([1.0, 1.0, 1.5, 1.0], device="cuda")
     got, want = (ts.ds_topk_softmax(vals, idx, 1000, ks=ks, top_p=q, rows_out=False) for q in (top_p, None))
     assert torch.equal(got, want) and (got > 0).sum(dim=1).tolist() == ks.tolist()
+
+
+def test_softmax_between_its_logits():
+    """Logits and probabilities as columns of one matrix share no memory; anything else is refused."""
+    wide = torch.randn(70, 1300, generator=_gen(3)).cuda()
+    want = ts.ds_softmax(wide[:, :640].clone())
+    got = ts.ds_softmax(wide[:, :640], out=wide[:, 650:1290])
+    assert torch.equal(got, want)
+    for out in (wide[:, :640], wide[:, 639:1279], wide[:, 1:641]):
+        with pytest.raises(ts.DSError):
+            ts.ds_softmax(wide[:, :640], out=out)

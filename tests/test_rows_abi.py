@@ -2,6 +2,7 @@
 structs match the header, and invalid calls are refused before the device is touched. Valid
 calls with no rows return at once."""
 import ctypes
+import random
 import re
 
 import pytest
@@ -166,3 +167,24 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
     for dim in (1, 3):
         with pytest.raises(ValueError):
             ts.ds_softmax(torch.zeros([2] * dim))
+
+
+@pytest.mark.parametrize("dtype,odtype", [(ts.FP32, ts.FP32), (ts.BF16, ts.BF16), (ts.BF16, ts.FP32)])
+def test_softmax_refuses_shared_memory_and_nothing_else(dtype, odtype):
+    """Against every pair of rows, one by one. Rows this long need a workspace, and without one a valid call is
+    refused for that: none gets as far as the device."""
+    rows, n = 3, 140000
+    xb, ob = (2 if d == ts.BF16 else 4 for d in (dtype, odtype))
+    rng = random.Random(dtype + 2 * odtype)
+    seen = set()
+    for case in range(400):
+        stride = n + rng.choice([0, 1, 9, n, 2 * n, 5 * n])
+        ostride = stride * xb // ob if case % 2 and stride * xb >= n * ob else n + rng.choice([0, 3, n, 3 * n])
+        x = 1 << 30
+        out = x + ob * rng.choice([-1, 0, 1, n, -n, n - 1, 1 - n, rng.randint(-6 * n, 6 * n), stride, -stride, stride + n])
+        meet = any(x + i * stride * xb < out + j * ostride * ob + n * ob and out + j * ostride * ob < x + i * stride * xb + n * xb
+                   for i in range(rows) for j in range(rows))
+        got = _softmax(x=x, out=out, rows=rows, n=n, stride=stride, ostride=ostride, dtype=dtype, odtype=odtype, ws=None)
+        assert got == (BAD if meet else ts.DS_ERR_WORKSPACE), (stride, ostride, out - x)
+        seen.add((meet, stride * xb == ostride * ob))
+    assert len(seen) == 4

@@ -1,6 +1,7 @@
 // C ABI of the operators beside the selection: argument validation (pure host code, before
 // any HIP call), launch cuts and dispatch.
 #include <cmath>
+#include <cstdlib>
 
 #include "ds_rows.h"
 
@@ -13,6 +14,28 @@ bool misaligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(
 // Rows of n elements, `stride` apart: sizes in range and the byte offsets in 63 bits.
 bool rows_ok(int64_t rows, int64_t n, int64_t stride) {
   return rows >= 0 && n >= 1 && n <= INT32_MAX && stride >= n && (rows == 0 || stride <= INT64_MAX / 4 / rows);
+}
+
+// Whether any of `rows` runs of a_len bytes, a_step apart from a on, shares a byte with any of those of b
+// (steps are not below lengths). Rows that lie among one another, as columns of one matrix do, need not.
+bool share_bytes(const void* a, int64_t a_step, int64_t a_len, const void* b, int64_t b_step, int64_t b_len,
+                 int64_t rows) {
+  // the distance of the first runs; runs i of a and j of b meet when d + j b_step - i a_step lies in (-b_len, a_len)
+  const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+  if (d >= (rows - 1) * a_step + a_len || -d >= (rows - 1) * b_step + b_len) return false;
+  if (rows == 1) return true;
+  if (a_step == b_step) {  // only the two differences j - i that bring d within one step of 0 can meet
+    int64_t t = -d / a_step;
+    if (-d % a_step < 0) --t;
+    return (std::llabs(t) < rows && d + t * a_step > -b_len) || (std::llabs(t + 1) < rows && d + (t + 1) * a_step < a_len);
+  }
+  for (int64_t i = 0, j = 0; i < rows && j < rows;) {
+    const int64_t at = d + j * b_step - i * a_step;
+    if (at >= a_len) ++i;
+    else if (at <= -b_len) ++j;
+    else return true;
+  }
+  return false;
 }
 
 int check_route(int64_t rows, int64_t experts, int64_t row_stride, int k, int dtype, const ds_route_config* cfg,
@@ -118,9 +141,10 @@ int ds_softmax(const void* x, int64_t rows, int64_t n, int64_t row_stride, int d
   if (!known(dtype) || !known(out_dtype)) return DS_ERR_INVALID_ARG;
   if (!rows_ok(rows, n, row_stride) || !rows_ok(rows, n, out_stride)) return DS_ERR_INVALID_ARG;
   if (rows == 0) return DS_OK;
-  if (!x || !out || x == out) return DS_ERR_INVALID_ARG;
-  if (misaligned(x, elem_bytes(dtype)) || misaligned(out, elem_bytes(out_dtype)) || misaligned(temperature, 4))
-    return DS_ERR_ALIGNMENT;
+  if (!x || !out) return DS_ERR_INVALID_ARG;
+  const int xb = elem_bytes(dtype), ob = elem_bytes(out_dtype);
+  if (misaligned(x, xb) || misaligned(out, ob) || misaligned(temperature, 4)) return DS_ERR_ALIGNMENT;
+  if (share_bytes(x, row_stride * xb, n * xb, out, out_stride * ob, n * ob, rows)) return DS_ERR_INVALID_ARG;
   const ds::RowCut c = ds::cut_softmax(rows, n, dtype);
   const int st = check_workspace(workspace, ws_bytes, softmax_bytes(rows, c));
   if (st != DS_OK) return st;
