@@ -372,7 +372,9 @@ int ds_route(const void* x, int64_t rows, int64_t experts, int64_t row_stride, i
  *                 slots without an expert. An expert that fills several slots of a row counts
  *                 once in S for each of them.
  *   grad_weights  [rows, k] float.
- *   grad_x        [rows, experts] of dtype, rows grad_stride elements apart; written whole.
+ *   grad_x        [rows, experts] of dtype, rows grad_stride elements apart; written whole. It may
+ *                 be x itself (grad_stride is row_stride then); otherwise its rows share no memory
+ *                 with x's (DS_ERR_INVALID_ARG).
  *   cfg           the forward call's (groups, topk_groups and group_top are checked the same
  *                 way and not used otherwise).
  */

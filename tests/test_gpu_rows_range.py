@@ -211,3 +211,31 @@ def test_softmax_between_its_logits():
     for out in (wide[:, :640], wide[:, 639:1279], wide[:, 1:641]):
         with pytest.raises(ts.DSError):
             ts.ds_softmax(wide[:, :640], out=out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,n,k", [(1, 9, 2), (300, 61, 6), (130, 256, 8), (50, 1024, 64)])
+def test_route_grad_over_its_logits(rows, n, k, dtype):
+    """The gradient may go over the logits: every row is read before it is written."""
+    full = torch.randn(rows, n + 3, generator=_gen(n)).to(DT[dtype]).cuda()
+    idx = torch.rand(rows, n, generator=_gen(k)).argsort(dim=1)[:, :k].to(torch.int32).contiguous().cuda()
+    g = torch.randn(rows, k, generator=_gen(k)).cuda()
+    for score in (ts.SCORE_SOFTMAX, ts.SCORE_SIGMOID):
+        for renorm in (False, True):
+            wide = full.clone()
+            x = wide[:, 2:n + 2]
+            want = ts.ds_route_grad(x, idx, g, score=score, renormalize=renorm)
+            got = ts.ds_route_grad(x, idx, g, score=score, renormalize=renorm, out=x)
+            assert got is x and torch.equal(got, want)
+            assert torch.equal(wide[:, :2], full[:, :2]) and torch.equal(wide[:, n + 2:], full[:, n + 2:])
+
+
+def test_route_grad_between_its_logits():
+    wide = torch.randn(100, 140, generator=_gen(5)).cuda()
+    x = wide[:, 3:64]
+    _, idx = ts.ds_route(x, 6)
+    g = torch.randn(100, 6, generator=_gen(6)).cuda()
+    want = ts.ds_route_grad(x, idx, g)
+    assert torch.equal(ts.ds_route_grad(x, idx, g, out=wide[:, 64:125]), want)
+    with pytest.raises(ts.DSError):
+        ts.ds_route_grad(x, idx, g, out=wide[:, 63:124])

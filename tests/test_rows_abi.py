@@ -188,3 +188,13 @@ def test_softmax_refuses_shared_memory_and_nothing_else(dtype, odtype):
         assert got == (BAD if meet else ts.DS_ERR_WORKSPACE), (stride, ostride, out - x)
         seen.add((meet, stride * xb == ostride * ob))
     assert len(seen) == 4
+
+
+@pytest.mark.parametrize("dtype", [ts.FP32, ts.BF16])
+def test_route_grad_refuses_shared_memory(dtype):
+    """Everything but x itself with its own stride."""
+    b = 2 if dtype == ts.BF16 else 4
+    x = 1 << 30
+    for out, stride, gstride in ((x + b, 64, 64), (x - 63 * b, 64, 64), (x + 101 * b, 164, 164), (x, 64, 65), (x, 100, 64),
+                                 (x + 4 * 64 * b - b, 64, 64), (x + 3 * 100 * b, 100, 64)):
+        assert _route_grad(x=x, out=out, stride=stride, gstride=gstride, dtype=dtype) == BAD, (out - x, stride, gstride)

@@ -111,9 +111,13 @@ int ds_route_grad(const void* x, int64_t rows, int64_t experts, int64_t row_stri
   if (!rows_ok(rows, experts, grad_stride)) return DS_ERR_INVALID_ARG;
   if (rows == 0) return DS_OK;
   if (!x || !idx || !grad_weights || !grad_x) return DS_ERR_INVALID_ARG;
-  if (misaligned(x, elem_bytes(dtype)) || misaligned(idx, 4) || misaligned(grad_weights, 4) ||
-      misaligned(grad_x, elem_bytes(dtype)))
+  const int eb = elem_bytes(dtype);
+  if (misaligned(x, eb) || misaligned(idx, 4) || misaligned(grad_weights, 4) || misaligned(grad_x, eb))
     return DS_ERR_ALIGNMENT;
+  // over x itself: the wave that writes a row has read it before
+  const bool over = x == grad_x && (row_stride == grad_stride || rows == 1);
+  if (!over && share_bytes(x, row_stride * eb, experts * eb, grad_x, grad_stride * eb, experts * eb, rows))
+    return DS_ERR_INVALID_ARG;
   (void)hipGetLastError();
   ds::RouteGradParams p{};
   p.x = x;
