@@ -431,8 +431,9 @@ int ds_topk_softmax(const void* vals, const int32_t* idx, int64_t rows, int k, i
  *                are certain (q_j is 1 at t_j and 0 elsewhere).
  *   draft_tokens [batch, drafts] int32 (NULL when drafts is 0). A token outside [0, n) is
  *                not accepted.
- *   draft_lens   NULL (all `drafts`), or [batch] int32, clamped to [0, drafts]; rows and tokens
- *                past a sequence's length are not read.
+ *   draft_lens   NULL (all `drafts`), or [batch] int32, clamped to [0, drafts]. Rows past a
+ *                sequence's length are not read; its tokens and numbers past it are, and may be
+ *                anything (draft_tokens and accept_u are whole [batch, drafts] arrays).
  *   accept_u     [batch, drafts] float in [0, 1) (NULL when drafts is 0); sample_u [batch].
  *   drafts       0 <= drafts <= DS_MAX_DRAFTS.
  *   out_tokens   [batch, drafts + 1] int32: the accepted drafts, the drawn token, then -1.

@@ -239,3 +239,25 @@ def test_route_grad_between_its_logits():
     assert torch.equal(ts.ds_route_grad(x, idx, g, out=wide[:, 64:125]), want)
     with pytest.raises(ts.DSError):
         ts.ds_route_grad(x, idx, g, out=wide[:, 63:124])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n", [700, 40001, 129280])
+def test_verify_past_a_drafts_end(dtype, n):
+    """What lies past a sequence's length takes no part: rows of NaN, tokens and numbers of any value."""
+    g = _gen(n)
+    B, K = 6, 4
+    target = torch.softmax(2 * torch.randn(B, K + 1, n, generator=g), dim=2).to(DT[dtype])
+    draft = torch.softmax(2 * torch.randn(B, K, n, generator=g), dim=2).to(DT[dtype])
+    tokens = draft.float().argmax(dim=2).to(torch.int32)
+    u, v = 0.3 * torch.rand(B, K, generator=g), torch.rand(B, generator=g)
+    lens = torch.tensor([0, 1, 2, 3, 4, 0], dtype=torch.int32)
+    want, wacc = orc.verify(_np(target), _np(draft), _np(tokens), _np(u), _np(v), _np(lens))
+    certain, cacc = orc.verify(_np(target), None, _np(tokens), _np(u), _np(v), _np(lens))
+    for b, m in enumerate(lens.tolist()):
+        target[b, m + 1:] = draft[b, m:] = u[b, m:] = float("nan")
+        tokens[b, m:] = torch.tensor([-2 ** 31, 2 ** 31 - 1, -1, n][:K - m], dtype=torch.int32)
+    got, acc = ts.ds_verify(target.cuda(), draft.cuda(), tokens.cuda(), u.cuda(), v.cuda(), draft_lens=lens.cuda())
+    assert np.array_equal(_np(got), want) and np.array_equal(_np(acc), wacc)
+    got, acc = ts.ds_verify(target.cuda(), None, tokens.cuda(), u.cuda(), v.cuda(), draft_lens=lens.cuda())
+    assert np.array_equal(_np(got), certain) and np.array_equal(_np(acc), cacc)
