@@ -589,9 +589,13 @@ static hipError_t softmax_out(SoftmaxParams p, hipStream_t s) {
     // few rows: several workgroups per row, each with its share of the stores and of the second
     // exponentials, but not so many that reading each row that often costs more (8 workgroups for
     // each of 7 rows of 50001 bf16 10.0 -> 7.9 us; 2 for 32 of 32000 fp32 change nothing, 4 take
-    // 7.0 us for 5.9)
-    if (vectors <= 1024 * 8)
-      while (p.together < 3 && p.rows << (p.together + 1) <= kCus / 4) ++p.together;
+    // 7.0 us for 5.9), nor more than the vectors that a thread may hold: they would store nothing. (With
+    // 5 to 7 of 8 vectors in the row, one to three of 8 workgroups store nothing: the other ones' single
+    // vectors still make it faster than 4 with two, 8 rows of 40960 bf16 6.2 and 6.45 us.)
+    if (vectors <= 1024 * 8) {
+      const int most = vectors <= 1024 * 4 ? 4 : 8;
+      while (2 << p.together <= most && p.rows << (p.together + 1) <= kCus / 4) ++p.together;
+    }
     if (vectors <= 1024 * 4) return launch_units(softmax_row_kernel<DT, OT, 1024, 4, 0>, p, p.rows << p.together, 1024, s);
     if (vectors <= 1024 * 8) return launch_units(softmax_row_kernel<DT, OT, 1024, 8, 0>, p, p.rows << p.together, 1024, s);
     constexpr bool kTwo = DT == DS_BF16;  // (two bytes an element)
