@@ -261,3 +261,14 @@ def test_verify_past_a_drafts_end(dtype, n):
     assert np.array_equal(_np(got), want) and np.array_equal(_np(acc), wacc)
     got, acc = ts.ds_verify(target.cuda(), None, tokens.cuda(), u.cuda(), v.cuda(), draft_lens=lens.cuda())
     assert np.array_equal(_np(got), certain) and np.array_equal(_np(acc), cacc)
+
+
+@pytest.mark.parametrize("shape", SHAPES["fp32"])
+def test_softmax_of_fp32s_least_differences(shape):
+    """Logits a few of fp32's least numbers apart, at temperatures that tell them apart and at ones whose inverse
+    is past fp32 (the limit: the maxima share the mass)."""
+    rows, n = shape
+    x = (2.0 ** -149 * torch.randint(-3, 1, (rows, n), generator=_gen(n)).double()).float()
+    t = torch.tensor([(1e-37, 2e-38, 1e-39, 1e-40, 1e-44)[r % 5] for r in range(rows)])
+    p = ts.ds_softmax(x.cuda(), temperature=t.cuda())
+    _close(p, _softmax(x, np.where(_np(t) < 4e-39, 1e-300, _np(t))), f"softmax {shape}")

@@ -8,9 +8,12 @@ constexpr int kSoftWaves = 8;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLog2E = 1.44269504088896341f;
 
-// (v - m) * scale by way of half the difference: of two finite numbers that does not overflow.
+// (v - m) * scale; by way of half the difference, which does not overflow for finite numbers, where the
+// product might be small all the same (and not elsewhere: half of fp32's least number is 0).
 __device__ __forceinline__ float apart(float v, float m, float scale) {
-  return fmaf(v, 0.5f, m * -0.5f) * (scale + scale);
+  const bool half = scale < 1.0f;
+  const float h = half ? 0.5f : 1.0f;
+  return fmaf(v, h, m * -h) * (half ? scale + scale : scale);
 }
 
 // exp((v - m) / t) with scale = log2(e) / t; exactly 1 at the maximum, infinities included.
