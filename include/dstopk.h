@@ -345,7 +345,8 @@ typedef struct ds_route_config {
  * An expert whose logit or bias is -inf is masked: it is never chosen and, with a logit of
  * -inf, takes no part in the softmax. A group's score counts its unmasked experts, and a group
  * without any is chosen after all others. Slots that no expert is left for hold index -1 and
- * weight 0, and weights whose scores sum to zero are 0. +inf is the limit (softmax: the +inf
+ * weight 0, and weights whose scores sum to zero are 0 (in double precision: a sigmoid is 0 below
+ * -745.13, a softmax's term that far below the row's maximum). +inf is the limit (softmax: the +inf
  * logits share the mass evenly). NaN: the row's output is unspecified.
  *   x            [rows, experts] of dtype, rows row_stride elements apart.
  *   experts      1 <= experts <= DS_MAX_EXPERTS; 1 <= k <= min(DS_MAX_ROUTE_K, experts).
@@ -366,8 +367,8 @@ int ds_route(const void* x, int64_t rows, int64_t experts, int64_t row_stride, i
  *     otherwise:    ds_e = h_e
  *     sigmoid:      dx_e = ds_e s_e (1 - s_e)
  *     softmax:      dx_e = s_e (ds_e - sum_i ds_i s_i), over all experts
- *   (the softmax with renormalize is zero for the experts that were not chosen). The bias has
- *   no gradient.
+ *   (the softmax with renormalize is zero for the experts that were not chosen, and is taken as
+ *   a softmax over the chosen ones alone, wherever the others are). The bias has no gradient.
  *   idx           [rows, k] int32: ds_route's out_idx; entries outside [0, experts) count as
  *                 slots without an expert. An expert that fills several slots of a row counts
  *                 once in S for each of them.

@@ -272,3 +272,33 @@ def test_softmax_of_fp32s_least_differences(shape):
     t = torch.tensor([(1e-37, 2e-38, 1e-39, 1e-40, 1e-44)[r % 5] for r in range(rows)])
     p = ts.ds_softmax(x.cuda(), temperature=t.cuda())
     _close(p, _softmax(x, np.where(_np(t) < 4e-39, 1e-300, _np(t))), f"softmax {shape}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_route_logits_of_a_finite_mask(dtype):
+    """Sigmoid scores that vanish in double: rows of masks alone have no weights and no gradient, rows with
+    some experts left have those. And the last scores that double holds."""
+    n, k = 48, 6
+    x = torch.randn(24, n, generator=_gen(71))
+    lows = [torch.finfo(DT[dtype]).min, -1e30, -1e10, -1000.0, -760.0, -720.0]
+    for r in range(24):
+        x[r, torch.randperm(n, generator=_gen(r))[(0, 3, 8, 48)[r // 6] if r % 6 < 5 else 0:]] = lows[r % 6]
+    x[5::6] += (4 * torch.rand(4, n, generator=_gen(72))).to(DT[dtype]).float()  # -720 to -716
+    x = x.to(DT[dtype])
+    g = torch.randn(24, k, generator=_gen(73))
+    for bias in (None, 0.1 * torch.randn(n, generator=_gen(74))):
+        w, i = ts.ds_route(x.cuda(), k, bias=None if bias is None else bias.cuda(), score=ts.SCORE_SIGMOID, renormalize=True)
+        ww, wi = orc.route(_np(x), k, None if bias is None else _np(bias), "sigmoid", renormalize=True)
+        assert np.array_equal(_np(i), wi)
+        _close(w, ww, "weights")
+        at = [r for r in range(24) if r % 6 < 5]  # (a division by the least of doubles overflows in the definition)
+        dx = _np(ts.ds_route_grad(x.cuda(), i, g.cuda(), score=ts.SCORE_SIGMOID, renormalize=True))
+        want, size = orc.route_grad(_np(x)[at], wi[at], _np(g)[at], "sigmoid", True, 1.0)
+        _close(torch.from_numpy(dx[at]), want, "gradient", size=4 * size, bf16=dtype == "bf16")
+        # (from the weights where the scores are ratios: dx_e = w_e (g_e - sum g w), 1 - s is 1)
+        for r in range(5, 24, 6):
+            d = np.zeros(n)
+            v = np.exp(_np(x)[r][wi[r]] + 720.0)
+            v = v / v.sum()
+            d[wi[r]] = v * (_np(g)[r] - (_np(g)[r] * v).sum())
+            _close(torch.from_numpy(dx[r:r + 1]), d[None], "gradient", size=np.full((1, n), 8.0), bf16=dtype == "bf16")

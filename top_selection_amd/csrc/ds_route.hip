@@ -93,10 +93,19 @@ __device__ __noinline__ void route_row_exact(const void* params, int64_t row, ui
 #pragma unroll
     for (int v = 0; v < V; ++v) s[v] *= inv;
   } else {
+    float least = xv[0];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       s[v] = 1.0 / (1.0 + exp(-static_cast<double>(xv[v])));
+      least = fminf(least, xv[v]);
       if (V > 4) __builtin_amdgcn_sched_barrier(0);
+    }
+    if (__any(least < -700.0f)) {  // exp(-x) overflows at 709: far below zero the score is exp(x)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (xv[v] < -700.0f) s[v] = exp(static_cast<double>(xv[v]));
+        if (V > 4) __builtin_amdgcn_sched_barrier(0);
+      }
     }
   }
   const bool limited = topk_groups < groups;
@@ -672,6 +681,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_grad_chosen_kernel(Rou
     }
     f = e >= 0 ? f : 0.0f;
     float s, slope;
+    bool none = false;  // no chosen expert has a score in double: there are no weights either
     if constexpr (SCORE == DS_SCORE_SOFTMAX) {
       const float m = row_reduce<LEVELS>(v, [](float a, float b) { return larger(a, b); });
       s = v == kNegInf ? 0.0f : v == m ? 1.0f : __builtin_amdgcn_exp2f((v - m) * kLog2E);
@@ -682,6 +692,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_grad_chosen_kernel(Rou
       float unit = 0.0f;
       if (p.renorm) {
         unit = row_reduce<LEVELS>(v, [](float a, float b) { return larger(a, b); });
+        none = unit < -745.1332f;
         unit = unit < 0.0f && unit > kNegInf ? unit : 0.0f;
       }
       const float part = 1.0f / (1.0f + __builtin_amdgcn_exp2f(fabsf(v) * -kLog2E));
@@ -691,7 +702,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_grad_chosen_kernel(Rou
     float d = f;
     if (p.renorm) {
       const float S = row_reduce<LEVELS>(s, plus<float>), fs = row_reduce<LEVELS>(f * s, plus<float>);
-      d = S > 0.0f ? (f - fs / S) / S : 0.0f;
+      d = S > 0.0f && !none ? (f - fs / S) / S : 0.0f;
     }
     const int place = e >= 0 ? row * pitch + e : -1;
     if (place >= 0) atomicAdd(tile + place, d * slope);
