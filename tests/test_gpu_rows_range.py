@@ -302,3 +302,38 @@ def test_route_logits_of_a_finite_mask(dtype):
             v = v / v.sum()
             d[wi[r]] = v * (_np(g)[r] - (_np(g)[r] * v).sum())
             _close(torch.from_numpy(dx[r:r + 1]), d[None], "gradient", size=np.full((1, n), 8.0), bf16=dtype == "bf16")
+
+
+MEAN = 2.0 ** -19  # 32 u, u = 2^-24 as in test_gpu_rows.py
+
+
+def _mean_close(got, want, label):
+    """The mean relative error of a row's fp32 numbers. The roundings are independent of each other and at most
+    u, so their squares' mean is at most u^2 / 3, and errors add as their squares: 3 in an exponent, 8 at most
+    here with its distance from the maximum (3 * 64 / 3 = 64 u^2), 140 additions on the path of a sum (47), the
+    sum's own exponents (64 again, were they all alike), exp2, two divisions and a product (4): 180 u^2, the
+    square of 13.4 u. The mean is not above the root of the mean square; 32 u is 2.4 times that."""
+    got, want = _np(got), np.asarray(want)
+    live = want > 0
+    err = np.where(live, np.abs(got - want) / np.where(live, want, 1), 0).sum(axis=1) / np.maximum(live.sum(axis=1), 1)
+    assert err.max() < MEAN, f"{label}: {err.max() * 2 ** 24} u"
+
+
+@pytest.mark.parametrize("dtype,shape", EACH)
+def test_softmax_mean_error(dtype, shape):
+    rows, n = shape
+    x = torch.randn(rows, n, generator=_gen(n)).clamp(-4, 4).to(DT[dtype])
+    _mean_close(ts.ds_softmax(x.cuda()), _softmax(x, 1.0), f"softmax {shape} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,k,groups,tg", [(256, 8, 8, 4), (61, 6, 1, 1), (1024, 16, 1, 1), (256, 20, 1, 1)])
+def test_route_mean_error(n, k, groups, tg, dtype):
+    """The chosen experts' weights, over all rows at once (a row has few)."""
+    x = torch.randn(300, n, generator=_gen(n)).clamp(-4, 4).to(DT[dtype])
+    for name, code in (("softmax", ts.SCORE_SOFTMAX), ("sigmoid", ts.SCORE_SIGMOID)):
+        for renorm in (False, True):
+            w, i = ts.ds_route(x.cuda(), k, score=code, groups=groups, topk_groups=tg, renormalize=renorm, scale=2.5)
+            ww, wi = orc.route(_np(x), k, None, name, groups, tg, 1, renorm, 2.5)
+            assert np.array_equal(_np(i), wi)
+            _mean_close(w.reshape(1, -1), ww.reshape(1, -1), f"route {name} {renorm}")
