@@ -404,9 +404,9 @@ int ds_softmax_workspace_size(int64_t rows, int64_t n, int dtype, size_t* bytes)
  *   The list (vals, idx) is ds_topk's: sorted by value, larger first, distinct indices, padded
  *   with index -1.
  *   Row r uses its first ks[r] entries (clamped to [1, k]); top_p keeps the shortest prefix
- *   of those whose mass reaches top_p[r] of theirs (at least one entry); the kept entries'
- *   probabilities sum to 1. Temperatures and infinities as in ds_softmax. The prefix is
- *   decided in double precision.
+ *   of those whose mass reaches top_p[r] of theirs (at least one entry, and all of them for a top_p
+ *   of 1 or more); the kept entries' probabilities sum to 1. Temperatures and infinities as in
+ *   ds_softmax. The prefix is decided in double precision.
  *   vals         [rows, k] of dtype; idx [rows, k] int32 (entries outside [0, n) are skipped in
  *                `out` and have no mass, like ds_topk's padding). 1 <= k <= DS_MAX_K.
  *   ks, temperature, top_p  NULL, or [rows] on the device (int32, float, float).

@@ -441,6 +441,8 @@ def ds_route(x, k: int, bias=None, score: int = SCORE_SOFTMAX, groups: int = 1, 
 
     Returns (weights [rows, k] fp32 or None, indices [rows, k] int32). bias: fp32 [experts],
     moves the choice only. counts: int32 [experts], gets the rows that chose each expert added.
+    Outside torch's autograd, as every call here: an x that requires a gradient gets it from
+    ds_route_grad, which the caller's backward pass calls.
     """
     torch = _torch()
     rows, n, rs = _matrix(x, "x")
@@ -467,7 +469,7 @@ def ds_route(x, k: int, bias=None, score: int = SCORE_SOFTMAX, groups: int = 1, 
 def ds_route_grad(x, idx, grad_weights, score: int = SCORE_SOFTMAX, renormalize: bool = False, scale: float = 1.0,
                   out=None, stream=None):
     """The gradient of ds_route's weights to its logits x, for the chosen experts idx [rows, k]
-    int32 and the weights' gradient [rows, k] fp32; [rows, experts] of x's dtype."""
+    int32 and the weights' gradient [rows, k] fp32; [rows, experts] of x's dtype. out may be x."""
     torch = _torch()
     rows, n, rs = _matrix(x, "x")
     dt, dev = _code(x.dtype), x.device
@@ -500,7 +502,7 @@ def _out_rows(out, out_dtype, rows: int, n: int, dev, stream):
 def ds_softmax(x, temperature=None, out_dtype=None, out=None, workspace=None, stream=None):
     """Probabilities [rows, n] (fp32, or out_dtype / out's type) of the logits x [rows, n] (bf16
     or fp32) at a temperature per row (fp32 [rows] on the device; not above 0: one-hot at the
-    first maximum); see include/dstopk.h."""
+    first maximum); see include/dstopk.h. out shares no memory with x."""
     torch = _torch()
     rows, n, rs = _matrix(x, "x")
     dt, dev = _code(x.dtype), x.device

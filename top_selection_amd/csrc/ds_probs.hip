@@ -379,8 +379,8 @@ __global__ __launch_bounds__(THREADS) void softmax_row_kernel(SoftmaxParams p) {
 #pragma unroll
     for (int j = 0; j < N; ++j) o[j] = O::narrow(q[j]);
     const auto to = reinterpret_cast<typename W::unaligned*>(out + i);
-    // past the caches, which keep more of the logits (50.1 -> 48.8 us for 256 x 129280 fp32), where a
-    // store writes whole lines (two stores of bf16 to fp32 share one: 26.9 -> 32.3 us at 128 rows)
+    // past the caches, which keep more of the logits (256 x 129280 fp32: a call after another into one
+    // buffer 50.3 -> 48.4 us, from a graph into 15 in turn 56.5 -> 53.8), where a store writes whole lines (two stores of bf16 to fp32 share one: 26.9 -> 32.3 us at 128 rows)
     if constexpr (sizeof(o) <= 16) __builtin_nontemporal_store(o, to);
     else *to = o;
   };
