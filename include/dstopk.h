@@ -449,6 +449,170 @@ int ds_verify(const void* target, int64_t target_stride, const void* draft, int6
               void* workspace, size_t ws_bytes, void* stream);
 int ds_verify_workspace_size(int64_t batch, int64_t n, int dtype, size_t* bytes);
 
+/* ------------------------------------------------------------------------------------------
+ * Behind a router: the slots of ds_route's choice sorted by expert, rows gathered to their
+ * experts and combined back with their weights (with the gradients), blocks of 128 quantised to
+ * 8-bit floats, and the experts' products of such operands. The conventions of the operators
+ * above hold. Offsets into all arrays are 64-bit; a slot is (row, j), numbered row * k + j.
+ */
+
+/* 8-bit element types: e4m3 (no infinities, largest 448) and e5m2 (IEEE-like, largest 57344) */
+#define DS_E4M3 2
+#define DS_E5M2 3
+
+#define DS_BLOCK 128 /* elements that share a scale */
+#define DS_MAX_EXPERT_ALIGN 1024
+
+/*
+ * Where the slots of rows [rows, k] lie when sorted by expert. All arrays are on the device;
+ * ds_expert_sort writes them and the other entries read them.
+ *   place     [rows, k]: the slot's position, or -1 (a slot without an expert).
+ *   order     [capacity]: the position's slot, or -1 (padding, and everything past the end).
+ *   offsets   [experts + 1]: expert e has the positions [offsets[e], offsets[e + 1]), a multiple
+ *             of `align` long; offsets[experts] is the end.
+ *   capacity  at least ds_expert_capacity's.
+ *   k         1 <= k <= DS_MAX_ROUTE_K; 1 <= experts <= DS_MAX_EXPERTS;
+ *             1 <= align <= DS_MAX_EXPERT_ALIGN; rows * k and capacity below 2^31.
+ */
+typedef struct ds_expert_plan {
+  int32_t* place;
+  int32_t* order;
+  int32_t* offsets;
+  int64_t rows;
+  int64_t capacity;
+  int32_t k;
+  int32_t experts;
+  int32_t align;
+} ds_expert_plan;
+
+/* ds_expert_capacity -- positions that hold every choice of experts (host only): each of at most
+ * min(rows * k, experts) segments with a slot may end in align - 1 positions of padding. */
+int ds_expert_capacity(int64_t rows, int k, int experts, int align, int64_t* capacity);
+
+/*
+ * ds_expert_sort -- writes the plan's arrays whole for the experts idx [rows, k] (ds_route's
+ * out_idx; entries outside [0, experts) are slots without an expert). An expert's slots keep their
+ * order, so the result does not depend on timing. An expert may fill several slots of a row.
+ *   idx        may not share memory with the plan's arrays, nor those with one another.
+ *   workspace  ds_expert_sort_workspace_size bytes, 8-byte aligned, as in ds_softmax.
+ * rows == 0 writes offsets of 0 and an order of -1.
+ */
+int ds_expert_sort(const int32_t* idx, const ds_expert_plan* plan, void* workspace, size_t ws_bytes, void* stream);
+int ds_expert_sort_workspace_size(int64_t rows, int k, int experts, size_t* bytes);
+
+/*
+ * The entries below take a plan. Positions and slots that a broken plan has out of range are
+ * skipped (read as -1), and its offsets are clamped to [0, capacity]. "The plan's positions" are
+ * those below offsets[experts]; rows of outputs at and past it are left as they were.
+ *
+ * ds_expert_gather -- every row to its slots' positions: out[p] = x[order[p] / k], bit by bit, and
+ * zeros in padding. Its gradient is ds_expert_combine without weights.
+ *   x    [rows, n] of dtype (DS_BF16 or DS_FP32), rows row_stride elements apart.
+ *   out  [capacity, n] of dtype, rows out_stride elements apart; shares no memory with x
+ *        (DS_ERR_INVALID_ARG if the two ranges meet).
+ */
+int ds_expert_gather(const void* x, int64_t n, int64_t row_stride, int dtype, const ds_expert_plan* plan, void* out,
+                     int64_t out_stride, void* stream);
+
+/*
+ * ds_expert_combine -- the rows back: out[r] = sum over j of weights[r, j] * y[place[r, j]], in fp32
+ * by one fused multiply-add a slot, j upwards from 0, rounded once. Slots without a position add nothing
+ * (their weight, whatever it is, is not looked at); a row of none is 0.
+ *   y        [capacity, n] of dtype, rows y_stride elements apart.
+ *   weights  NULL (all 1), or [rows, k] float.
+ *   out      [rows, n] of dtype, rows out_stride elements apart; shares no memory with y.
+ */
+int ds_expert_combine(const void* y, int64_t n, int64_t y_stride, int dtype, const ds_expert_plan* plan,
+                      const float* weights, void* out, int64_t out_stride, void* stream);
+
+/*
+ * ds_expert_combine_grad -- the gradients of ds_expert_combine, with g the gradient of its out:
+ *   grad_y[place[r, j]] = weights[r, j] * g[r], zeros in padding (written for the plan's positions);
+ *   grad_weights[r, j] = sum over i of g[r, i] * y[place[r, j], i], 0 for slots without a position.
+ *   g             [rows, n] of dtype, rows g_stride elements apart.
+ *   y             the forward call's (not read, and may be NULL, when grad_weights is NULL).
+ *   weights       NULL (all 1), or [rows, k] float.
+ *   grad_y        NULL, or [capacity, n] of dtype, rows grad_stride elements apart. It may be y itself
+ *                 (grad_stride is y_stride then); otherwise it shares no memory with y, and never with g.
+ *   grad_weights  NULL, or [rows, k] float. Not both NULL.
+ */
+int ds_expert_combine_grad(const void* g, int64_t g_stride, const void* y, int64_t y_stride, int64_t n, int dtype,
+                           const ds_expert_plan* plan, const float* weights, void* grad_y, int64_t grad_stride,
+                           float* grad_weights, void* stream);
+
+/* how ds_block_quantize's blocks lie */
+#define DS_BLOCK_ROW 0    /* 1 x 128 along the rows */
+#define DS_BLOCK_COLUMN 1 /* 128 x 1 along the columns, written transposed */
+#define DS_BLOCK_TILE 2   /* 128 x 128 */
+
+/*
+ * ds_block_quantize -- 8-bit floats with a scale for each block of 128:
+ *   scale = max(|block|, 2^-100) / largest of q_dtype, in fp32;  q = x / scale, correctly rounded to
+ *   fp32 and then to nearest even.
+ * A block that holds an infinity or a NaN has scale NaN and q of 0, so all that is computed from it is
+ * NaN. Blocks start at multiples of 128; the last of a row may be shorter. With P the positions
+ * (the plan's capacity, or rows without a plan) and ceil16 the next multiple of 16:
+ *   DS_BLOCK_ROW     q [P, ceil16(n)], scales [P, ceil(n / 128)]. With a plan (whose rows are x's) row p
+ *                    is x[order[p] / k], and zeros in padding.
+ *   DS_BLOCK_COLUMN  q [n, ceil16(P)], scales [n, ceil(P / 128)]: the same rows, transposed; a scale
+ *                    for 128 positions of one column. With a plan, its align is a multiple of 128, so that
+ *                    no block meets two experts.
+ *   DS_BLOCK_TILE    q [rows, ceil16(n)], scales [ceil(rows / 128), ceil(n / 128)], without a plan.
+ * What a plan's end leaves over (whole rows of q and scales, or columns) is left as it was; elements of q
+ * from n (P) to its ceil16 are written as 0.
+ *   x         [rows, n] of dtype (DS_BF16 or DS_FP32), rows row_stride elements apart.
+ *   q         rows q_stride bytes apart; q and q_stride are multiples of 16 (DS_ERR_ALIGNMENT).
+ *   q_dtype   DS_E4M3 or DS_E5M2.
+ *   scales    contiguous float. q and scales share no memory with x or one another.
+ */
+int ds_block_quantize(const void* x, int64_t rows, int64_t n, int64_t row_stride, int dtype, int layout,
+                      const ds_expert_plan* plan, void* q, int64_t q_stride, int q_dtype, float* scales, void* stream);
+
+/* how ds_block_product's groups lie */
+#define DS_GROUP_NONE 0
+#define DS_GROUP_ROWS 1
+#define DS_GROUP_INNER 2
+
+/*
+ * One side of ds_block_product: 8-bit rows along the inner axis and their scales.
+ *   q           rows `stride` bytes apart; q and stride are multiples of 16.
+ *   scales      contiguous float: [rows, ceil(k / 128)], or with scale_rows of 128 [groups, ceil(n / 128),
+ *               ceil(k / 128)].
+ *   dtype       DS_E4M3 or DS_E5M2 (b: DS_E4M3 only, DS_ERR_UNSUPPORTED otherwise).
+ *   scale_rows  1, or (b only, and not with DS_GROUP_INNER) 128.
+ */
+typedef struct ds_block_operand {
+  const void* q;
+  const float* scales;
+  int64_t stride;
+  int32_t dtype;
+  int32_t scale_rows;
+} ds_block_operand;
+
+/*
+ * ds_block_product -- out = a b^T of operands in blocks of 128 along the inner axis:
+ *   out[i, j] = sum over blocks t of a.scale[i, t] * b.scale[j, t] * (sum over the block of a.q[i, .] * b.q[j, .])
+ * with sums in fp32, rounded once to out_dtype.
+ *   DS_GROUP_NONE   a [m, k], b [n, k], out [m, n]; groups is 1 and offsets NULL.
+ *   DS_GROUP_ROWS   the rows of a and out are in `groups` segments, row i in [offsets[g], offsets[g + 1])
+ *                   with b's group g: b [groups, n, k] (n rows `stride` bytes apart after another). Rows
+ *                   outside [offsets[0], offsets[groups]) are left as they were.
+ *   DS_GROUP_INNER  the inner axis is in segments: out [groups, m, n], group g the sum over
+ *                   [offsets[g], offsets[g + 1]) only, 0 where that is empty. Segments start and end at
+ *                   multiples of 128 (others count as the next multiple); a.scale_rows and b.scale_rows are 1.
+ * Offsets (device, [groups + 1]) rise from [0]; they are clamped to [0, m] ([0, k]), and a segment that
+ * ends before it starts is empty. Segments that overlap leave the shared rows unspecified.
+ *   m, n        1 <= n < 2^31, 0 <= m < 2^31; 1 <= groups <= DS_MAX_EXPERTS.
+ *   k           a multiple of 16 (DS_ERR_ALIGNMENT otherwise) below 2^31; with 0 the operands are not looked
+ *               at and the sums are 0.
+ *   out         [m, n] ([groups, m, n]) of out_dtype (DS_BF16 or DS_FP32), rows out_stride elements
+ *               apart; shares no memory with the operands.
+ * The gradients are products too: a's is g b, with g quantised along its rows and b's q and scales transposed
+ * (tiles stay tiles); b's is g^T a, with both quantised in columns (DS_BLOCK_COLUMN) and the tokens as inner axis.
+ */
+int ds_block_product(const ds_block_operand* a, const ds_block_operand* b, int64_t m, int64_t n, int64_t k, int group,
+                     int groups, const int32_t* offsets, void* out, int64_t out_stride, int out_dtype, void* stream);
+
 /*
  * ds_probe_read -- measurement aid, not part of top-k (tutorial chapter 37, section 6.1: the
  * method's measure is how close it comes to reading the input once; this is the plain read

@@ -11,4 +11,7 @@ from ._binding import (BF16, DS_ERR_ALIGNMENT, DS_ERR_DEVICE, DS_ERR_INVALID_ARG
                        SCORE_SOFTMAX, SCORE_SIGMOID, DS_MAX_EXPERTS, DS_MAX_ROUTE_K, DS_MAX_ROUTE_GROUPS, DS_MAX_DRAFTS,
                        DSError, decode_stats, ds_probe_copy, ds_probe_read, ds_status_string, ds_topk, ds_topk_ex,
                        ds_topk_merge, ds_topk_noalloc, ds_topk_plan, ds_topk_slices, ds_topk_workspace_size, dtype_code, ds_route, ds_route_grad, ds_softmax,
-                       ds_softmax_workspace_size, ds_topk_softmax, ds_verify, ds_verify_workspace_size, header_functions, lib, stats_buffer)
+                       ds_softmax_workspace_size, ds_topk_softmax, ds_verify, ds_verify_workspace_size, header_functions, lib, stats_buffer,
+                       E4M3, E5M2, DS_BLOCK, DS_MAX_EXPERT_ALIGN, BLOCK_ROW, BLOCK_COLUMN, BLOCK_TILE, GROUP_NONE, GROUP_ROWS,
+                       GROUP_INNER, ExpertPlan, ds_expert_capacity, ds_expert_sort, ds_expert_sort_workspace_size,
+                       ds_expert_gather, ds_expert_combine, ds_expert_combine_grad, ds_block_quantize, ds_block_product)

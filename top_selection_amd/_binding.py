@@ -10,12 +10,14 @@ import ctypes
 import os
 import re
 import threading
-from typing import Dict, Optional, Tuple
+from typing import Dict, NamedTuple, Optional, Tuple
 
 import numpy as np
 
 BF16 = 0
 FP32 = 1
+E4M3 = 2
+E5M2 = 3
 
 DS_OK = 0
 DS_ERR_INVALID_ARG = -1
@@ -36,6 +38,10 @@ DS_MAX_EXPERTS = 1024
 DS_MAX_ROUTE_K = 64
 DS_MAX_ROUTE_GROUPS = 64
 DS_MAX_DRAFTS = 64
+DS_BLOCK = 128
+DS_MAX_EXPERT_ALIGN = 1024
+BLOCK_ROW, BLOCK_COLUMN, BLOCK_TILE = 0, 1, 2
+GROUP_NONE, GROUP_ROWS, GROUP_INNER = 0, 1, 2
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # DS_LIBRARY names another build of the library (e.g. one with host-side sanitizers)
@@ -60,6 +66,17 @@ class ds_config(ctypes.Structure):
 class ds_route_config(ctypes.Structure):
     _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
                 ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class ds_expert_plan(ctypes.Structure):
+    _fields_ = [("place", ctypes.c_void_p), ("order", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("capacity", ctypes.c_int64), ("k", ctypes.c_int32),
+                ("experts", ctypes.c_int32), ("align", ctypes.c_int32)]
+
+
+class ds_block_operand(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("scale_rows", ctypes.c_int32)]
 
 
 STATS_FIELDS = ["appended", "compactions", "work", "max_len", "reads", "index_sum", "monotone", "slice_lo",
@@ -116,6 +133,23 @@ def lib() -> ctypes.CDLL:
             L.ds_verify.restype = ci
             L.ds_verify_workspace_size.argtypes = [i64, i64, ci, szp]
             L.ds_verify_workspace_size.restype = ci
+            plp, opp = ctypes.POINTER(ds_expert_plan), ctypes.POINTER(ds_block_operand)
+            L.ds_expert_capacity.argtypes = [i64, ci, ci, ci, ctypes.POINTER(i64)]
+            L.ds_expert_capacity.restype = ci
+            L.ds_expert_sort.argtypes = [vp, plp, vp, sz, vp]
+            L.ds_expert_sort.restype = ci
+            L.ds_expert_sort_workspace_size.argtypes = [i64, ci, ci, szp]
+            L.ds_expert_sort_workspace_size.restype = ci
+            L.ds_expert_gather.argtypes = [vp, i64, i64, ci, plp, vp, i64, vp]
+            L.ds_expert_gather.restype = ci
+            L.ds_expert_combine.argtypes = [vp, i64, i64, ci, plp, vp, vp, i64, vp]
+            L.ds_expert_combine.restype = ci
+            L.ds_expert_combine_grad.argtypes = [vp, i64, vp, i64, i64, ci, plp, vp, vp, i64, vp, vp]
+            L.ds_expert_combine_grad.restype = ci
+            L.ds_block_quantize.argtypes = [vp, i64, i64, i64, ci, ci, plp, vp, i64, ci, vp, vp]
+            L.ds_block_quantize.restype = ci
+            L.ds_block_product.argtypes = [opp, opp, i64, i64, i64, ci, ci, vp, vp, i64, ci, vp]
+            L.ds_block_product.restype = ci
             L.ds_status_string.argtypes = [ci]
             L.ds_status_string.restype = ctypes.c_char_p
             _lib = L
@@ -582,6 +616,258 @@ def ds_verify(target, draft, draft_tokens, accept_u, sample_u, draft_lens=None, 
           _operand(accept_u, "accept_u", f32, each, dev), _operand(sample_u, "sample_u", f32, per_seq, dev),
           batch, K, n, dt, tp, ap, ws, ws_bytes)
     return out_tokens, out_accepted
+
+
+# ------------------------------------------------------------------------- behind a router
+class ExpertPlan(NamedTuple):
+    """Where the slots of rows [rows, k] lie when sorted by expert (see include/dstopk.h): int32
+    device tensors place [rows, k] (a slot's position, or -1), order [capacity] (a position's slot, or
+    -1) and offsets [experts + 1]; every expert's segment is a multiple of align long."""
+    place: object
+    order: object
+    offsets: object
+    align: int = 1
+
+
+def _plan(plan: ExpertPlan, device):
+    """The plan as the C entries take it, its rows and its capacity."""
+    i32 = _torch().int32
+    place, order, offsets, align = plan
+    for t, what, dims in ((place, "place", 2), (order, "order", 1), (offsets, "offsets", 1)):
+        if t.dtype != i32 or t.dim() != dims or t.device != device or not t.is_contiguous():
+            raise ValueError(f"the plan's {what} must be a contiguous int32 tensor of {dims} dimensions on {device}")
+    rows, k = place.shape
+    capacity = order.shape[0]
+    return ds_expert_plan(place.data_ptr(), order.data_ptr(), offsets.data_ptr(), rows, capacity, k,
+                          offsets.shape[0] - 1, align), rows, capacity
+
+
+def ds_expert_capacity(rows: int, k: int, experts: int, align: int = 1) -> int:
+    """The length of a plan's order: positions that hold every choice of experts."""
+    c = ctypes.c_int64(0)
+    st = _function("ds_expert_capacity")(rows, k, experts, align, ctypes.byref(c))
+    if st != DS_OK:
+        raise DSError(st, "ds_expert_capacity")
+    return int(c.value)
+
+
+def ds_expert_sort_workspace_size(rows: int, k: int, experts: int) -> int:
+    return _workspace_size("ds_expert_sort_workspace_size", rows, k, experts)
+
+
+def ds_expert_sort(idx, experts: int, align: int = 1, out: Optional[ExpertPlan] = None, workspace=None,
+                   stream=None) -> ExpertPlan:
+    """The slots of idx [rows, k] (int32, as ds_route returns them) sorted by expert; entries outside
+    [0, experts) are slots without an expert. out: a plan of the same sizes whose tensors are written."""
+    torch = _torch()
+    if idx.dim() != 2 or idx.dtype != torch.int32 or not idx.is_cuda or not idx.is_contiguous():
+        raise ValueError("idx must be a contiguous 2-D int32 device tensor [rows, k]")
+    (rows, k), dev = idx.shape, idx.device
+    if out is None:
+        out = ExpertPlan(_empty((rows, k), torch.int32, dev, stream),
+                         _empty((ds_expert_capacity(rows, k, experts, align),), torch.int32, dev, stream),
+                         _empty((experts + 1,), torch.int32, dev, stream), align)
+    elif out.place.shape != idx.shape or out.offsets.shape != (experts + 1,) or out.align != align:
+        raise ValueError("out must be a plan of idx's shape, of the experts and of the alignment")
+    plan, _, _ = _plan(out, dev)
+    keep, ws, ws_bytes = _scratch(ds_expert_sort_workspace_size(rows, k, experts), workspace, dev, stream)
+    _call("ds_expert_sort", dev, stream, idx.data_ptr(), ctypes.byref(plan), ws, ws_bytes)
+    return out
+
+
+def _rows_out(out, rows: int, n: int, dtype, dev, stream, what: str = "out"):
+    """An output matrix and its row stride: the one given, or a new one."""
+    if out is None:
+        return _empty((rows, n), dtype, dev, stream), n
+    _, _, stride = _matrix(out, what)
+    if out.shape != (rows, n) or out.dtype != dtype or out.device != dev:
+        raise ValueError(f"{what} must be a [{rows}, {n}] tensor of {dtype} on {dev}")
+    return out, stride
+
+
+def ds_expert_gather(x, plan: ExpertPlan, out=None, stream=None):
+    """Every row of x [rows, n] (bf16 or fp32) at its slots' positions: [capacity, n], zeros in the
+    segments' padding, and from the plan's end on what out held (uninitialised in a new tensor). Its
+    gradient is ds_expert_combine without weights."""
+    rows, n, rs = _matrix(x, "x")
+    dt, dev = _code(x.dtype), x.device
+    c, plan_rows, capacity = _plan(plan, dev)
+    if plan_rows != rows:
+        raise ValueError("x must have the plan's rows")
+    out, os = _rows_out(out, capacity, n, x.dtype, dev, stream)
+    _call("ds_expert_gather", dev, stream, x.data_ptr(), n, rs, dt, ctypes.byref(c), out.data_ptr(), os)
+    return out
+
+
+def ds_expert_combine(y, plan: ExpertPlan, weights=None, out=None, stream=None):
+    """The rows back: [rows, n], row r the sum of weights[r, j] (fp32; None: 1) times y's row at slot
+    (r, j)'s position, y [capacity, n] (bf16 or fp32). The gradient is ds_expert_combine_grad."""
+    capacity, n, ys = _matrix(y, "y")
+    dt, dev = _code(y.dtype), y.device
+    c, rows, plan_capacity = _plan(plan, dev)
+    if plan_capacity != capacity:
+        raise ValueError("y must have the plan's capacity of rows")
+    out, os = _rows_out(out, rows, n, y.dtype, dev, stream)
+    _call("ds_expert_combine", dev, stream, y.data_ptr(), n, ys, dt, ctypes.byref(c),
+          None if weights is None else _operand(weights, "weights", _torch().float32, plan.place.shape, dev),
+          out.data_ptr(), os)
+    return out
+
+
+def ds_expert_combine_grad(grad, y, plan: ExpertPlan, weights=None, grad_y: bool = True, grad_weights: bool = True,
+                           out_y=None, out_weights=None, stream=None):
+    """The gradients of ds_expert_combine for grad [rows, n], the gradient of its result: (grad_y
+    [capacity, n] or None, grad_weights [rows, k] fp32 or None). From the plan's end on grad_y holds what
+    out_y held. out_y may be y itself. y may be None when grad_weights is False."""
+    torch = _torch()
+    rows, n, gs = _matrix(grad, "grad")
+    dt, dev = _code(grad.dtype), grad.device
+    c, plan_rows, capacity = _plan(plan, dev)
+    if plan_rows != rows:
+        raise ValueError("grad must have the plan's rows")
+    yp, ys, op, os, wp = None, n, None, n, None
+    if grad_weights:
+        if y is None:
+            raise ValueError("y is needed for the weights' gradient")
+        _, _, ys = _matrix(y, "y")
+        if y.shape != (capacity, n) or y.dtype != grad.dtype or y.device != dev:
+            raise ValueError("y must be [capacity, n] of grad's dtype on its device")
+        yp = y.data_ptr()
+        if out_weights is None:
+            out_weights = _empty(plan.place.shape, torch.float32, dev, stream)
+        wp = _operand(out_weights, "out_weights", torch.float32, plan.place.shape, dev)
+    if grad_y:
+        out_y, os = _rows_out(out_y, capacity, n, grad.dtype, dev, stream, "out_y")
+        op = out_y.data_ptr()
+    _call("ds_expert_combine_grad", dev, stream, grad.data_ptr(), gs, yp, ys, n, dt, ctypes.byref(c),
+          None if weights is None else _operand(weights, "weights", torch.float32, plan.place.shape, dev), op, os, wp)
+    return out_y if grad_y else None, out_weights if grad_weights else None
+
+
+_codes8: Dict[object, int] = {}
+
+
+def _code8(dtype) -> int:
+    code = _codes8.get(dtype)
+    if code is None:
+        torch = _torch()
+        _codes8.update({torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2})
+        code = _codes8.get(dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {dtype}; expected torch.float8_e4m3fn or torch.float8_e5m2")
+    return code
+
+
+def ds_block_quantize(x, layout: int = BLOCK_ROW, dtype=None, plan: Optional[ExpertPlan] = None, out=None,
+                      out_scales=None, stream=None):
+    """x [rows, n] (bf16 or fp32) in blocks of 128 as 8-bit floats (torch.float8_e4m3fn, or
+    float8_e5m2) and fp32 scales; see include/dstopk.h for the layouts and a plan's part. Returns (q,
+    scales): BLOCK_ROW q [P, n up to 16s], scales [P, ceil(n / 128)]; BLOCK_COLUMN (transposed)
+    q [n, P up to 16s], scales [n, ceil(P / 128)]; BLOCK_TILE q [rows, n up to 16s], scales
+    [ceil(rows / 128), ceil(n / 128)], P the plan's capacity or the rows. What lies behind the plan's
+    end is what the outputs held. BLOCK_TILE takes a stack x [groups, rows, n] too (experts' weights)."""
+    torch = _torch()
+    dtype = dtype or torch.float8_e4m3fn
+    if x.dim() == 3:
+        return _quantize_stack(x, layout, dtype, plan, out, out_scales, stream)
+    rows, n, rs = _matrix(x, "x")
+    dt, qt, dev = _code(x.dtype), _code8(dtype), x.device
+    c, positions = None, rows
+    if plan is not None:
+        c, plan_rows, positions = _plan(plan, dev)
+        if plan_rows != rows:
+            raise ValueError("x must have the plan's rows")
+        c = ctypes.byref(c)
+    if layout == BLOCK_COLUMN:
+        q_rows, cols, shape = n, positions, (n, -(-positions // DS_BLOCK))
+    else:
+        q_rows, cols = positions, n
+        shape = (-(-positions // DS_BLOCK) if layout == BLOCK_TILE else positions, -(-n // DS_BLOCK))
+    out, qs = _rows_out(out, q_rows, -(-cols // 16) * 16, dtype, dev, stream)
+    if out_scales is None:
+        out_scales = _empty(shape, torch.float32, dev, stream)
+    _call("ds_block_quantize", dev, stream, x.data_ptr(), rows, n, rs, dt, layout, c, out.data_ptr(), qs, qt,
+          _operand(out_scales, "out_scales", torch.float32, shape, dev))
+    return out, out_scales
+
+
+def _quantize_stack(x, layout, dtype, plan, out, out_scales, stream):
+    """ds_block_quantize of each matrix of a contiguous stack (one call where tiles do not cross them)."""
+    torch = _torch()
+    if layout != BLOCK_TILE or plan is not None:
+        raise ValueError("a stack of matrices is quantised in tiles, without a plan")
+    if not x.is_cuda or not x.is_contiguous():
+        raise ValueError("a stack of matrices must be a contiguous device tensor")
+    G, rows, n = x.shape
+    wide, tiles = -(-n // 16) * 16, (-(-rows // DS_BLOCK), -(-n // DS_BLOCK))
+    if out is None:
+        out = _empty((G * rows, wide), dtype, x.device, stream).view(G, rows, wide)
+    if out_scales is None:
+        out_scales = _empty((G * tiles[0], tiles[1]), torch.float32, x.device, stream).view(G, *tiles)
+    if out.shape != (G, rows, wide) or out.dtype != dtype or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous [{G}, {rows}, {wide}] tensor of {dtype}")
+    if out_scales.shape != (G, *tiles) or out_scales.dtype != torch.float32 or not out_scales.is_contiguous():
+        raise ValueError(f"out_scales must be a contiguous {(G, *tiles)} fp32 tensor")
+    if rows % DS_BLOCK == 0:
+        ds_block_quantize(x.view(G * rows, n), layout, dtype, None, out.view(G * rows, wide),
+                          out_scales.view(G * tiles[0], tiles[1]), stream)
+    else:
+        for g in range(G):
+            ds_block_quantize(x[g], layout, dtype, None, out[g], out_scales[g], stream)
+    return out, out_scales
+
+
+def ds_block_product(a, a_scales, b, b_scales, offsets=None, inner: bool = False, out=None, out_dtype=None,
+                     stream=None):
+    """a b^T of 8-bit operands with a scale for each 128 along the inner axis (ds_block_quantize's);
+    bf16 (or out_dtype / out's type: bf16 or fp32). a [m, k] with scales [m, ceil(k / 128)].
+      offsets None   b [n, k]; [m, n].
+      offsets        int32 [groups + 1], the segments of a's rows (a plan's offsets), b [groups, n, k];
+                     [m, n], rows outside the segments hold what out held.
+      inner=True     offsets are segments of the inner axis, at multiples of 128; b [n, k] with scales
+                     [n, ceil(k / 128)]; [groups, m, n].
+    b is e4m3, with scales [.., n, ceil(k / 128)] or, in tiles, [.., ceil(n / 128), ceil(k / 128)]; a is e4m3
+    or e5m2. k is a multiple of 16. The gradients are products of the same kind (include/dstopk.h)."""
+    torch = _torch()
+    m, k, a_stride = _matrix(a, "a")
+    a_type, dev = _code8(a.dtype), a.device
+    stacked = offsets is not None and not inner
+    if stacked:
+        groups_b, n, kb, b_stride = _batch_rows(b, "b")
+    else:
+        n, kb, b_stride = _matrix(b, "b")
+        groups_b = 1
+    if kb != k or b.device != dev:
+        raise ValueError("b must have a's inner length and device")
+    b_type, blocks, group, groups, op = _code8(b.dtype), -(-k // DS_BLOCK), GROUP_NONE, 1, None
+    if offsets is not None:
+        group, groups = (GROUP_INNER if inner else GROUP_ROWS), offsets.shape[0] - 1
+        if offsets.dim() != 1 or groups < 1 or (stacked and groups != groups_b):
+            raise ValueError("offsets must be 1-D, one more than the groups")
+        op = _operand(offsets, "offsets", torch.int32, (groups + 1,), dev)
+    elif inner:
+        raise ValueError("inner needs offsets")
+    shape = (groups, m, n) if inner else (m, n)
+    if out is None:
+        out = _empty((groups * m, n) if inner else shape, out_dtype or torch.bfloat16, dev, stream)
+        stride = n
+        if inner:
+            out = out.view(shape)
+    else:
+        if out.shape != shape or out.device != dev or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError(f"out must be {shape} of out_dtype on {dev}")
+        stride = _batch_rows(out, "out")[3] if inner else _matrix(out, "out")[2]
+    scale_rows = 1
+    if not inner and b_scales.dim() == b.dim() and b_scales.shape[-2] != n:
+        scale_rows = DS_BLOCK
+    lead = (groups_b,) if stacked else ()
+    sp = _operand(b_scales, "b_scales", torch.float32, (*lead, n if scale_rows == 1 else -(-n // DS_BLOCK), blocks), dev)
+    of_a = ds_block_operand(a.data_ptr(), _operand(a_scales, "a_scales", torch.float32, (m, blocks), dev), a_stride,
+                            a_type, 1)
+    of_b = ds_block_operand(b.data_ptr(), sp, b_stride, b_type, scale_rows)
+    _call("ds_block_product", dev, stream, ctypes.byref(of_a), ctypes.byref(of_b), m, n, k, group, groups, op,
+          out.data_ptr(), stride, _code(out.dtype))
+    return out
 
 
 def stats_buffer(rows: int, slices: int, device):

@@ -41,6 +41,10 @@ UNITS = [(f"select_{dt}{'_stats' if st else ''}{'_ext' if ex else ''}", "ds_sele
     ("probs", "ds_probs.hip", []),
     ("verify", "ds_verify.hip", []),
     ("rows_api", "ds_rows_api.cpp", []),
+    ("expert", "ds_expert.hip", []),
+    ("blocks", "ds_blocks.hip", []),
+    ("product", "ds_product.hip", []),
+    ("expert_api", "ds_expert_api.cpp", []),
     ("noalloc", "ds_noalloc.hip", []),
     ("api", "ds_api.cpp", [])]
 

@@ -1,0 +1,371 @@
+// Slots sorted by expert, rows gathered to their slots' positions and combined back, and the
+// gradients of that.
+#include "ds_expert.h"
+#include "ds_rows_device.h"
+
+namespace ds {
+namespace {
+
+// ------------------------------------------------------------------------------------- sort
+// A stable counting sort: position = offsets[e] + slots of e in earlier chunks + in earlier
+// waves of the chunk + in earlier lanes. A wave takes its slots in order, 64 at a time; lanes
+// with equal experts find one another by ballots over the experts' bits, so no atomic decides a place.
+
+__device__ __forceinline__ int expert_of(const SortParams& p, int64_t slot, int64_t end) {
+  const int e = slot < end ? p.idx[slot] : -1;
+  return static_cast<uint32_t>(e) < static_cast<uint32_t>(p.experts) ? e : -1;
+}
+
+// Counts of a chunk's slots by expert.
+__global__ __launch_bounds__(1024) void sort_count_kernel(SortParams p) {
+  __shared__ int hist[DS_MAX_EXPERTS];
+  for (int e = threadIdx.x; e < p.experts; e += 1024) hist[e] = 0;
+  __syncthreads();
+  const int64_t lo = blockIdx.x * p.chunk, hi = lo + p.chunk < p.slots ? lo + p.chunk : p.slots;
+  for (int64_t s = lo + threadIdx.x; s < hi; s += 1024) {
+    const int e = expert_of(p, s, hi);
+    if (e >= 0) atomicAdd(&hist[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.experts; e += 1024) p.counts[static_cast<int64_t>(blockIdx.x) * p.experts + e] = hist[e];
+}
+
+template <int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void sort_place_kernel(SortParams p) {
+  constexpr int T = WAVES * 64;
+  extern __shared__ int lds[];
+  const int E = p.experts, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int* mine = lds + wave * E;           // [WAVES][E]: the waves' counts, then their next positions
+  int* total = lds + WAVES * E;         // [E]: slots of the expert
+  int* before = total + E;              // [E]: of them in earlier chunks
+  int* start = before + E;              // [E + 1]: offsets
+  __shared__ int wave_sums[WAVES];
+  for (int i = tid; i < (WAVES + 2) * E; i += T) lds[i] = 0;
+  __syncthreads();
+
+  const int64_t lo = blockIdx.x * p.chunk, hi = lo + p.chunk < p.slots ? lo + p.chunk : p.slots;
+  const int64_t sub = ((hi - lo + WAVES - 1) / WAVES + 63) / 64 * 64;
+  const int64_t wlo = lo + wave * sub < hi ? lo + wave * sub : hi, whi = wlo + sub < hi ? wlo + sub : hi;
+  for (int64_t s = wlo + lane; s < whi; s += 64) {
+    const int e = expert_of(p, s, whi);
+    if (e >= 0) atomicAdd(&mine[e], 1);
+  }
+  if (p.chunks > 1) {
+    // the threads share the chunks' counts: each takes an expert of some chunks
+    const int64_t all = static_cast<int64_t>(p.chunks) * E;
+    for (int64_t i = tid; i < all; i += T) {
+      const int v = p.counts[i], c = static_cast<int>(i / E), e = static_cast<int>(i - static_cast<int64_t>(c) * E);
+      if (v) {
+        atomicAdd(&total[e], v);
+        if (c < static_cast<int>(blockIdx.x)) atomicAdd(&before[e], v);
+      }
+    }
+  }
+  __syncthreads();
+  if (p.chunks == 1) {
+    for (int e = tid; e < E; e += T) {
+      int t = 0;
+      for (int w = 0; w < WAVES; ++w) t += lds[w * E + e];
+      total[e] = t;
+    }
+    __syncthreads();
+  }
+
+  // offsets: an exclusive sum of the padded counts, a run of experts a thread
+  const int per = (E + T - 1) / T, e0 = tid * per, e1 = e0 + per < E ? e0 + per : E;
+  int run = 0;
+  for (int e = e0; e < e1; ++e) run += (total[e] + p.align - 1) / p.align * p.align;
+  int incl = run;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(incl, d);
+    if (lane >= d) incl += v;
+  }
+  if (lane == 63) wave_sums[wave] = incl;
+  __syncthreads();
+  int at = incl - run;
+  for (int w = 0; w < wave; ++w) at += wave_sums[w];
+  for (int e = e0; e < e1; ++e) {
+    start[e] = at;
+    at += (total[e] + p.align - 1) / p.align * p.align;
+    if (e == E - 1) start[E] = at;
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += T) {
+    int next = start[e] + before[e];
+    for (int w = 0; w < WAVES; ++w) {
+      const int c = lds[w * E + e];
+      lds[w * E + e] = next;
+      next += c;
+    }
+  }
+  __syncthreads();
+
+  // places
+  const int bits = 32 - __clz(E);
+  for (int64_t s0 = wlo; s0 < whi; s0 += 64) {
+    const int64_t s = s0 + lane;
+    const int e = expert_of(p, s, whi);
+    uint64_t same = __ballot(e >= 0);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t set = __ballot((e >> b) & 1);
+      same &= ((e >> b) & 1) ? set : ~set;
+    }
+    int pos = -1;
+    if (e >= 0) pos = mine[e] + __popcll(same & ((1ull << lane) - 1));
+    wave_sync();
+    if (e >= 0 && (same >> lane) == 1) mine[e] = pos + 1;  // the last of the equals
+    wave_sync();
+    if (s < whi) p.place[s] = pos;
+    if (pos >= 0) p.order[pos] = static_cast<int>(s);
+  }
+
+  // padding at the segments' ends, shared by the workgroups, and what lies past the end
+  for (int e = blockIdx.x; e < E; e += p.chunks) {
+    for (int i = start[e] + total[e] + tid; i < start[e + 1]; i += T) p.order[i] = -1;
+  }
+  for (int64_t i = start[E] + static_cast<int64_t>(blockIdx.x) * T + tid; i < p.capacity;
+       i += static_cast<int64_t>(p.chunks) * T)
+    p.order[i] = -1;
+  if (blockIdx.x == 0)
+    for (int e = tid; e <= E; e += T) p.offsets[e] = start[e];
+}
+
+// ----------------------------------------------------------------------------------- rows
+// A team of LANES lanes takes a row; its lanes take the row's 16-byte vectors in turn and the
+// elements past the last whole vector one each.
+
+__device__ __forceinline__ int position(const Plan& q, int64_t slot) {
+  const int pos = q.place[slot];
+  return pos >= 0 && pos < q.capacity ? pos : -1;
+}
+
+// Clears the padding rows of 16 of the last align - 1 positions of a segment (unit: expert, then
+// sixteenths), `bytes` long; `also(position)` runs for each with all threads.
+constexpr int kPadRun = 16;
+__device__ __forceinline__ int pad_parts(int align) { return (align - 1 + kPadRun - 1) / kPadRun; }
+
+template <class F>
+__device__ __forceinline__ void for_padding(const Plan& q, int64_t unit, F&& each) {
+  const int parts = pad_parts(q.align), e = static_cast<int>(unit / parts), part = static_cast<int>(unit % parts);
+  const int64_t cap = q.capacity;
+  int64_t lo = q.offsets[e], hi = q.offsets[e + 1];
+  lo = lo < 0 ? 0 : lo;
+  hi = hi < cap ? hi : cap;
+  const int64_t at = hi - (part + 1) * kPadRun + (threadIdx.x & (kPadRun - 1));
+  bool pad = false;
+  if (at >= lo && at >= hi - (q.align - 1)) {
+    const int s = q.order[at];
+    pad = s < 0 || s >= q.rows * q.k;
+  }
+  uint32_t mask = static_cast<uint32_t>(__ballot(pad)) & 0xFFFFu;
+  while (mask) {
+    const int i = __ffs(mask) - 1;
+    mask &= mask - 1;
+    each(hi - (part + 1) * kPadRun + i);
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void clear_row(typename Elem<DT>::T* row, int64_t n) {
+  constexpr int V = Elem<DT>::kPer16;
+  using Vt = Vec<DT, V>;
+  const int64_t whole = n / V;
+  typename Vt::type z = {};
+  for (int64_t v = threadIdx.x; v < whole; v += 256) *reinterpret_cast<typename Vt::unaligned*>(row + v * V) = z;
+  if (whole * V + threadIdx.x < n) row[whole * V + threadIdx.x] = 0;
+}
+
+template <int DT, int LANES>
+__global__ __launch_bounds__(256) void gather_kernel(MoveParams p) {
+  using T = typename Elem<DT>::T;
+  constexpr int V = Elem<DT>::kPer16;
+  using Vt = Vec<DT, V>;
+  const int64_t unit = p.unit0 + blockIdx.x;
+  T* out = static_cast<T*>(p.out);
+  if (unit < p.pad_units) {
+    for_padding(p.plan, unit, [&](int64_t at) { clear_row<DT>(out + at * p.out_stride, p.n); });
+    return;
+  }
+  const int64_t r = (unit - p.pad_units) * (256 / LANES) + threadIdx.x / LANES;
+  if (r >= p.plan.rows) return;
+  const int lane = threadIdx.x % LANES, k = p.plan.k;
+  const T* x = static_cast<const T*>(p.x) + r * p.x_stride;
+  const int64_t whole = p.n / V, slot = r * k;
+  for (int64_t v = lane; v < whole; v += LANES) {
+    const typename Vt::type d = *reinterpret_cast<const typename Vt::unaligned*>(x + v * V);
+    for (int j = 0; j < k; ++j) {
+      const int64_t at = position(p.plan, slot + j);
+      if (at >= 0) *reinterpret_cast<typename Vt::unaligned*>(out + at * p.out_stride + v * V) = d;
+    }
+  }
+  for (int64_t i = whole * V + lane; i < p.n; i += LANES) {
+    const T d = x[i];
+    for (int j = 0; j < k; ++j) {
+      const int64_t at = position(p.plan, slot + j);
+      if (at >= 0) out[at * p.out_stride + i] = d;
+    }
+  }
+}
+
+template <int DT, int LANES>
+__global__ __launch_bounds__(256) void combine_kernel(MoveParams p) {
+  using T = typename Elem<DT>::T;
+  constexpr int V = Elem<DT>::kPer16;
+  using Vt = Vec<DT, V>;
+  const int64_t r = (p.unit0 + blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
+  if (r >= p.plan.rows) return;
+  const int lane = threadIdx.x % LANES, k = p.plan.k;
+  const T* y = static_cast<const T*>(p.x);
+  T* out = static_cast<T*>(p.out) + r * p.out_stride;
+  const int64_t whole = p.n / V, slot = r * k;
+  for (int64_t v = lane; v < whole; v += LANES) {
+    float acc[V] = {};
+    for (int j = 0; j < k; ++j) {
+      const int64_t at = position(p.plan, slot + j);
+      if (at < 0) continue;
+      const float w = p.weights ? p.weights[slot + j] : 1.0f;
+      const typename Vt::type d = *reinterpret_cast<const typename Vt::unaligned*>(y + at * p.x_stride + v * V);
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(w, Elem<DT>::widen(d[i]), acc[i]);
+    }
+    typename Vt::type o;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = Elem<DT>::narrow(acc[i]);
+    *reinterpret_cast<typename Vt::unaligned*>(out + v * V) = o;
+  }
+  for (int64_t i = whole * V + lane; i < p.n; i += LANES) {
+    float acc = 0;
+    for (int j = 0; j < k; ++j) {
+      const int64_t at = position(p.plan, slot + j);
+      if (at < 0) continue;
+      const float w = p.weights ? p.weights[slot + j] : 1.0f;
+      acc = __builtin_fmaf(w, Elem<DT>::widen(y[at * p.x_stride + i]), acc);
+    }
+    out[i] = Elem<DT>::narrow(acc);
+  }
+}
+
+// One wave a row.
+template <int DT>
+__global__ __launch_bounds__(256) void combine_grad_kernel(MoveParams p) {
+  using T = typename Elem<DT>::T;
+  constexpr int V = Elem<DT>::kPer16;
+  using Vt = Vec<DT, V>;
+  const int64_t unit = p.unit0 + blockIdx.x;
+  T* out = static_cast<T*>(p.out);
+  if (unit < p.pad_units) {
+    for_padding(p.plan, unit, [&](int64_t at) { clear_row<DT>(out + at * p.out_stride, p.n); });
+    return;
+  }
+  const int64_t r = (unit - p.pad_units) * 4 + threadIdx.x / 64;
+  if (r >= p.plan.rows) return;
+  const int lane = threadIdx.x % 64, k = p.plan.k;
+  const T* g = static_cast<const T*>(p.g) + r * p.g_stride;
+  const T* y = static_cast<const T*>(p.x);
+  const int64_t whole = p.n / V, slot = r * k;
+  float mine = 0;  // lane j: the gradient of slot j's weight
+  for (int j = 0; j < k; ++j) {
+    const int64_t at = position(p.plan, slot + j);
+    if (at < 0) continue;
+    const float w = p.weights ? p.weights[slot + j] : 1.0f;
+    float dot = 0;
+    for (int64_t v = lane; v < whole; v += 64) {
+      const typename Vt::type d = *reinterpret_cast<const typename Vt::unaligned*>(g + v * V);
+      if (p.out_weights) {
+        const typename Vt::type e = *reinterpret_cast<const typename Vt::unaligned*>(y + at * p.x_stride + v * V);
+#pragma unroll
+        for (int i = 0; i < V; ++i) dot = __builtin_fmaf(Elem<DT>::widen(d[i]), Elem<DT>::widen(e[i]), dot);
+      }
+      if (out) {
+        typename Vt::type o;
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = Elem<DT>::narrow(w * Elem<DT>::widen(d[i]));
+        *reinterpret_cast<typename Vt::unaligned*>(out + at * p.out_stride + v * V) = o;
+      }
+    }
+    for (int64_t i = whole * V + lane; i < p.n; i += 64) {
+      const float d = Elem<DT>::widen(g[i]);
+      if (p.out_weights) dot = __builtin_fmaf(d, Elem<DT>::widen(y[at * p.x_stride + i]), dot);
+      if (out) out[at * p.out_stride + i] = Elem<DT>::narrow(w * d);
+    }
+    const float sum = wave_sum(dot);
+    if (lane == j) mine = sum;
+  }
+  if (p.out_weights && lane < k) p.out_weights[slot + lane] = mine;
+}
+
+// Lanes of a team: what a row's vectors fill, up to a workgroup.
+template <int DT>
+int lanes_for(int64_t n) {
+  const int64_t v = n / Elem<DT>::kPer16;
+  return v <= 32 ? 16 : v <= 128 ? 64 : 256;
+}
+
+}  // namespace
+
+SortCut cut_sort(int64_t slots) {
+  // one workgroup up to 8192 slots; from there chunks of 4096, and at most 256 of them
+  if (slots <= 8192) return {slots, 1};
+  int64_t chunk = 4096;
+  while ((slots + chunk - 1) / chunk > kCus) chunk *= 2;
+  return {chunk, static_cast<int32_t>((slots + chunk - 1) / chunk)};
+}
+
+hipError_t launch_sort(const SortParams& p, hipStream_t s) {
+  if (p.chunks > 1) {
+    hipLaunchKernelGGL(sort_count_kernel, dim3(p.chunks), dim3(1024), 0, s, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const auto bytes = [&](int waves) { return static_cast<size_t>((waves + 3) * p.experts + 1) * sizeof(int); };
+  if (p.chunk <= 1024)
+    hipLaunchKernelGGL(sort_place_kernel<4>, dim3(p.chunks), dim3(256), bytes(4), s, p);
+  else if (p.experts > 512)  // the waves' counts within 64 KiB of LDS
+    hipLaunchKernelGGL(sort_place_kernel<8>, dim3(p.chunks), dim3(512), bytes(8), s, p);
+  else
+    hipLaunchKernelGGL(sort_place_kernel<16>, dim3(p.chunks), dim3(1024), bytes(16), s, p);
+  return hipGetLastError();
+}
+
+namespace {
+int64_t pad_units_of(const Plan& q) {
+  return static_cast<int64_t>(q.experts) * ((q.align - 1 + kPadRun - 1) / kPadRun);
+}
+int64_t teams(int64_t rows, int lanes) { return (rows + 256 / lanes - 1) / (256 / lanes); }
+
+template <int DT>
+hipError_t gather_of(MoveParams p, hipStream_t s) {
+  const int lanes = lanes_for<DT>(p.n);
+  p.pad_units = pad_units_of(p.plan);
+  const int64_t units = p.pad_units + teams(p.plan.rows, lanes);
+  return lanes == 16   ? launch_units(gather_kernel<DT, 16>, p, units, 256, s)
+         : lanes == 64 ? launch_units(gather_kernel<DT, 64>, p, units, 256, s)
+                       : launch_units(gather_kernel<DT, 256>, p, units, 256, s);
+}
+
+template <int DT>
+hipError_t combine_of(MoveParams p, hipStream_t s) {
+  const int lanes = lanes_for<DT>(p.n);
+  const int64_t units = teams(p.plan.rows, lanes);
+  return lanes == 16   ? launch_units(combine_kernel<DT, 16>, p, units, 256, s)
+         : lanes == 64 ? launch_units(combine_kernel<DT, 64>, p, units, 256, s)
+                       : launch_units(combine_kernel<DT, 256>, p, units, 256, s);
+}
+}  // namespace
+
+hipError_t launch_gather(int dtype, MoveParams p, hipStream_t s) {
+  return dtype == DS_BF16 ? gather_of<DS_BF16>(p, s) : gather_of<DS_FP32>(p, s);
+}
+
+hipError_t launch_combine(int dtype, MoveParams p, hipStream_t s) {
+  return dtype == DS_BF16 ? combine_of<DS_BF16>(p, s) : combine_of<DS_FP32>(p, s);
+}
+
+hipError_t launch_combine_grad(int dtype, MoveParams p, hipStream_t s) {
+  p.pad_units = p.out ? pad_units_of(p.plan) : 0;
+  const int64_t units = p.pad_units + teams(p.plan.rows, 64);
+  return dtype == DS_BF16 ? launch_units(combine_grad_kernel<DS_BF16>, p, units, 256, s)
+                          : launch_units(combine_grad_kernel<DS_FP32>, p, units, 256, s);
+}
+
+}  // namespace ds
