@@ -183,14 +183,258 @@ __global__ __launch_bounds__(256) void product_small_kernel(ProductParams p) {
   store4<OT>(static_cast<typename Elem<OT>::T*>(p.out) + out_row * p.out_stride, n0 + wave * 16 + quad * 4, p.n, v);
 }
 
+// ------------------------------------------------------------------------- tiles through LDS
+// The sixteen-byte parts of a tile's rows of 128 lie in LDS in an order that makes a fragment's reads
+// (sixteen rows, one part each, consecutive rows or every sixteenth four) meet every bank once.
+__device__ __forceinline__ int part_at(int row, int part) {
+  return part ^ (row & 7) ^ ((row >> 3) & 1) ^ ((row >> 4) & 1) ^ (((row >> 5) & 1) << 2);
+}
+
+template <int AT, bool EXACT>
+__device__ __forceinline__ v4f tile_product(v8i b, v8i a) {
+  if constexpr (EXACT) return block_product<AT>(b, a);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, v4f{0, 0, 0, 0}, 0, AT == DS_E5M2 ? 1 : 0, 0, 0, 0, 0);
+}
+
+// Loads of sixteen (four) bytes a lane from base + offset to LDS from `lds` on, lane after lane, past the
+// registers. The compiler holds every LDS read back until such loads have arrived, wherever they write,
+// so they are issued behind its back: wait_loads() before the barrier that the readers wait at.
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)p));
+}
+__device__ __forceinline__ void load_to_lds16(const void* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base), "s"(lds) : "memory");
+}
+__device__ __forceinline__ void load_to_lds4(const void* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(offset), "s"(base), "s"(lds) : "memory");
+}
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+template <int TM, int TN, int BROWS>
+struct Stage {
+  uint8_t a[TM][128];
+  uint8_t b[TN][128];
+  float sa[TM];
+  float sb[BROWS == 1 ? TN : 64];
+};
+
+// WM x WN waves, each of MF x NF fragments of sixteen.
+template <int AT, int BROWS, int GROUP, int OT, int WM, int WN, int MF, int NF>
+struct Tiled {
+  static constexpr int kWaves = WM * WN, kThreads = kWaves * 64, TM = WM * MF * 16, TN = WN * NF * 16;
+  static constexpr bool kExact = OT == DS_FP32;
+  static constexpr int kLoadsA = TM / 8 / kWaves, kLoadsB = TN / 8 / kWaves;  // of eight rows, a wave
+  using S = Stage<TM, TN, BROWS>;
+
+  // A block's rows to LDS: a wave's load is eight rows, its lane l the part part_at(row, l % 8) of row l / 8.
+  // Rows past the last repeat it (they are not stored).
+  struct Source {
+    const uint8_t* a;
+    const uint8_t* b;
+    uint32_t ao[kLoadsA], bo[kLoadsB];  // bytes from there
+    const float* sa;
+    const float* sb;
+    uint32_t sao, sbo;
+  };
+
+  static __device__ __forceinline__ void stage(S& s, const Source& q, int64_t k, int wave) {
+    const uint8_t* a = q.a + k;
+    const uint8_t* b = q.b + k;
+#pragma unroll
+    for (int i = 0; i < kLoadsA; ++i) load_to_lds16(a, q.ao[i], lds_address(s.a[(i * kWaves + wave) * 8]));
+#pragma unroll
+    for (int i = 0; i < kLoadsB; ++i) load_to_lds16(b, q.bo[i], lds_address(s.b[(i * kWaves + wave) * 8]));
+    // the scales: a float a row
+    const int64_t kb = k / 128;
+    if (wave < TM / 64) load_to_lds4(q.sa + kb, q.sao, lds_address(s.sa + wave * 64));
+    if constexpr (BROWS == 1) {
+      if (wave >= kWaves - TN / 64) load_to_lds4(q.sb + kb, q.sbo, lds_address(s.sb + (wave - (kWaves - TN / 64)) * 64));
+    }
+  }
+
+  // The last block of an inner length that is no multiple of 128: through registers, zeros past the end.
+  static __device__ __forceinline__ void stage_rest(S& s, const Source& q, int64_t k, int64_t k1) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int i = 0; i < kLoadsA; ++i) {
+      const int row = (i * kWaves + wave) * 8 + lane / 8;
+      const bool live = k + part_at(row, lane & 7) * 16 < k1;
+      *reinterpret_cast<v4i*>(&s.a[row][(lane & 7) * 16]) =
+          live ? *reinterpret_cast<const v4i*>(q.a + k + q.ao[i]) : v4i{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int i = 0; i < kLoadsB; ++i) {
+      const int row = (i * kWaves + wave) * 8 + lane / 8;
+      const bool live = k + part_at(row, lane & 7) * 16 < k1;
+      *reinterpret_cast<v4i*>(&s.b[row][(lane & 7) * 16]) =
+          live ? *reinterpret_cast<const v4i*>(q.b + k + q.bo[i]) : v4i{0, 0, 0, 0};
+    }
+    const int64_t kb = k / 128;
+    if (wave < TM / 64) s.sa[threadIdx.x] = *reinterpret_cast<const float*>(reinterpret_cast<const char*>(q.sa + kb) + q.sao);
+    if constexpr (BROWS == 1) {
+      if (wave >= kWaves - TN / 64)
+        s.sb[threadIdx.x - (kThreads - TN)] = *reinterpret_cast<const float*>(reinterpret_cast<const char*>(q.sb + kb) + q.sbo);
+    }
+  }
+
+  static __device__ __forceinline__ v8i fragment(const uint8_t (*rows)[128], int row, int quad) {
+    const v4i lo = *reinterpret_cast<const v4i*>(&rows[row][part_at(row, quad) * 16]);
+    const v4i hi = *reinterpret_cast<const v4i*>(&rows[row][part_at(row, quad + 4) * 16]);
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+
+  // Lane l of a fragment: a row l % 16, and of b the rows whose results make 4 NF consecutive columns a lane.
+  static __device__ __forceinline__ int b_row(int f, int lane) {
+    return (lane % 16) / 4 * (4 * NF) + f * 4 + lane % 4;
+  }
+
+  static __device__ __forceinline__ void compute(const S& s, float sb, float (&acc)[MF][NF][4]) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, quad = lane >> 4;
+    const int m = wave / WN * (MF * 16), n = wave % WN * (NF * 16);
+    v8i b[NF];
+    v4f scales[NF];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      b[f] = fragment(s.b, n + b_row(f, lane), quad);
+      if constexpr (BROWS == 1) scales[f] = *reinterpret_cast<const v4f*>(&s.sb[n + quad * (4 * NF) + f * 4]);
+    }
+#pragma unroll
+    for (int e = 0; e < MF; ++e) {
+      const int row = m + e * 16 + lane % 16;
+      const v8i a = fragment(s.a, row, quad);
+      const float sa = BROWS == 1 ? s.sa[row] : s.sa[row] * sb;
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        const v4f d = tile_product<AT, kExact>(b[f], a);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc[e][f][i] = __builtin_fmaf(BROWS == 1 ? sa * scales[f][i] : sa, d[i], acc[e][f][i]);
+      }
+    }
+  }
+
+  static __device__ __forceinline__ void run(const ProductParams& p, S& s0, S& s1) {
+    // eight neighbouring workgroups are on eight XCDs: each XCD takes runs of 32 tiles, whose rows share its L2
+    const int64_t id = p.unit0 + blockIdx.x;
+    const int64_t unit = (id / 256) * 256 + (id % 8) * 32 + id / 8 % 32;
+    if (unit >= p.units) return;
+    // tiles in bands of four m tiles, m first
+    const int64_t band = 4 * p.n_tiles, of = unit / band, in = unit - of * band;
+    const int64_t high = p.m_tiles - of * 4 < 4 ? p.m_tiles - of * 4 : 4;
+    Tile t;
+    if (!find_tile<GROUP, TM>(p, of * 4 + in % high, t)) return;
+    const int64_t n0 = in / high * TN;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t b0 = GROUP == DS_GROUP_ROWS ? t.group * p.n : 0;
+    const int mlast = static_cast<int>(t.m1 - t.m0 < TM ? t.m1 - t.m0 : TM) - 1;
+    const int nlast = static_cast<int>(p.n - n0 < TN ? p.n - n0 : TN) - 1;
+    Source q;
+    q.a = p.a + t.m0 * p.a_stride;
+    q.b = p.b + (b0 + n0) * p.b_stride;
+#pragma unroll
+    for (int i = 0; i < kLoadsA; ++i) {
+      const int row = (i * kWaves + wave) * 8 + lane / 8;
+      q.ao[i] = min(row, mlast) * static_cast<uint32_t>(p.a_stride) + part_at(row, lane & 7) * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < kLoadsB; ++i) {
+      const int row = (i * kWaves + wave) * 8 + lane / 8;
+      q.bo[i] = min(row, nlast) * static_cast<uint32_t>(p.b_stride) + part_at(row, lane & 7) * 16;
+    }
+    q.sa = p.sa + t.m0 * p.blocks;
+    q.sao = min(static_cast<int>(threadIdx.x), mlast) * static_cast<uint32_t>(p.blocks) * 4;
+    const float* sb_row = p.sb;
+    if constexpr (BROWS == 1) {
+      q.sb = p.sb + (b0 + n0) * p.blocks;
+      q.sbo = min(max(static_cast<int>(threadIdx.x) - (kThreads - TN), 0), nlast) * static_cast<uint32_t>(p.blocks) * 4;
+    } else {
+      const int64_t b_blocks = (p.n + 127) / 128, at = (n0 + wave % WN * (NF * 16)) / 128;
+      sb_row += ((GROUP == DS_GROUP_ROWS ? t.group * b_blocks : 0) + (at < b_blocks ? at : b_blocks - 1)) * p.blocks;
+    }
+    float acc[MF][NF][4] = {};
+    const int64_t whole = t.k0 + (t.k1 - t.k0) / 128 * 128;
+    int64_t k = t.k0;
+    const auto sb = [&](int64_t at) { return BROWS == 1 ? 0.0f : sb_row[at / 128]; };
+    if (k < whole) {
+      stage(s0, q, k, wave);
+      while (true) {
+        wait_loads();
+        __syncthreads();
+        if (k + 128 < whole) stage(s1, q, k + 128, wave);
+        compute(s0, sb(k), acc);
+        k += 128;
+        if (k >= whole) break;
+        wait_loads();
+        __syncthreads();
+        if (k + 128 < whole) stage(s0, q, k + 128, wave);
+        compute(s1, sb(k), acc);
+        k += 128;
+        if (k >= whole) break;
+      }
+    }
+    if (k < t.k1) {
+      __syncthreads();
+      stage_rest(s0, q, k, t.k1);
+      __syncthreads();
+      compute(s0, sb(k), acc);
+    }
+    // a lane has 4 NF consecutive columns of MF rows
+    const int quad = lane >> 4;
+    const int64_t n = n0 + wave % WN * (NF * 16) + quad * (4 * NF);
+    typename Elem<OT>::T* out = static_cast<typename Elem<OT>::T*>(p.out);
+    const int64_t first = GROUP == DS_GROUP_INNER ? t.group * p.m : 0;
+#pragma unroll
+    for (int e = 0; e < MF; ++e) {
+      const int64_t m = t.m0 + wave / WN * (MF * 16) + e * 16 + lane % 16;
+      if (m >= t.m1) continue;
+      typename Elem<OT>::T* row = out + (first + m) * p.out_stride;
+      if (n + 4 * NF <= p.n) {
+        constexpr int V = Elem<OT>::kPer16;
+        using Vt = Vec<OT, V>;
+#pragma unroll
+        for (int c = 0; c < 4 * NF; c += V) {
+          typename Vt::type o;
+#pragma unroll
+          for (int i = 0; i < V; ++i) o[i] = Elem<OT>::narrow(acc[e][(c + i) / 4][(c + i) % 4]);
+          *reinterpret_cast<typename Vt::unaligned*>(row + n + c) = o;
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4 * NF; ++c)
+          if (n + c < p.n) row[n + c] = Elem<OT>::narrow(acc[e][c / 4][c % 4]);
+      }
+    }
+  }
+};
+
+template <int AT, int BROWS, int GROUP, int OT, int WM, int WN, int MF, int NF>
+__global__ __launch_bounds__(WM * WN * 64, 2) void product_tiled_kernel(ProductParams p) {
+  using K = Tiled<AT, BROWS, GROUP, OT, WM, WN, MF, NF>;
+  __shared__ typename K::S s0, s1;
+  K::run(p, s0, s1);
+}
+
+// Tiles of TM x TN: how many (an upper bound where the segments decide).
+template <int GROUP>
+void count_tiles(ProductParams& p, int tm, int tn) {
+  p.m_tiles = (p.m + tm - 1) / tm;
+  if (GROUP == DS_GROUP_ROWS) p.m_tiles = p.m < p.m / tm + p.groups ? p.m : p.m / tm + p.groups;
+  if (GROUP == DS_GROUP_INNER) p.m_tiles *= p.groups;
+  p.n_tiles = (p.n + tn - 1) / tn;
+  p.units = p.m_tiles * p.n_tiles;
+}
+
 template <int AT, int BROWS, int GROUP, int OT>
 hipError_t product_of(ProductParams p, hipStream_t s) {
-  constexpr int TM = 16, TN = 64;
-  p.m_tiles = (p.m + TM - 1) / TM;
-  if (GROUP == DS_GROUP_ROWS) p.m_tiles = p.m < p.m / TM + p.groups ? p.m : p.m / TM + p.groups;
-  if (GROUP == DS_GROUP_INNER) p.m_tiles *= p.groups;
-  p.n_tiles = (p.n + TN - 1) / TN;
-  return launch_units(product_small_kernel<AT, BROWS, GROUP, OT>, p, p.m_tiles * p.n_tiles, 256, s);
+  // rows of a per segment, on average
+  const int64_t rows = GROUP == DS_GROUP_ROWS ? p.m / p.groups : p.m;
+  // (a tile's rows are reached by 32-bit offsets)
+  if (rows >= 64 && p.a_stride < (1 << 23) && p.b_stride < (1 << 23)) {
+    count_tiles<GROUP>(p, 256, 256);
+    return launch_units(product_tiled_kernel<AT, BROWS, GROUP, OT, 2, 4, 8, 4>, p, (p.units + 255) / 256 * 256, 512, s);
+  }
+  count_tiles<GROUP>(p, 16, 64);
+  return launch_units(product_small_kernel<AT, BROWS, GROUP, OT>, p, p.units, 256, s);
 }
 
 template <int AT, int OT>
