@@ -184,10 +184,13 @@ __global__ __launch_bounds__(256) void product_small_kernel(ProductParams p) {
 }
 
 // ------------------------------------------------------------------------- tiles through LDS
-// The sixteen-byte parts of a tile's rows of 128 lie in LDS in an order that makes a fragment's reads
-// (sixteen rows, one part each, consecutive rows or every sixteenth four) meet every bank once.
-__device__ __forceinline__ int part_at(int row, int part) {
-  return part ^ (row & 7) ^ ((row >> 3) & 1) ^ ((row >> 4) & 1) ^ (((row >> 5) & 1) << 2);
+// The sixteen-byte parts of a tile's rows of 128 lie in LDS in an order that makes a fragment's reads (sixteen
+// rows, one part each) meet every bank once, and whose fragments' addresses differ by constants: a's rows
+// are consecutive, b's four of each of four runs (Tiled::b_row).
+__device__ __forceinline__ int a_part(int row, int part) { return part ^ (row & 7); }
+template <int NF>
+__device__ __forceinline__ int b_part(int row, int part) {
+  return part ^ (((row >> 1) & 1) | (row / (4 * NF) % 4 << 1));
 }
 
 template <int AT, bool EXACT>
@@ -212,10 +215,10 @@ __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)"
 
 template <int TM, int TN, int BROWS>
 struct Stage {
-  uint8_t a[TM][128];
-  uint8_t b[TN][128];
   float sa[TM];
   float sb[BROWS == 1 ? TN : 64];
+  uint8_t a[TM][128];
+  uint8_t b[TN][128];
 };
 
 // WM x WN waves, each of MF x NF fragments of sixteen.
@@ -226,7 +229,7 @@ struct Tiled {
   static constexpr int kLoadsA = TM / 8 / kWaves, kLoadsB = TN / 8 / kWaves;  // of eight rows, a wave
   using S = Stage<TM, TN, BROWS>;
 
-  // A block's rows to LDS: a wave's load is eight rows, its lane l the part part_at(row, l % 8) of row l / 8.
+  // A block's rows to LDS: a wave's load is eight rows, its lane l a part of row l / 8.
   // Rows past the last repeat it (they are not stored).
   struct Source {
     const uint8_t* a;
@@ -258,14 +261,14 @@ struct Tiled {
 #pragma unroll
     for (int i = 0; i < kLoadsA; ++i) {
       const int row = (i * kWaves + wave) * 8 + lane / 8;
-      const bool live = k + part_at(row, lane & 7) * 16 < k1;
+      const bool live = k + a_part(row, lane & 7) * 16 < k1;
       *reinterpret_cast<v4i*>(&s.a[row][(lane & 7) * 16]) =
           live ? *reinterpret_cast<const v4i*>(q.a + k + q.ao[i]) : v4i{0, 0, 0, 0};
     }
 #pragma unroll
     for (int i = 0; i < kLoadsB; ++i) {
       const int row = (i * kWaves + wave) * 8 + lane / 8;
-      const bool live = k + part_at(row, lane & 7) * 16 < k1;
+      const bool live = k + b_part<NF>(row, lane & 7) * 16 < k1;
       *reinterpret_cast<v4i*>(&s.b[row][(lane & 7) * 16]) =
           live ? *reinterpret_cast<const v4i*>(q.b + k + q.bo[i]) : v4i{0, 0, 0, 0};
     }
@@ -277,10 +280,9 @@ struct Tiled {
     }
   }
 
-  static __device__ __forceinline__ v8i fragment(const uint8_t (*rows)[128], int row, int quad) {
-    const v4i lo = *reinterpret_cast<const v4i*>(&rows[row][part_at(row, quad) * 16]);
-    const v4i hi = *reinterpret_cast<const v4i*>(&rows[row][part_at(row, quad + 4) * 16]);
-    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  static __device__ __forceinline__ v8i join(const uint8_t* lo, const uint8_t* hi) {
+    return __builtin_shufflevector(*reinterpret_cast<const v4i*>(lo), *reinterpret_cast<const v4i*>(hi), 0, 1, 2, 3, 4, 5,
+                                   6, 7);
   }
 
   // Lane l of a fragment: a row l % 16, and of b the rows whose results make 4 NF consecutive columns a lane.
@@ -288,28 +290,49 @@ struct Tiled {
     return (lane % 16) / 4 * (4 * NF) + f * 4 + lane % 4;
   }
 
+  // A block: the matrix unit works on a fragment's products while the sums of the fragment before are scaled
+  // and added and the next fragment is read; the order is the source's.
   static __device__ __forceinline__ void compute(const S& s, float sb, float (&acc)[MF][NF][4]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, quad = lane >> 4;
-    const int m = wave / WN * (MF * 16), n = wave % WN * (NF * 16);
-    v8i b[NF];
+    const int m = wave / WN * (MF * 16) + lane % 16, n = wave % WN * (NF * 16);
+    const uint8_t* a_lo = &s.a[m][a_part(m, quad) * 16];
+    const uint8_t* a_hi = &s.a[m][a_part(m, quad + 4) * 16];
+    const int b0 = n + b_row(0, lane);
+    const uint8_t* b_lo = &s.b[b0][b_part<NF>(b0, quad) * 16];
+    const uint8_t* b_hi = &s.b[b0][b_part<NF>(b0, quad + 4) * 16];
+    v8i b[NF], a = join(a_lo, a_hi);
+    float sa = s.sa[m];
     v4f scales[NF];
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
-      b[f] = fragment(s.b, n + b_row(f, lane), quad);
+      b[f] = join(b_lo + f * 512, b_hi + f * 512);
       if constexpr (BROWS == 1) scales[f] = *reinterpret_cast<const v4f*>(&s.sb[n + quad * (4 * NF) + f * 4]);
     }
+    v4f d[2][NF];
+    float factor[2];
 #pragma unroll
-    for (int e = 0; e < MF; ++e) {
-      const int row = m + e * 16 + lane % 16;
-      const v8i a = fragment(s.a, row, quad);
-      const float sa = BROWS == 1 ? s.sa[row] : s.sa[row] * sb;
+    for (int e = 0; e <= MF; ++e) {
+      v8i next;
+      float next_sa = 0;
+      if (e + 1 < MF) {
+        next = join(a_lo + (e + 1) * 2048, a_hi + (e + 1) * 2048);
+        next_sa = s.sa[m + (e + 1) * 16];
+      }
+      factor[e & 1] = BROWS == 1 ? sa : sa * sb;
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
-        const v4f d = tile_product<AT, kExact>(b[f], a);
+        if (e < MF) d[e & 1][f] = tile_product<AT, kExact>(b[f], a);
+        if (e > 0) {
+          const float by = factor[(e - 1) & 1];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          acc[e][f][i] = __builtin_fmaf(BROWS == 1 ? sa * scales[f][i] : sa, d[i], acc[e][f][i]);
+          for (int i = 0; i < 4; ++i)
+            acc[e - 1][f][i] =
+                __builtin_fmaf(BROWS == 1 ? by * scales[f][i] : by, d[(e - 1) & 1][f][i], acc[e - 1][f][i]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
+      a = next;
+      sa = next_sa;
     }
   }
 
@@ -334,12 +357,12 @@ struct Tiled {
 #pragma unroll
     for (int i = 0; i < kLoadsA; ++i) {
       const int row = (i * kWaves + wave) * 8 + lane / 8;
-      q.ao[i] = min(row, mlast) * static_cast<uint32_t>(p.a_stride) + part_at(row, lane & 7) * 16;
+      q.ao[i] = min(row, mlast) * static_cast<uint32_t>(p.a_stride) + a_part(row, lane & 7) * 16;
     }
 #pragma unroll
     for (int i = 0; i < kLoadsB; ++i) {
       const int row = (i * kWaves + wave) * 8 + lane / 8;
-      q.bo[i] = min(row, nlast) * static_cast<uint32_t>(p.b_stride) + part_at(row, lane & 7) * 16;
+      q.bo[i] = min(row, nlast) * static_cast<uint32_t>(p.b_stride) + b_part<NF>(row, lane & 7) * 16;
     }
     q.sa = p.sa + t.m0 * p.blocks;
     q.sao = min(static_cast<int>(threadIdx.x), mlast) * static_cast<uint32_t>(p.blocks) * 4;
@@ -354,10 +377,23 @@ struct Tiled {
     float acc[MF][NF][4] = {};
     const int64_t whole = t.k0 + (t.k1 - t.k0) / 128 * 128;
     int64_t k = t.k0;
-    const auto sb = [&](int64_t at) { return BROWS == 1 ? 0.0f : sb_row[at / 128]; };
+    // of 64 blocks a lane holds the scale of one
+    float held = 0;
+    const auto sb = [&](int64_t at) {
+      if constexpr (BROWS == 1) return 0.0f;
+      return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(held), static_cast<int>(at / 128 % 64)));
+    };
+    const auto hold = [&](int64_t at) {
+      if constexpr (BROWS != 1)
+        if (at / 128 % 64 == 0) {
+          held = sb_row[at / 128 + lane < p.blocks ? at / 128 + lane : p.blocks - 1];
+          asm volatile("" : "+v"(held));  // waited for here, and not among the loads to LDS
+        }
+    };
     if (k < whole) {
       stage(s0, q, k, wave);
       while (true) {
+        hold(k);
         wait_loads();
         __syncthreads();
         if (k + 128 < whole) stage(s1, q, k + 128, wave);
@@ -373,6 +409,7 @@ struct Tiled {
       }
     }
     if (k < t.k1) {
+      hold(k);
       __syncthreads();
       stage_rest(s0, q, k, t.k1);
       __syncthreads();
