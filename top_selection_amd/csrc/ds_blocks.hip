@@ -7,8 +7,8 @@ namespace {
 
 // scale = max(|block|, 2^-100) / largest; q = x / scale. The quotient is the correctly rounded one by
 // Markstein's theorem: with inv the correctly rounded reciprocal and q0 = x inv, q0 + (x - q0 scale) inv in
-// two fused steps is x / scale rounded once, as long as the remainder is no subnormal: blocks below 2^-60
-// divide.
+// two fused steps is x / scale rounded once, as long as the remainder is no subnormal: blocks below 2^-60 are
+// multiplied by 2^64 first (scale too), which is exact.
 template <int QT>
 struct Eight;
 template <>
@@ -32,28 +32,27 @@ struct Eight<DS_E5M2> {
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
 struct Scale {
-  float scale, inv;
-  bool tiny;
+  float scale;         // as it is stored
+  float by, inv, raise;  // raise scale, its reciprocal (0: the block is not finite), 1 or 2^64
 };
 template <int QT>
 __device__ __forceinline__ Scale scale_of(uint32_t most) {
-  if (most >= 0x7F800000u) return {__uint_as_float(0x7FC00000u), 0.0f, false};
+  if (most >= 0x7F800000u) return {__uint_as_float(0x7FC00000u), 0.0f, 0.0f, 0.0f};
   const float top = fmaxf(__uint_as_float(most), 0x1p-100f);
-  const float scale = top / Eight<QT>::kLargest;
-  return {scale, 1.0f / scale, top < 0x1p-60f};
+  const float scale = top / Eight<QT>::kLargest, raise = top < 0x1p-60f ? 0x1p64f : 1.0f;
+  return {scale, scale * raise, 1.0f / (scale * raise), raise};
 }
 
 // Four elements. A block without a scale is 0 (its infinities and NaN are not converted).
-template <int QT>
+template <int QT, bool RAISE>
 __device__ __forceinline__ uint32_t quantize4(float a, float b, float c, float d, const Scale& s) {
   const auto one = [&](float v) {
-    if (s.tiny) return v / s.scale;
-    const float q0 = v * s.inv;
-    return __builtin_fmaf(__builtin_fmaf(-q0, s.scale, v), s.inv, q0);
+    const float x = RAISE ? v * s.raise : v, q0 = x * s.inv;
+    return __builtin_fmaf(__builtin_fmaf(-q0, s.by, x), s.inv, q0);
   };
-  if (s.inv == 0.0f) return 0;
   const int lo = Eight<QT>::template pack<false>(one(a), one(b), 0);
-  return static_cast<uint32_t>(Eight<QT>::template pack<true>(one(c), one(d), lo));
+  const uint32_t q = static_cast<uint32_t>(Eight<QT>::template pack<true>(one(c), one(d), lo));
+  return s.inv == 0.0f ? 0u : q;
 }
 
 // Sixteen elements of a row from column c on, 0 past n.
@@ -77,14 +76,17 @@ __device__ __forceinline__ void load16(const typename Elem<DT>::T* row, int64_t 
 __device__ __forceinline__ uint32_t most16(const float (&v)[16]) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) m = max(m, magnitude(v[i]));
+  for (int i = 0; i < 16; i += 2) m = max(max(magnitude(v[i]), magnitude(v[i + 1])), m);  // (one instruction of three)
   return m;
 }
 
 template <int QT>
 __device__ __forceinline__ uint4 quantize16(const float (&v)[16], const Scale& s) {
-  return {quantize4<QT>(v[0], v[1], v[2], v[3], s), quantize4<QT>(v[4], v[5], v[6], v[7], s),
-          quantize4<QT>(v[8], v[9], v[10], v[11], s), quantize4<QT>(v[12], v[13], v[14], v[15], s)};
+  if (__any(s.raise != 1.0f))
+    return {quantize4<QT, true>(v[0], v[1], v[2], v[3], s), quantize4<QT, true>(v[4], v[5], v[6], v[7], s),
+            quantize4<QT, true>(v[8], v[9], v[10], v[11], s), quantize4<QT, true>(v[12], v[13], v[14], v[15], s)};
+  return {quantize4<QT, false>(v[0], v[1], v[2], v[3], s), quantize4<QT, false>(v[4], v[5], v[6], v[7], s),
+          quantize4<QT, false>(v[8], v[9], v[10], v[11], s), quantize4<QT, false>(v[12], v[13], v[14], v[15], s)};
 }
 
 __device__ __forceinline__ int64_t plan_end(const Plan& q) {
@@ -143,57 +145,101 @@ __global__ __launch_bounds__(256) void quantize_row_kernel(QuantizeParams p) {
   }
 }
 
-// A workgroup takes 128 positions of 64 columns through LDS; four lanes take a column.
+// A workgroup takes 128 positions of 64 columns through LDS: rows are read in vectors (all of a thread's at
+// once: first the rows' numbers, then the rows), and a thread takes 32 elements of one (fp32) or two (bf16)
+// columns, four or eight lanes a column, whose 16-byte stores make whole lines. The rows' distance in LDS makes the
+// reads down the columns meet every bank once.
 template <int DT, int QT>
-__global__ __launch_bounds__(256) void quantize_column_kernel(QuantizeParams p) {
+__global__ __launch_bounds__(256, 4) void quantize_column_kernel(QuantizeParams p) {
   using T = typename Elem<DT>::T;
-  constexpr int V = Elem<DT>::kPer16, kCols = 64, kPerRow = kCols / V, kRows = 256 / kPerRow;
+  constexpr int V = Elem<DT>::kPer16, kCols = 64, kPerRow = kCols / V, kRows = 256 / kPerRow, kEach = 128 / kRows;
+  constexpr int kPairs = DT == DS_BF16 ? 2 : 1;  // columns a 32-bit word
+  constexpr int kStep = kCols / kPairs + 1;      // words a row
   using Vt = Vec<DT, V>;
-  __shared__ T tile[128][kCols + 4 / sizeof(T)];
+  __shared__ uint32_t tile[128 * kStep + 8];
+  const auto word = [&](int row) { return row * kStep + (kPairs == 2 ? (row >> 6) * 8 : 0); };
   const bool sorted = p.plan.place != nullptr;
   const int64_t P = sorted ? p.plan.capacity : p.rows, end = sorted ? plan_end(p.plan) : P;
-  const int64_t col_units = (p.n + kCols - 1) / kCols, unit = p.unit0 + blockIdx.x;
-  const int64_t p0 = unit / col_units * 128, c0 = unit % col_units * kCols;
-  if (p0 >= end) return;
-  const int tc = threadIdx.x % kPerRow * V;
-  for (int i = threadIdx.x / kPerRow; i < 128; i += kRows) {
-    int64_t r = -1;
-    if (p0 + i < end) {
-      r = p0 + i;
+  // Neighbouring workgroups are on eight XCDs: each takes an eighth of the columns, so that a row's second and
+  // later readings (a token's other experts) find it in that XCD's L2.
+  const int64_t per = p.col_units, unit = p.unit0 + blockIdx.x, turn = unit / p.xcds;
+  const int64_t p0 = turn / per * 128, c0 = (unit % p.xcds * per + turn % per) * kCols;
+  if (p0 >= end || c0 >= p.n) return;
+  const int tc = threadIdx.x % kPerRow * V, tr = threadIdx.x / kPerRow;
+  // where the positions' rows begin (one division a position); padding is read from the first row and cleared
+  const T* x = static_cast<const T*>(p.x);
+  __shared__ int64_t rows[128];
+  if (threadIdx.x < 128) {
+    const int64_t at = p0 + threadIdx.x;
+    int64_t from = -1;
+    if (at < end) {
+      from = at;
       if (sorted) {
-        const int s = p.plan.order[p0 + i];
-        r = s >= 0 && s < p.plan.rows * p.plan.k ? s / p.plan.k : -1;
+        const int slot = p.plan.order[at];
+        from = slot >= 0 && slot < p.plan.rows * p.plan.k ? slot / p.plan.k : -1;
       }
     }
-    typename Vt::type d = {};
-    if (r >= 0) {
-      const T* row = static_cast<const T*>(p.x) + r * p.row_stride + c0 + tc;
-      if (c0 + tc + V <= p.n) {
-        d = *reinterpret_cast<const typename Vt::unaligned*>(row);
-      } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-          if (c0 + tc + e < p.n) d[e] = row[e];
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) tile[i][tc + e] = d[e];
+    rows[threadIdx.x] = from < 0 ? -1 : from * p.row_stride;
   }
   __syncthreads();
-  const int col = threadIdx.x / 4, part = threadIdx.x % 4;
-  if (c0 + col >= p.n) return;
-  float v[2][16];
+  int64_t from[kEach];
+  typename Vt::type d[kEach];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i / 16][i % 16] = Elem<DT>::widen(tile[part * 32 + i][col]);
-  const uint32_t most =
-      row_reduce<2>(max(most16(v[0]), most16(v[1])), [](uint32_t a, uint32_t b) { return max(a, b); });
-  const Scale s = scale_of<QT>(most);
-  const int64_t wide = (P + 15) / 16 * 16, at = p0 + part * 32;
-  uint8_t* q = p.q + (c0 + col) * p.q_stride + at;
+  for (int i = 0; i < kEach; ++i) from[i] = rows[tr + i * kRows];
+  if (c0 + kCols <= p.n) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-    if (at + 16 * h < wide) *reinterpret_cast<uint4*>(q + 16 * h) = quantize16<QT>(v[h], s);
-  if (part == 0) p.scales[(c0 + col) * ((P + 127) / 128) + p0 / 128] = s.scale;
+    for (int i = 0; i < kEach; ++i)
+      d[i] = *reinterpret_cast<const typename Vt::unaligned*>(x + (from[i] < 0 ? 0 : from[i]) + c0 + tc);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const int64_t c = c0 + tc + e;
+        const T one = x[(from[i] < 0 ? 0 : from[i]) + (c < p.n ? c : p.n - 1)];
+        d[i][e] = c < p.n ? one : T{0};
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    if (from[i] < 0) d[i] = typename Vt::type{};
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const auto w = __builtin_bit_cast(__attribute__((ext_vector_type(4))) uint32_t, d[i]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) tile[word(tr + i * kRows) + tc / kPairs + e] = w[e];
+  }
+  __syncthreads();
+  constexpr int kLanes = 4 * kPairs;  // a column
+  const int part = threadIdx.x % kLanes, col = threadIdx.x / kLanes * kPairs;
+  float v[2][16];  // bf16: of two columns; fp32: of rows 64 apart
+#pragma unroll
+  for (int i = 0; i < 32 / kPairs; ++i) {
+    const uint32_t w = tile[word(i / 16 * 64 + part * 16 + i % 16) + col / kPairs];
+    if constexpr (kPairs == 2) {
+      v[0][i] = __uint_as_float(w << 16);
+      v[1][i] = __uint_as_float(w & 0xFFFF0000u);
+    } else {
+      v[i / 16][i % 16] = __uint_as_float(w);
+    }
+  }
+  const auto top = [](uint32_t a, uint32_t b) { return max(a, b); };
+  Scale s[2];
+  if constexpr (kPairs == 2) {
+    s[0] = scale_of<QT>(row_reduce<3>(most16(v[0]), top));
+    s[1] = scale_of<QT>(row_reduce<3>(most16(v[1]), top));
+  } else {
+    s[0] = s[1] = scale_of<QT>(row_reduce<2>(max(most16(v[0]), most16(v[1])), top));
+  }
+  const int64_t wide = (P + 15) / 16 * 16, blocks = (P + 127) / 128;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t c = c0 + col + (kPairs == 2 ? h : 0), at = p0 + part * 16 + (kPairs == 2 ? 0 : h * 64);
+    if (c < p.n) {
+      if (at < wide) *reinterpret_cast<uint4*>(p.q + c * p.q_stride + at) = quantize16<QT>(v[h], s[h]);
+      if (part == 0 && (kPairs == 2 || h == 0)) p.scales[c * blocks + p0 / 128] = s[h].scale;
+    }
+  }
 }
 
 // A workgroup takes a tile of 128 x 128; eight lanes take a row's 128, four rows a thread.
@@ -241,7 +287,10 @@ hipError_t quantize_of(int layout, QuantizeParams p, hipStream_t s) {
   }
   if (layout == DS_BLOCK_COLUMN) {
     const int64_t P = sorted ? p.plan.capacity : p.rows;
-    return launch_units(quantize_column_kernel<DT, QT>, p, (P + 127) / 128 * ((p.n + 63) / 64), 256, s);
+    const int64_t units = (p.n + 63) / 64;
+    p.xcds = units >= 8 ? 8 : 1;
+    p.col_units = (units + p.xcds - 1) / p.xcds;
+    return launch_units(quantize_column_kernel<DT, QT>, p, (P + 127) / 128 * p.col_units * p.xcds, 256, s);
   }
   return launch_units(quantize_tile_kernel<DT, QT>, p, (p.rows + 127) / 128 * nb, 256, s);
 }

@@ -70,6 +70,8 @@ struct QuantizeParams {
   // set by the launcher
   int64_t pad_units;
   int64_t unit0;
+  int64_t col_units;  // columns: workgroups across, for each of `xcds`
+  int64_t xcds;
 };
 hipError_t launch_quantize(int dtype, int q_dtype, int layout, QuantizeParams p, hipStream_t s);
 
