@@ -94,6 +94,7 @@ __device__ __forceinline__ int64_t plan_end(const Plan& q) {
   return end < 0 ? 0 : end < q.capacity ? end : q.capacity;
 }
 
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 constexpr int kPadRun = 16;
 
 // Eight lanes take a block of a row, sixteen elements each.
@@ -132,7 +133,7 @@ __global__ __launch_bounds__(256) void quantize_row_kernel(QuantizeParams p) {
   const Scale s = scale_of<QT>(most);
   const uint4 q = quantize16<QT>(v, s);
   const auto put = [&](int64_t at) {
-    if (c < nc) *reinterpret_cast<uint4*>(p.q + at * p.q_stride + c) = q;
+    if (c < nc) __builtin_nontemporal_store(v4u{q.x, q.y, q.z, q.w}, reinterpret_cast<v4u*>(p.q + at * p.q_stride + c));
     if (threadIdx.x % 8 == 0) p.scales[at * nb + b] = s.scale;
   };
   if (!p.plan.place) {

@@ -175,6 +175,18 @@ __device__ __forceinline__ void clear_row(typename Elem<DT>::T* row, int64_t n) 
   if (whole * V + threadIdx.x < n) row[whole * V + threadIdx.x] = 0;
 }
 
+// A team's row; of whole waves it is the same in all lanes, so that places and weights are read as scalars.
+template <int LANES>
+__device__ __forceinline__ int64_t team_row(int64_t unit) {
+  const int64_t r = unit * (256 / LANES) + threadIdx.x / LANES;
+  if constexpr (LANES < 64) return r;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(r));
+  return static_cast<int64_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(r >> 32))) << 32 | lo;
+}
+
+// A row is read once and written to all its slots' positions, a few vectors a lane at a time, past the caches
+// (an ordinary store: 129 us for 8192 x 8 rows of 4096 bf16, this: 122).
+constexpr int kHeld = 4;
 template <int DT, int LANES>
 __global__ __launch_bounds__(256) void gather_kernel(MoveParams p) {
   using T = typename Elem<DT>::T;
@@ -186,16 +198,24 @@ __global__ __launch_bounds__(256) void gather_kernel(MoveParams p) {
     for_padding(p.plan, unit, [&](int64_t at) { clear_row<DT>(out + at * p.out_stride, p.n); });
     return;
   }
-  const int64_t r = (unit - p.pad_units) * (256 / LANES) + threadIdx.x / LANES;
+  const int64_t r = team_row<LANES>(unit - p.pad_units);
   if (r >= p.plan.rows) return;
   const int lane = threadIdx.x % LANES, k = p.plan.k;
   const T* x = static_cast<const T*>(p.x) + r * p.x_stride;
   const int64_t whole = p.n / V, slot = r * k;
-  for (int64_t v = lane; v < whole; v += LANES) {
-    const typename Vt::type d = *reinterpret_cast<const typename Vt::unaligned*>(x + v * V);
+  for (int64_t v0 = lane; v0 < whole; v0 += LANES * kHeld) {
+    typename Vt::type d[kHeld];
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h)
+      if (v0 + h * LANES < whole) d[h] = *reinterpret_cast<const typename Vt::unaligned*>(x + (v0 + h * LANES) * V);
     for (int j = 0; j < k; ++j) {
       const int64_t at = position(p.plan, slot + j);
-      if (at >= 0) *reinterpret_cast<typename Vt::unaligned*>(out + at * p.out_stride + v * V) = d;
+      if (at < 0) continue;
+      T* to = out + at * p.out_stride;
+#pragma unroll
+      for (int h = 0; h < kHeld; ++h)
+        if (v0 + h * LANES < whole)
+          __builtin_nontemporal_store(d[h], reinterpret_cast<typename Vt::unaligned*>(to + (v0 + h * LANES) * V));
     }
   }
   for (int64_t i = whole * V + lane; i < p.n; i += LANES) {
@@ -207,26 +227,40 @@ __global__ __launch_bounds__(256) void gather_kernel(MoveParams p) {
   }
 }
 
+// Rows of y are read once, past the caches: eight slots' at a time, so that their loads wait together.
+constexpr int kSlots = 8;
 template <int DT, int LANES>
 __global__ __launch_bounds__(256) void combine_kernel(MoveParams p) {
   using T = typename Elem<DT>::T;
   constexpr int V = Elem<DT>::kPer16;
   using Vt = Vec<DT, V>;
-  const int64_t r = (p.unit0 + blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
+  const int64_t r = team_row<LANES>(p.unit0 + blockIdx.x);
   if (r >= p.plan.rows) return;
   const int lane = threadIdx.x % LANES, k = p.plan.k;
   const T* y = static_cast<const T*>(p.x);
   T* out = static_cast<T*>(p.out) + r * p.out_stride;
   const int64_t whole = p.n / V, slot = r * k;
+  const auto weight = [&](int j) { return p.weights ? p.weights[slot + j] : 1.0f; };
   for (int64_t v = lane; v < whole; v += LANES) {
     float acc[V] = {};
-    for (int j = 0; j < k; ++j) {
-      const int64_t at = position(p.plan, slot + j);
-      if (at < 0) continue;
-      const float w = p.weights ? p.weights[slot + j] : 1.0f;
-      const typename Vt::type d = *reinterpret_cast<const typename Vt::unaligned*>(y + at * p.x_stride + v * V);
+    for (int j0 = 0; j0 < k; j0 += kSlots) {
+      typename Vt::type d[kSlots];
+      float w[kSlots];
+      int64_t at[kSlots];
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(w, Elem<DT>::widen(d[i]), acc[i]);
+      for (int j = 0; j < kSlots; ++j) {
+        at[j] = j0 + j < k ? position(p.plan, slot + j0 + j) : -1;
+        w[j] = at[j] >= 0 ? weight(j0 + j) : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j)
+        if (at[j] >= 0)
+          d[j] = __builtin_nontemporal_load(reinterpret_cast<const typename Vt::unaligned*>(y + at[j] * p.x_stride + v * V));
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j)
+        if (at[j] >= 0)
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(w[j], Elem<DT>::widen(d[j][i]), acc[i]);
     }
     typename Vt::type o;
 #pragma unroll
@@ -237,16 +271,15 @@ __global__ __launch_bounds__(256) void combine_kernel(MoveParams p) {
     float acc = 0;
     for (int j = 0; j < k; ++j) {
       const int64_t at = position(p.plan, slot + j);
-      if (at < 0) continue;
-      const float w = p.weights ? p.weights[slot + j] : 1.0f;
-      acc = __builtin_fmaf(w, Elem<DT>::widen(y[at * p.x_stride + i]), acc);
+      if (at >= 0) acc = __builtin_fmaf(weight(j), Elem<DT>::widen(y[at * p.x_stride + i]), acc);
     }
     out[i] = Elem<DT>::narrow(acc);
   }
 }
 
-// One wave a row.
-template <int DT>
+// One wave a row: it holds up to 8 vectors a lane of g while it goes through the slots (a longer row's parts
+// one after another), reads y's row, adds their products, and writes the gradient's.
+template <int DT, int NV>
 __global__ __launch_bounds__(256) void combine_grad_kernel(MoveParams p) {
   using T = typename Elem<DT>::T;
   constexpr int V = Elem<DT>::kPer16;
@@ -257,39 +290,56 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(MoveParams p) {
     for_padding(p.plan, unit, [&](int64_t at) { clear_row<DT>(out + at * p.out_stride, p.n); });
     return;
   }
-  const int64_t r = (unit - p.pad_units) * 4 + threadIdx.x / 64;
+  const int64_t r = team_row<64>(unit - p.pad_units);
   if (r >= p.plan.rows) return;
   const int lane = threadIdx.x % 64, k = p.plan.k;
   const T* g = static_cast<const T*>(p.g) + r * p.g_stride;
   const T* y = static_cast<const T*>(p.x);
   const int64_t whole = p.n / V, slot = r * k;
   float mine = 0;  // lane j: the gradient of slot j's weight
-  for (int j = 0; j < k; ++j) {
-    const int64_t at = position(p.plan, slot + j);
-    if (at < 0) continue;
-    const float w = p.weights ? p.weights[slot + j] : 1.0f;
-    float dot = 0;
-    for (int64_t v = lane; v < whole; v += 64) {
-      const typename Vt::type d = *reinterpret_cast<const typename Vt::unaligned*>(g + v * V);
-      if (p.out_weights) {
-        const typename Vt::type e = *reinterpret_cast<const typename Vt::unaligned*>(y + at * p.x_stride + v * V);
+  for (int64_t v0 = lane;; v0 += 64 * NV) {
+    typename Vt::type d[NV];
 #pragma unroll
-        for (int i = 0; i < V; ++i) dot = __builtin_fmaf(Elem<DT>::widen(d[i]), Elem<DT>::widen(e[i]), dot);
+    for (int h = 0; h < NV; ++h)
+      if (v0 + h * 64 < whole) d[h] = *reinterpret_cast<const typename Vt::unaligned*>(g + (v0 + h * 64) * V);
+    const bool last = v0 - lane + 64 * NV >= whole;  // the elements past the last whole vector go with it
+    const int64_t tail = whole * V + lane;
+    const bool one = last && tail < p.n;
+    const float gt = one ? Elem<DT>::widen(g[tail]) : 0.0f;
+    for (int j = 0; j < k; ++j) {
+      const int64_t at = position(p.plan, slot + j);
+      if (at < 0) continue;
+      if (p.out_weights) {
+        const T* from = y + at * p.x_stride;
+        typename Vt::type e[NV];
+#pragma unroll
+        for (int h = 0; h < NV; ++h)
+          if (v0 + h * 64 < whole)
+            e[h] = __builtin_nontemporal_load(reinterpret_cast<const typename Vt::unaligned*>(from + (v0 + h * 64) * V));
+        float dot = one ? gt * Elem<DT>::widen(from[tail]) : 0.0f;
+#pragma unroll
+        for (int h = 0; h < NV; ++h)
+          if (v0 + h * 64 < whole)
+#pragma unroll
+            for (int i = 0; i < V; ++i) dot = __builtin_fmaf(Elem<DT>::widen(d[h][i]), Elem<DT>::widen(e[h][i]), dot);
+        const float sum = wave_sum(dot);
+        if (lane == j) mine += sum;
       }
       if (out) {
-        typename Vt::type o;
+        const float w = p.weights ? p.weights[slot + j] : 1.0f;
+        T* to = out + at * p.out_stride;
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = Elem<DT>::narrow(w * Elem<DT>::widen(d[i]));
-        *reinterpret_cast<typename Vt::unaligned*>(out + at * p.out_stride + v * V) = o;
+        for (int h = 0; h < NV; ++h)
+          if (v0 + h * 64 < whole) {
+            typename Vt::type o;
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[i] = Elem<DT>::narrow(w * Elem<DT>::widen(d[h][i]));
+            __builtin_nontemporal_store(o, reinterpret_cast<typename Vt::unaligned*>(to + (v0 + h * 64) * V));
+          }
+        if (one) to[tail] = Elem<DT>::narrow(w * gt);
       }
     }
-    for (int64_t i = whole * V + lane; i < p.n; i += 64) {
-      const float d = Elem<DT>::widen(g[i]);
-      if (p.out_weights) dot = __builtin_fmaf(d, Elem<DT>::widen(y[at * p.x_stride + i]), dot);
-      if (out) out[at * p.out_stride + i] = Elem<DT>::narrow(w * d);
-    }
-    const float sum = wave_sum(dot);
-    if (lane == j) mine = sum;
+    if (last) break;
   }
   if (p.out_weights && lane < k) p.out_weights[slot + lane] = mine;
 }
@@ -351,6 +401,15 @@ hipError_t combine_of(MoveParams p, hipStream_t s) {
          : lanes == 64 ? launch_units(combine_kernel<DT, 64>, p, units, 256, s)
                        : launch_units(combine_kernel<DT, 256>, p, units, 256, s);
 }
+
+template <int DT>
+hipError_t grad_of(const MoveParams& p, int64_t units, hipStream_t s) {
+  const int64_t v = p.n / Elem<DT>::kPer16;  // vectors of a row
+  return v <= 64    ? launch_units(combine_grad_kernel<DT, 1>, p, units, 256, s)
+         : v <= 128 ? launch_units(combine_grad_kernel<DT, 2>, p, units, 256, s)
+         : v <= 256 ? launch_units(combine_grad_kernel<DT, 4>, p, units, 256, s)
+                    : launch_units(combine_grad_kernel<DT, 8>, p, units, 256, s);
+}
 }  // namespace
 
 hipError_t launch_gather(int dtype, MoveParams p, hipStream_t s) {
@@ -364,8 +423,7 @@ hipError_t launch_combine(int dtype, MoveParams p, hipStream_t s) {
 hipError_t launch_combine_grad(int dtype, MoveParams p, hipStream_t s) {
   p.pad_units = p.out ? pad_units_of(p.plan) : 0;
   const int64_t units = p.pad_units + teams(p.plan.rows, 64);
-  return dtype == DS_BF16 ? launch_units(combine_grad_kernel<DS_BF16>, p, units, 256, s)
-                          : launch_units(combine_grad_kernel<DS_FP32>, p, units, 256, s);
+  return dtype == DS_BF16 ? grad_of<DS_BF16>(p, units, s) : grad_of<DS_FP32>(p, units, s);
 }
 
 }  // namespace ds
