@@ -633,22 +633,32 @@ def _plan(plan: ExpertPlan, device):
     """The plan as the C entries take it, its rows and its capacity."""
     i32 = _torch().int32
     place, order, offsets, align = plan
-    for t, what, dims in ((place, "place", 2), (order, "order", 1), (offsets, "offsets", 1)):
-        if t.dtype != i32 or t.dim() != dims or t.device != device or not t.is_contiguous():
-            raise ValueError(f"the plan's {what} must be a contiguous int32 tensor of {dims} dimensions on {device}")
-    rows, k = place.shape
-    capacity = order.shape[0]
-    return ds_expert_plan(place.data_ptr(), order.data_ptr(), offsets.data_ptr(), rows, capacity, k,
-                          offsets.shape[0] - 1, align), rows, capacity
+    if not (place.dtype == order.dtype == offsets.dtype == i32 and place.device == order.device == offsets.device == device
+            and place.is_contiguous() and order.is_contiguous() and offsets.is_contiguous()):
+        raise ValueError(f"a plan's tensors must be contiguous int32 tensors on {device}")
+    try:
+        rows, k = place.shape
+        capacity, = order.shape
+        ends, = offsets.shape
+    except ValueError:
+        raise ValueError("a plan's place must be 2-D, order and offsets 1-D") from None
+    return ds_expert_plan(place.data_ptr(), order.data_ptr(), offsets.data_ptr(), rows, capacity, k, ends - 1,
+                          align), rows, capacity
 
 
 def ds_expert_capacity(rows: int, k: int, experts: int, align: int = 1) -> int:
     """The length of a plan's order: positions that hold every choice of experts."""
-    c = ctypes.c_int64(0)
-    st = _function("ds_expert_capacity")(rows, k, experts, align, ctypes.byref(c))
-    if st != DS_OK:
-        raise DSError(st, "ds_expert_capacity")
-    return int(c.value)
+    key = ("ds_expert_capacity", rows, k, experts, align)
+    size = _sizes.get(key)
+    if size is None:
+        c = ctypes.c_int64(0)
+        st = _function("ds_expert_capacity")(rows, k, experts, align, ctypes.byref(c))
+        if st != DS_OK:
+            raise DSError(st, "ds_expert_capacity")
+        if len(_sizes) >= 4096:
+            _sizes.clear()
+        size = _sizes[key] = int(c.value)
+    return size
 
 
 def ds_expert_sort_workspace_size(rows: int, k: int, experts: int) -> int:
@@ -662,14 +672,18 @@ def ds_expert_sort(idx, experts: int, align: int = 1, out: Optional[ExpertPlan] 
     torch = _torch()
     if idx.dim() != 2 or idx.dtype != torch.int32 or not idx.is_cuda or not idx.is_contiguous():
         raise ValueError("idx must be a contiguous 2-D int32 device tensor [rows, k]")
-    (rows, k), dev = idx.shape, idx.device
+    shape, dev, i32 = idx.shape, idx.device, torch.int32
+    rows, k = shape
     if out is None:
-        out = ExpertPlan(_empty((rows, k), torch.int32, dev, stream),
-                         _empty((ds_expert_capacity(rows, k, experts, align),), torch.int32, dev, stream),
-                         _empty((experts + 1,), torch.int32, dev, stream), align)
-    elif out.place.shape != idx.shape or out.offsets.shape != (experts + 1,) or out.align != align:
+        capacity = ds_expert_capacity(rows, k, experts, align)
+        place, order = _empty(shape, i32, dev, stream), _empty((capacity,), i32, dev, stream)
+        offsets = _empty((experts + 1,), i32, dev, stream)
+        out = ExpertPlan(place, order, offsets, align)
+        plan = ds_expert_plan(place.data_ptr(), order.data_ptr(), offsets.data_ptr(), rows, capacity, k, experts, align)
+    elif out.place.shape != shape or out.offsets.shape != (experts + 1,) or out.align != align:
         raise ValueError("out must be a plan of idx's shape, of the experts and of the alignment")
-    plan, _, _ = _plan(out, dev)
+    else:
+        plan, _, _ = _plan(out, dev)
     keep, ws, ws_bytes = _scratch(ds_expert_sort_workspace_size(rows, k, experts), workspace, dev, stream)
     _call("ds_expert_sort", dev, stream, idx.data_ptr(), ctypes.byref(plan), ws, ws_bytes)
     return out

@@ -16,29 +16,37 @@ __device__ __forceinline__ int expert_of(const SortParams& p, int64_t slot, int6
   return static_cast<uint32_t>(e) < static_cast<uint32_t>(p.experts) ? e : -1;
 }
 
+constexpr int kTogether = 4;  // slots a lane loads at a time
+
 // Counts of a chunk's slots by expert.
 __global__ __launch_bounds__(1024) void sort_count_kernel(SortParams p) {
   __shared__ int hist[DS_MAX_EXPERTS];
   for (int e = threadIdx.x; e < p.experts; e += 1024) hist[e] = 0;
   __syncthreads();
   const int64_t lo = blockIdx.x * p.chunk, hi = lo + p.chunk < p.slots ? lo + p.chunk : p.slots;
-  for (int64_t s = lo + threadIdx.x; s < hi; s += 1024) {
-    const int e = expert_of(p, s, hi);
-    if (e >= 0) atomicAdd(&hist[e], 1);
+  for (int64_t s = lo + threadIdx.x; s < hi; s += 1024 * kTogether) {
+    int e[kTogether];
+#pragma unroll
+    for (int i = 0; i < kTogether; ++i) e[i] = expert_of(p, s + i * 1024, hi);
+#pragma unroll
+    for (int i = 0; i < kTogether; ++i)
+      if (e[i] >= 0) atomicAdd(&hist[e[i]], 1);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < p.experts; e += 1024) p.counts[static_cast<int64_t>(blockIdx.x) * p.experts + e] = hist[e];
 }
 
+// Places of a chunk's slots. Every workgroup adds up all chunks' counts for itself (they are few and in L2),
+// which saves a launch.
 template <int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void sort_place_kernel(SortParams p) {
   constexpr int T = WAVES * 64;
   extern __shared__ int lds[];
   const int E = p.experts, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int* mine = lds + wave * E;           // [WAVES][E]: the waves' counts, then their next positions
-  int* total = lds + WAVES * E;         // [E]: slots of the expert
-  int* before = total + E;              // [E]: of them in earlier chunks
-  int* start = before + E;              // [E + 1]: offsets
+  int* mine = lds + wave * E;    // [WAVES][E]: the waves' counts, then their next positions
+  int* total = lds + WAVES * E;  // [E]: slots of the expert
+  int* before = total + E;       // [E]: of them in earlier chunks
+  int* start = before + E;       // [E + 1]: offsets
   __shared__ int wave_sums[WAVES];
   for (int i = tid; i < (WAVES + 2) * E; i += T) lds[i] = 0;
   __syncthreads();
@@ -46,25 +54,34 @@ __global__ __launch_bounds__(WAVES * 64) void sort_place_kernel(SortParams p) {
   const int64_t lo = blockIdx.x * p.chunk, hi = lo + p.chunk < p.slots ? lo + p.chunk : p.slots;
   const int64_t sub = ((hi - lo + WAVES - 1) / WAVES + 63) / 64 * 64;
   const int64_t wlo = lo + wave * sub < hi ? lo + wave * sub : hi, whi = wlo + sub < hi ? wlo + sub : hi;
-  for (int64_t s = wlo + lane; s < whi; s += 64) {
-    const int e = expert_of(p, s, whi);
-    if (e >= 0) atomicAdd(&mine[e], 1);
+  for (int64_t s = wlo + lane; s < whi; s += 64 * kTogether) {
+    int e[kTogether];
+#pragma unroll
+    for (int i = 0; i < kTogether; ++i) e[i] = expert_of(p, s + i * 64, whi);
+#pragma unroll
+    for (int i = 0; i < kTogether; ++i)
+      if (e[i] >= 0) atomicAdd(&mine[e[i]], 1);
   }
   if (p.chunks > 1) {
-    // the threads share the chunks' counts: each takes an expert of some chunks
-    const int64_t all = static_cast<int64_t>(p.chunks) * E;
-    for (int64_t i = tid; i < all; i += T) {
-      const int v = p.counts[i], c = static_cast<int>(i / E), e = static_cast<int>(i - static_cast<int64_t>(c) * E);
-      if (v) {
-        atomicAdd(&total[e], v);
-        if (c < static_cast<int>(blockIdx.x)) atomicAdd(&before[e], v);
+    // threads that share an expert take every so many-th chunk
+    const int wide = E <= 64 ? 64 : 1 << (32 - __clz(E - 1)), every = T >= wide ? T / wide : 1;
+    for (int e = tid % wide; e < E; e += T >= wide ? wide : T) {
+      int all = 0, early = 0;
+#pragma unroll 8
+      for (int c = T >= wide ? tid / wide : 0; c < p.chunks; c += every) {
+        const int v = p.counts[static_cast<int64_t>(c) * E + e];
+        all += v;
+        early += c < static_cast<int>(blockIdx.x) ? v : 0;
       }
+      atomicAdd(&total[e], all);
+      atomicAdd(&before[e], early);
     }
-  }
-  __syncthreads();
-  if (p.chunks == 1) {
+    __syncthreads();
+  } else {
+    __syncthreads();
     for (int e = tid; e < E; e += T) {
       int t = 0;
+#pragma unroll
       for (int w = 0; w < WAVES; ++w) t += lds[w * E + e];
       total[e] = t;
     }
@@ -73,9 +90,11 @@ __global__ __launch_bounds__(WAVES * 64) void sort_place_kernel(SortParams p) {
 
   // offsets: an exclusive sum of the padded counts, a run of experts a thread
   const int per = (E + T - 1) / T, e0 = tid * per, e1 = e0 + per < E ? e0 + per : E;
+  const auto padded = [&](int n) { return p.align == 1 ? n : (n + p.align - 1) / p.align * p.align; };
   int run = 0;
-  for (int e = e0; e < e1; ++e) run += (total[e] + p.align - 1) / p.align * p.align;
+  for (int e = e0; e < e1; ++e) run += padded(total[e]);
   int incl = run;
+#pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const int v = __shfl_up(incl, d);
     if (lane >= d) incl += v;
@@ -83,45 +102,63 @@ __global__ __launch_bounds__(WAVES * 64) void sort_place_kernel(SortParams p) {
   if (lane == 63) wave_sums[wave] = incl;
   __syncthreads();
   int at = incl - run;
-  for (int w = 0; w < wave; ++w) at += wave_sums[w];
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) at += w < wave ? wave_sums[w] : 0;
   for (int e = e0; e < e1; ++e) {
     start[e] = at;
-    at += (total[e] + p.align - 1) / p.align * p.align;
+    at += padded(total[e]);
     if (e == E - 1) start[E] = at;
   }
   __syncthreads();
   for (int e = tid; e < E; e += T) {
-    int next = start[e] + before[e];
+    int c[WAVES], next = start[e] + before[e];
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) c[w] = lds[w * E + e];
+#pragma unroll
     for (int w = 0; w < WAVES; ++w) {
-      const int c = lds[w * E + e];
       lds[w * E + e] = next;
-      next += c;
+      next += c[w];
     }
   }
   __syncthreads();
 
   // places
   const int bits = 32 - __clz(E);
-  for (int64_t s0 = wlo; s0 < whi; s0 += 64) {
-    const int64_t s = s0 + lane;
-    const int e = expert_of(p, s, whi);
-    uint64_t same = __ballot(e >= 0);
-    for (int b = 0; b < bits; ++b) {
-      const uint64_t set = __ballot((e >> b) & 1);
-      same &= ((e >> b) & 1) ? set : ~set;
+  for (int64_t s0 = wlo + lane; s0 < wlo + sub && wlo < whi; s0 += 64 * kTogether) {
+    int e[kTogether];
+#pragma unroll
+    for (int i = 0; i < kTogether; ++i) e[i] = expert_of(p, s0 + i * 64, whi);
+#pragma unroll
+    for (int i = 0; i < kTogether; ++i) {
+      const int64_t s = s0 + i * 64;
+      uint64_t same = __ballot(e[i] >= 0);
+      for (int b = 0; b < bits; ++b) {
+        const uint64_t set = __ballot((e[i] >> b) & 1);
+        same &= ((e[i] >> b) & 1) ? set : ~set;
+      }
+      int pos = -1;
+      if (e[i] >= 0) pos = mine[e[i]] + __popcll(same & ((1ull << lane) - 1));
+      wave_sync();
+      if (e[i] >= 0 && (same >> lane) == 1) mine[e[i]] = pos + 1;  // the last of the equals
+      wave_sync();
+      if (s < whi) p.place[s] = pos;
+      if (pos >= 0) p.order[pos] = static_cast<int>(s);
     }
-    int pos = -1;
-    if (e >= 0) pos = mine[e] + __popcll(same & ((1ull << lane) - 1));
-    wave_sync();
-    if (e >= 0 && (same >> lane) == 1) mine[e] = pos + 1;  // the last of the equals
-    wave_sync();
-    if (s < whi) p.place[s] = pos;
-    if (pos >= 0) p.order[pos] = static_cast<int>(s);
   }
 
-  // padding at the segments' ends, shared by the workgroups, and what lies past the end
-  for (int e = blockIdx.x; e < E; e += p.chunks) {
-    for (int i = start[e] + total[e] + tid; i < start[e + 1]; i += T) p.order[i] = -1;
+  // padding at the segments' ends, an expert a wave (a lane holds where one's padding lies), and what is
+  // past the end
+  if (p.align > 1) {
+    const int step = p.chunks * WAVES;
+    for (int first = blockIdx.x * WAVES + wave; first < E; first += step * 64) {
+      const int e = first + lane * step;
+      const int from = e < E ? start[e] + total[e] : 0, to = e < E ? start[e + 1] : 0;
+      for (uint64_t left = __ballot(from < to); left; left &= left - 1) {
+        const int l = __ffsll(static_cast<unsigned long long>(left)) - 1;
+        const int end = __builtin_amdgcn_readlane(to, l);
+        for (int i = __builtin_amdgcn_readlane(from, l) + lane; i < end; i += 64) p.order[i] = -1;
+      }
+    }
   }
   for (int64_t i = start[E] + static_cast<int64_t>(blockIdx.x) * T + tid; i < p.capacity;
        i += static_cast<int64_t>(p.chunks) * T)
@@ -265,7 +302,7 @@ __global__ __launch_bounds__(256) void combine_kernel(MoveParams p) {
     typename Vt::type o;
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = Elem<DT>::narrow(acc[i]);
-    *reinterpret_cast<typename Vt::unaligned*>(out + v * V) = o;
+    __builtin_nontemporal_store(o, reinterpret_cast<typename Vt::unaligned*>(out + v * V));
   }
   for (int64_t i = whole * V + lane; i < p.n; i += LANES) {
     float acc = 0;
