@@ -113,79 +113,112 @@ __device__ __forceinline__ bool find_tile(const ProductParams& p, int64_t mt, Ti
   return true;
 }
 
-// Sixteen bytes of a row's block, 0 past the end.
-__device__ __forceinline__ v4i load_part(const uint8_t* row, int64_t k, int64_t k1) {
-  return k < k1 ? *reinterpret_cast<const v4i*>(row + k) : v4i{0, 0, 0, 0};
+// A row's part of a block: 32 bytes a lane, 0 past the end.
+__device__ __forceinline__ v8i load_block(const uint8_t* row, int64_t k, int64_t k1, int quad) {
+  v4i lo{0, 0, 0, 0}, hi{0, 0, 0, 0};
+  const int64_t at = k + quad * 16;
+  if (k + 128 <= k1) {  // (the same in all lanes)
+    lo = *reinterpret_cast<const v4i*>(row + at);
+    hi = *reinterpret_cast<const v4i*>(row + at + 64);
+  } else {
+    if (at < k1) lo = *reinterpret_cast<const v4i*>(row + at);
+    if (at + 64 < k1) hi = *reinterpret_cast<const v4i*>(row + at + 64);
+  }
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-template <int OT>
-__device__ __forceinline__ void store4(typename Elem<OT>::T* out, int64_t n0, int64_t n, const float (&v)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (n0 + i < n) out[n0 + i] = Elem<OT>::narrow(v[i]);
-}
-
-// Sixteen rows of a and 64 of b a workgroup; its four waves take every fourth block of the inner
-// axis, and their sums are joined in LDS in the waves' order.
-template <int AT, int BROWS, int GROUP, int OT>
-__global__ __launch_bounds__(256) void product_small_kernel(ProductParams p) {
-  __shared__ float part[4][64][16 + 1];
+// Few rows: b is read once from memory, straight into registers, and that is what bounds the kernel. A
+// workgroup takes 16 MF rows of a and 16 NF of b; its W waves take every W-th block of the inner axis, the next
+// one's loads on their way while one is worked on, and their sums are joined in LDS in the waves' order. The sums
+// are exact (block_product): the matrix unit has time.
+template <int AT, int BROWS, int GROUP, int OT, int MF, int NF, int W>
+__global__ __launch_bounds__(W * 64) void product_small_kernel(ProductParams p) {
+  constexpr int TN = NF * 16;
+  __shared__ float part[W][64][MF * NF * 4 + 1];
   const int64_t unit = p.unit0 + blockIdx.x;
   Tile t;
-  if (!find_tile<GROUP, 16>(p, unit / p.n_tiles, t)) return;
-  const int64_t n0 = unit % p.n_tiles * 64;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, quad = lane >> 4;
+  if (!find_tile<GROUP, MF * 16>(p, unit / p.n_tiles, t)) return;
+  const int64_t n0 = unit % p.n_tiles * TN;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), row = lane & 15, quad = lane >> 4;
   const int64_t b0 = GROUP == DS_GROUP_ROWS ? t.group * p.n : 0;
-  const int64_t b_blocks = (p.n + 127) / 128;
-  const bool a_live = t.m0 + row < t.m1;
-  const uint8_t* a = p.a + (t.m0 + row) * p.a_stride;
-  float acc[4][4] = {};
-  for (int64_t k = t.k0 + wave * 128; k < t.k1; k += 4 * 128) {
-    const int64_t kb = k / 128;
-    v4i a0{}, a1{};
-    float sa = 0;
-    if (a_live) {
-      a0 = load_part(a, k + quad * 16, t.k1);
-      a1 = load_part(a, k + 64 + quad * 16, t.k1);
-      sa = p.sa[(t.m0 + row) * p.blocks + kb];
-    }
-    const Wide av = widen<AT>(__builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7));
+  const uint8_t *a[MF], *b[NF];  // (rows past the last repeat it; they are not stored)
+  const float *sa[MF], *sb[BROWS == 1 ? NF * 4 : 1];
 #pragma unroll
-    for (int f = 0; f < 4; ++f) {
-      const int64_t n = n0 + f * 16 + row;
-      v4i b0v{}, b1v{};
-      if (n < p.n) {
-        const uint8_t* b = p.b + (b0 + n) * p.b_stride;
-        b0v = load_part(b, k + quad * 16, t.k1);
-        b1v = load_part(b, k + 64 + quad * 16, t.k1);
-      }
-      const v4f d = block_product(widen<DS_E4M3>(__builtin_shufflevector(b0v, b1v, 0, 1, 2, 3, 4, 5, 6, 7)), av);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t nn = n0 + f * 16 + quad * 4 + i;
-        float sb = 0;
-        if (nn < p.n)
-          sb = BROWS == 1 ? p.sb[(b0 + nn) * p.blocks + kb]
-                          : p.sb[((GROUP == DS_GROUP_ROWS ? t.group * b_blocks : 0) + nn / 128) * p.blocks + kb];
-        acc[f][i] = __builtin_fmaf(sa * sb, d[i], acc[f][i]);
-      }
-    }
+  for (int e = 0; e < MF; ++e) {
+    const int64_t m = t.m0 + e * 16 + row < t.m1 ? t.m0 + e * 16 + row : t.m1 - 1;
+    a[e] = p.a + m * p.a_stride;
+    sa[e] = p.sa + m * p.blocks;
   }
 #pragma unroll
-  for (int f = 0; f < 4; ++f)
+  for (int f = 0; f < NF; ++f) {
+    const int64_t n = n0 + f * 16 + row < p.n ? n0 + f * 16 + row : p.n - 1;
+    b[f] = p.b + (b0 + n) * p.b_stride;
+  }
+  if constexpr (BROWS == 1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) part[wave][lane][f * 4 + i] = acc[f][i];
+    for (int q = 0; q < NF * 4; ++q) {
+      const int64_t n = n0 + q / 4 * 16 + quad * 4 + q % 4;
+      sb[q] = p.sb + (b0 + (n < p.n ? n : p.n - 1)) * p.blocks;
+    }
+  } else {
+    sb[0] = p.sb + ((GROUP == DS_GROUP_ROWS ? t.group * ((p.n + 127) / 128) : 0) + n0 / 128) * p.blocks;
+  }
+  struct Block {
+    v8i a[MF], b[NF];
+    float sa[MF], sb[BROWS == 1 ? NF * 4 : 1];
+  };
+  const auto load = [&](int64_t k, Block& q) {
+#pragma unroll
+    for (int f = 0; f < NF; ++f) q.b[f] = load_block(b[f], k, t.k1, quad);
+#pragma unroll
+    for (int e = 0; e < MF; ++e) {
+      q.a[e] = load_block(a[e], k, t.k1, quad);
+      q.sa[e] = sa[e][k / 128];
+    }
+#pragma unroll
+    for (int i = 0; i < (BROWS == 1 ? NF * 4 : 1); ++i) q.sb[i] = sb[i][k / 128];
+  };
+  float acc[MF][NF][4] = {};
+  Block now, next;
+  int64_t k = t.k0 + wave * 128;
+  if (k < t.k1) load(k, now);
+  for (; k < t.k1; k += W * 128) {
+    if (k + W * 128 < t.k1) load(k + W * 128, next);
+    Wide bw[NF];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) bw[f] = widen<DS_E4M3>(now.b[f]);
+#pragma unroll
+    for (int e = 0; e < MF; ++e) {
+      const Wide aw = widen<AT>(now.a[e]);
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        const v4f d = block_product(bw[f], aw);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc[e][f][i] = __builtin_fmaf(now.sa[e] * now.sb[BROWS == 1 ? f * 4 + i : 0], d[i], acc[e][f][i]);
+      }
+    }
+    now = next;
+  }
+#pragma unroll
+  for (int q = 0; q < MF * NF * 4; ++q) part[wave][lane][q] = acc[q / (NF * 4)][q / 4 % NF][q % 4];
   __syncthreads();
-  // wave f stores b rows 16 f on
-  float v[4];
+  // the fragments' results are shared by the waves
+  typename Elem<OT>::T* out = static_cast<typename Elem<OT>::T*>(p.out);
+  const int64_t first = GROUP == DS_GROUP_INNER ? t.group * p.m : 0;
+  for (int q = wave; q < MF * NF; q += W) {
+    float v[4] = {};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int at = wave * 4 + i;
-    v[i] = part[0][lane][at] + part[1][lane][at] + part[2][lane][at] + part[3][lane][at];
+    for (int w = 0; w < W; ++w)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += part[w][lane][q * 4 + i];
+    const int64_t m = t.m0 + q / NF * 16 + row, n = n0 + q % NF * 16 + quad * 4;
+    if (m >= t.m1) continue;
+    typename Elem<OT>::T* to = out + (first + m) * p.out_stride;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < p.n) to[n + i] = Elem<OT>::narrow(v[i]);
   }
-  if (!a_live) return;
-  const int64_t out_row = (GROUP == DS_GROUP_INNER ? t.group * p.m : 0) + t.m0 + row;
-  store4<OT>(static_cast<typename Elem<OT>::T*>(p.out) + out_row * p.out_stride, n0 + wave * 16 + quad * 4, p.n, v);
 }
 
 // ------------------------------------------------------------------------- tiles through LDS
@@ -510,23 +543,34 @@ void count_tiles(ProductParams& p, int tm, int tn) {
   p.units = p.m_tiles * p.n_tiles;
 }
 
+template <int AT, int BROWS, int GROUP, int OT, int MF, int NF, int W>
+hipError_t small_of(ProductParams& p, hipStream_t s) {
+  count_tiles<GROUP>(p, MF * 16, NF * 16);
+  return launch_units(product_small_kernel<AT, BROWS, GROUP, OT, MF, NF, W>, p, p.units, W * 64, s);
+}
+
+template <int AT, int BROWS, int GROUP, int OT, int WM, int WN, int MF, int NF>
+hipError_t tiled_of(ProductParams& p, hipStream_t s) {
+  count_tiles<GROUP>(p, WM * MF * 16, WN * NF * 16);
+  return launch_units(product_tiled_kernel<AT, BROWS, GROUP, OT, WM, WN, MF, NF>, p, (p.units + 255) / 256 * 256,
+                      WM * WN * 64, s);
+}
+
 template <int AT, int BROWS, int GROUP, int OT>
 hipError_t product_of(ProductParams p, hipStream_t s) {
   // rows of a per segment, on average
-  const int64_t rows = GROUP == DS_GROUP_ROWS ? p.m / p.groups : p.m;
+  const int64_t rows = GROUP == DS_GROUP_ROWS ? (p.m + p.groups - 1) / p.groups : p.m;
   // (a tile's rows are reached by 32-bit offsets)
   if (rows >= 64 && p.a_stride < (1 << 23) && p.b_stride < (1 << 23)) {
     // (as bf16 the fragments take more registers)
-    if constexpr (OT == DS_FP32) {
-      count_tiles<GROUP>(p, 256, 128);
-      return launch_units(product_tiled_kernel<AT, BROWS, GROUP, OT, 4, 2, 4, 4>, p, (p.units + 255) / 256 * 256, 512, s);
-    } else {
-      count_tiles<GROUP>(p, 256, 256);
-      return launch_units(product_tiled_kernel<AT, BROWS, GROUP, OT, 2, 4, 8, 4>, p, (p.units + 255) / 256 * 256, 512, s);
-    }
+    if constexpr (OT == DS_FP32) return tiled_of<AT, BROWS, GROUP, OT, 4, 2, 4, 4>(p, s);
+    return tiled_of<AT, BROWS, GROUP, OT, 2, 4, 8, 4>(p, s);
   }
+  if (rows > 16) return small_of<AT, BROWS, GROUP, OT, 4, 4, 4>(p, s);
+  // enough workgroups to fill the card, by narrower ones
   count_tiles<GROUP>(p, 16, 64);
-  return launch_units(product_small_kernel<AT, BROWS, GROUP, OT>, p, p.units, 256, s);
+  if (p.units >= 2 * kCus) return small_of<AT, BROWS, GROUP, OT, 1, 4, 4>(p, s);
+  return small_of<AT, BROWS, GROUP, OT, 1, 1, 8>(p, s);
 }
 
 template <int AT, int OT>
