@@ -1,4 +1,6 @@
 // Products of 8-bit operands with a scale for each block of 128 along the inner axis.
+#include <type_traits>
+
 #include "ds_expert.h"
 #include "ds_rows_device.h"
 
@@ -128,8 +130,9 @@ __device__ __forceinline__ v8i load_block(const uint8_t* row, int64_t k, int64_t
 }
 
 // Few rows: b is read once from memory, straight into registers, and that is what bounds the kernel. A
-// workgroup takes 16 MF rows of a and 16 NF of b; its W waves take every W-th block of the inner axis, the next
-// one's loads on their way while one is worked on, and their sums are joined in LDS in the waves' order. The sums
+// workgroup takes 16 MF rows of a and 16 NF of b; its W waves take every W-th block of the inner axis, and their sums
+// are joined in LDS in the waves' order. Loads of one block a wave at a time and many waves: with two (four)
+// blocks' registers fewer fit (32 rows of 27 experts, 2048 x 4096: 40 us; 42, 52). The sums
 // are exact (block_product): the matrix unit has time.
 template <int AT, int BROWS, int GROUP, int OT, int MF, int NF, int W>
 __global__ __launch_bounds__(W * 64) void product_small_kernel(ProductParams p) {
@@ -163,42 +166,33 @@ __global__ __launch_bounds__(W * 64) void product_small_kernel(ProductParams p) 
   } else {
     sb[0] = p.sb + ((GROUP == DS_GROUP_ROWS ? t.group * ((p.n + 127) / 128) : 0) + n0 / 128) * p.blocks;
   }
-  struct Block {
-    v8i a[MF], b[NF];
-    float sa[MF], sb[BROWS == 1 ? NF * 4 : 1];
-  };
-  const auto load = [&](int64_t k, Block& q) {
+  float acc[MF][NF][4] = {};
+  for (int64_t k = t.k0 + wave * 128; k < t.k1; k += W * 128) {
+    v8i aq[MF], bq[NF];
+    float by_a[MF], by_b[BROWS == 1 ? NF * 4 : 1];
 #pragma unroll
-    for (int f = 0; f < NF; ++f) q.b[f] = load_block(b[f], k, t.k1, quad);
+    for (int f = 0; f < NF; ++f) bq[f] = load_block(b[f], k, t.k1, quad);
 #pragma unroll
     for (int e = 0; e < MF; ++e) {
-      q.a[e] = load_block(a[e], k, t.k1, quad);
-      q.sa[e] = sa[e][k / 128];
+      aq[e] = load_block(a[e], k, t.k1, quad);
+      by_a[e] = sa[e][k / 128];
     }
 #pragma unroll
-    for (int i = 0; i < (BROWS == 1 ? NF * 4 : 1); ++i) q.sb[i] = sb[i][k / 128];
-  };
-  float acc[MF][NF][4] = {};
-  Block now, next;
-  int64_t k = t.k0 + wave * 128;
-  if (k < t.k1) load(k, now);
-  for (; k < t.k1; k += W * 128) {
-    if (k + W * 128 < t.k1) load(k + W * 128, next);
+    for (int i = 0; i < (BROWS == 1 ? NF * 4 : 1); ++i) by_b[i] = sb[i][k / 128];
     Wide bw[NF];
 #pragma unroll
-    for (int f = 0; f < NF; ++f) bw[f] = widen<DS_E4M3>(now.b[f]);
+    for (int f = 0; f < NF; ++f) bw[f] = widen<DS_E4M3>(bq[f]);
 #pragma unroll
     for (int e = 0; e < MF; ++e) {
-      const Wide aw = widen<AT>(now.a[e]);
+      const Wide aw = widen<AT>(aq[e]);
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
-        const v4f d = block_product(bw[f], aw);
+        const v4f sum = block_product(bw[f], aw);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          acc[e][f][i] = __builtin_fmaf(now.sa[e] * now.sb[BROWS == 1 ? f * 4 + i : 0], d[i], acc[e][f][i]);
+          acc[e][f][i] = __builtin_fmaf(by_a[e] * by_b[BROWS == 1 ? f * 4 + i : 0], sum[i], acc[e][f][i]);
       }
     }
-    now = next;
   }
 #pragma unroll
   for (int q = 0; q < MF * NF * 4; ++q) part[wave][lane][q] = acc[q / (NF * 4)][q / 4 % NF][q % 4];
@@ -253,7 +247,8 @@ __device__ __forceinline__ v4f tile_product(const Operand<DS_E4M3, true>& b, con
 
 // Loads of sixteen (four) bytes a lane from base + offset to LDS from `lds` on, lane after lane, past the
 // registers. The compiler holds every LDS read back until such loads have arrived, wherever they write,
-// so they are issued behind its back: wait_loads() before the barrier that the readers wait at.
+// so they are issued behind its back: wait_loads (for all but the newest LEFT) before the barrier that the readers
+// wait at.
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)p));
 }
@@ -263,7 +258,10 @@ __device__ __forceinline__ void load_to_lds16(const void* base, uint32_t offset,
 __device__ __forceinline__ void load_to_lds4(const void* base, uint32_t offset, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(offset), "s"(base), "s"(lds) : "memory");
 }
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"i"(LEFT) : "memory");
+}
 
 template <int TM, int TN, int BROWS>
 struct Stage {
@@ -273,8 +271,8 @@ struct Stage {
   uint8_t b[TN][128];
 };
 
-// WM x WN waves, each of MF x NF fragments of sixteen.
-template <int AT, int BROWS, int GROUP, int OT, int WM, int WN, int MF, int NF>
+// WM x WN waves, each of MF x NF fragments of sixteen; STAGES blocks in LDS.
+template <int AT, int BROWS, int GROUP, int OT, int WM, int WN, int MF, int NF, int STAGES>
 struct Tiled {
   static constexpr int kWaves = WM * WN, kThreads = kWaves * 64, TM = WM * MF * 16, TN = WN * NF * 16;
   static constexpr bool kExact = OT == DS_FP32;
@@ -411,7 +409,7 @@ struct Tiled {
     }
   }
 
-  static __device__ __forceinline__ void run(const ProductParams& p, S (&stages)[2]) {
+  static __device__ __forceinline__ void run(const ProductParams& p, S (&stages)[STAGES]) {
     // eight neighbouring workgroups are on eight XCDs: each XCD takes runs of 32 tiles, whose rows share its L2
     const int64_t id = p.unit0 + blockIdx.x;
     const int64_t unit = (id / 256) * 256 + (id % 8) * 32 + id / 8 % 32;
@@ -449,22 +447,36 @@ struct Tiled {
       const int64_t b_blocks = (p.n + 127) / 128, at = (n0 + wave % WN * (NF * 16)) / 128;
       sb_row += ((GROUP == DS_GROUP_ROWS ? t.group * b_blocks : 0) + (at < b_blocks ? at : b_blocks - 1)) * p.blocks;
     }
-    // Two stages in turn: while a block is worked on in one, the next is on its way to the other. `turn`: all
-    // waves have read block k, and the next has arrived; the one after it is sent for. (Behind the last block
-    // it still waits, and what is read then is not used.)
+    // The stages in turn: while a block is worked on in one, the next ones are on their way to the others. `turn`:
+    // all waves have read block k and the next has arrived; the one that takes block k's place is sent for.
+    // (Behind the last block it still waits, and what is read then is not used.)
     int64_t k = t.k0;
     int now = 0;
-    const auto turn = [&] {
-      wait_loads();
+    const bool extra = wave < TM / 64 || (BROWS == 1 && wave >= kWaves - TN / 64);  // loads scales too
+    const auto arrived = [&](auto ahead) {  // all but the loads of the `ahead` newest stages
+      constexpr int kLoads = kLoadsA + kLoadsB, kAhead = decltype(ahead)::value;
+      static_assert((kLoads + 1) * kAhead < 64, "the counter's range");
+      if (k + STAGES * 128 <= t.k1 && kAhead > 0) {
+        if (extra) {
+          wait_loads<(kLoads + 1) * kAhead>();
+        } else {
+          wait_loads<kLoads * kAhead>();
+        }
+      } else {
+        wait_loads<0>();  // (near the end fewer stages are under way)
+      }
       __syncthreads();
-      if (k + 256 < t.k1) stage(stages[now], q, k + 256, t.k1, wave);
-      now ^= 1;
+    };
+    const auto turn = [&] {
+      arrived(std::integral_constant<int, STAGES - 2>{});
+      if (k + STAGES * 128 < t.k1) stage(stages[now], q, k + STAGES * 128, t.k1, wave);
+      now = now + 1 == STAGES ? 0 : now + 1;
     };
     if (k < t.k1) {
-      stage(stages[0], q, k, t.k1, wave);
-      wait_loads();
-      __syncthreads();
-      if (k + 128 < t.k1) stage(stages[1], q, k + 128, t.k1, wave);
+#pragma unroll
+      for (int i = 0; i < STAGES; ++i)
+        if (k + i * 128 < t.k1) stage(stages[i], q, k + i * 128, t.k1, wave);
+      arrived(std::integral_constant<int, STAGES - 1>{});
     }
     if (wave / WN * (MF * 16) > mlast || wave % WN * (NF * 16) > nlast) {
       // the wave's rows or columns lie past the end: it only loads
@@ -491,7 +503,7 @@ struct Tiled {
         }
         compute(at, sb, h, acc, [&] {
           turn();
-          at.move(now ? kStage : 0u - kStage);
+          at.move(now ? kStage : 0u - (STAGES - 1) * kStage);
         });
       }
 #pragma unroll
@@ -526,10 +538,10 @@ struct Tiled {
   }
 };
 
-template <int AT, int BROWS, int GROUP, int OT, int WM, int WN, int MF, int NF>
+template <int AT, int BROWS, int GROUP, int OT, int WM, int WN, int MF, int NF, int STAGES>
 __global__ __launch_bounds__(WM * WN * 64, 2) void product_tiled_kernel(ProductParams p) {
-  using K = Tiled<AT, BROWS, GROUP, OT, WM, WN, MF, NF>;
-  __shared__ typename K::S stages[2];
+  using K = Tiled<AT, BROWS, GROUP, OT, WM, WN, MF, NF, STAGES>;
+  __shared__ typename K::S stages[STAGES];
   K::run(p, stages);
 }
 
@@ -549,28 +561,40 @@ hipError_t small_of(ProductParams& p, hipStream_t s) {
   return launch_units(product_small_kernel<AT, BROWS, GROUP, OT, MF, NF, W>, p, p.units, W * 64, s);
 }
 
-template <int AT, int BROWS, int GROUP, int OT, int WM, int WN, int MF, int NF>
+template <int AT, int BROWS, int GROUP, int OT, int WM, int WN, int MF, int NF, int STAGES>
 hipError_t tiled_of(ProductParams& p, hipStream_t s) {
   count_tiles<GROUP>(p, WM * MF * 16, WN * NF * 16);
-  return launch_units(product_tiled_kernel<AT, BROWS, GROUP, OT, WM, WN, MF, NF>, p, (p.units + 255) / 256 * 256,
+  return launch_units(product_tiled_kernel<AT, BROWS, GROUP, OT, WM, WN, MF, NF, STAGES>, p, (p.units + 255) / 256 * 256,
                       WM * WN * 64, s);
 }
 
+// Which kernel. Up to 16 rows (a segment, on average) b's bytes are all that counts: narrow workgroups, the
+// narrower where there are few. Above, the one whose rounds of a tile a CU take least; a round's time does not
+// depend on the size much (us for 32 blocks of the inner axis, measured with one round of tiles on the card: small
+// tiles of 32 x 32 11, through LDS 64 x 128 20, 128 x 128 28, 256 x 256 62; with exact sums 16, 36, 60 and, 256 x 128,
+// 86). Small tiles share a CU, so parts of their rounds count.
 template <int AT, int BROWS, int GROUP, int OT>
 hipError_t product_of(ProductParams p, hipStream_t s) {
-  // rows of a per segment, on average
+  constexpr bool kExact = OT == DS_FP32;
   const int64_t rows = GROUP == DS_GROUP_ROWS ? (p.m + p.groups - 1) / p.groups : p.m;
-  // (a tile's rows are reached by 32-bit offsets)
-  if (rows >= 64 && p.a_stride < (1 << 23) && p.b_stride < (1 << 23)) {
-    // (as bf16 the fragments take more registers)
-    if constexpr (OT == DS_FP32) return tiled_of<AT, BROWS, GROUP, OT, 4, 2, 4, 4>(p, s);
-    return tiled_of<AT, BROWS, GROUP, OT, 2, 4, 8, 4>(p, s);
+  const int64_t segments = GROUP == DS_GROUP_NONE ? 1 : p.groups;
+  const auto tiles = [&](int tm, int tn) { return segments * ((rows + tm - 1) / tm) * ((p.n + tn - 1) / tn); };
+  const auto rounds = [&](int tm, int tn) { return static_cast<double>((tiles(tm, tn) + kCus - 1) / kCus); };
+  if (rows <= 16) {
+    if (tiles(16, 32) >= 2 * kCus) return small_of<AT, BROWS, GROUP, OT, 1, 2, 8>(p, s);
+    return small_of<AT, BROWS, GROUP, OT, 1, 1, 8>(p, s);
   }
-  if (rows > 16) return small_of<AT, BROWS, GROUP, OT, 4, 4, 4>(p, s);
-  // enough workgroups to fill the card, by narrower ones
-  count_tiles<GROUP>(p, 16, 64);
-  if (p.units >= 2 * kCus) return small_of<AT, BROWS, GROUP, OT, 1, 4, 4>(p, s);
-  return small_of<AT, BROWS, GROUP, OT, 1, 1, 8>(p, s);
+  const double part = static_cast<double>(tiles(32, 32)) / kCus;
+  const double small = (kExact ? 16 : 11) * (part > 1 ? part : 1), t64 = (kExact ? 36 : 20) * rounds(64, 128);
+  const double t128 = (kExact ? 60 : 28) * rounds(128, 128);
+  const double t256 = kExact ? 86 * rounds(256, 128) : 62 * rounds(256, 256);
+  // (a tile's rows are reached by 32-bit offsets)
+  const bool near = p.a_stride < (1 << 23) && p.b_stride < (1 << 23);
+  if (!near || (small <= t64 && small <= t128 && small <= t256)) return small_of<AT, BROWS, GROUP, OT, 2, 2, 8>(p, s);
+  if (t64 <= t128 && t64 <= t256) return tiled_of<AT, BROWS, GROUP, OT, 2, 4, 2, 2, 6>(p, s);
+  if (t128 <= t256) return tiled_of<AT, BROWS, GROUP, OT, 4, 2, 2, 4, 4>(p, s);
+  if constexpr (kExact) return tiled_of<AT, BROWS, GROUP, OT, 4, 2, 4, 4, 3>(p, s);  // (as bf16 fragments take more registers)
+  return tiled_of<AT, BROWS, GROUP, OT, 2, 4, 8, 4, 2>(p, s);
 }
 
 template <int AT, int OT>
