@@ -569,10 +569,11 @@ hipError_t tiled_of(ProductParams& p, hipStream_t s) {
 }
 
 // Which kernel. Up to 16 rows (a segment, on average) b's bytes are all that counts: narrow workgroups, the
-// narrower where there are few. Above, the one whose rounds of a tile a CU take least; a round's time does not
-// depend on the size much (us for 32 blocks of the inner axis, measured with one round of tiles on the card: small
-// tiles of 32 x 32 11, through LDS 64 x 128 20, 128 x 128 28, 256 x 256 62; with exact sums 16, 36, 60 and, 256 x 128,
-// 86). Small tiles share a CU, so parts of their rounds count.
+// narrower where there are few. Above, the one whose rounds of tiles take least. A round's time hardly depends on
+// how full it is (us for 32 blocks of the inner axis, measured: tiles of 32 x 32 11, through LDS 64 x 128 20, 128 x 128
+// 28, 256 x 256 62; with exact sums 16, 36 and 58); where tiles share a CU (the smallest; the largest of exact
+// sums, two of which hide each other's starts and ends: 665 us for a weights' gradient that 256 x 128 alone
+// took 740 for) parts of rounds count.
 template <int AT, int BROWS, int GROUP, int OT>
 hipError_t product_of(ProductParams p, hipStream_t s) {
   constexpr bool kExact = OT == DS_FP32;
@@ -584,17 +585,20 @@ hipError_t product_of(ProductParams p, hipStream_t s) {
     if (tiles(16, 32) >= 2 * kCus) return small_of<AT, BROWS, GROUP, OT, 1, 2, 8>(p, s);
     return small_of<AT, BROWS, GROUP, OT, 1, 1, 8>(p, s);
   }
-  const double part = static_cast<double>(tiles(32, 32)) / kCus;
-  const double small = (kExact ? 16 : 11) * (part > 1 ? part : 1), t64 = (kExact ? 36 : 20) * rounds(64, 128);
-  const double t128 = (kExact ? 60 : 28) * rounds(128, 128);
-  const double t256 = kExact ? 86 * rounds(256, 128) : 62 * rounds(256, 256);
+  const auto shared = [&](int64_t tiles_, double by) { return tiles_ > kCus / by ? by * tiles_ / kCus : 1.0; };
+  const double small = (kExact ? 16 : 11) * shared(tiles(32, 32), 1.0), t64 = (kExact ? 36 : 20) * rounds(64, 128);
+  const double t128 = kExact ? 58 * shared(tiles(128, 128), 0.7) : 28 * rounds(128, 128);
+  const double t256 = kExact ? t128 : 62 * rounds(256, 256);
   // (a tile's rows are reached by 32-bit offsets)
   const bool near = p.a_stride < (1 << 23) && p.b_stride < (1 << 23);
   if (!near || (small <= t64 && small <= t128 && small <= t256)) return small_of<AT, BROWS, GROUP, OT, 2, 2, 8>(p, s);
   if (t64 <= t128 && t64 <= t256) return tiled_of<AT, BROWS, GROUP, OT, 2, 4, 2, 2, 6>(p, s);
-  if (t128 <= t256) return tiled_of<AT, BROWS, GROUP, OT, 4, 2, 2, 4, 4>(p, s);
-  if constexpr (kExact) return tiled_of<AT, BROWS, GROUP, OT, 4, 2, 4, 4, 3>(p, s);  // (as bf16 fragments take more registers)
-  return tiled_of<AT, BROWS, GROUP, OT, 2, 4, 8, 4, 2>(p, s);
+  if constexpr (kExact) {
+    return tiled_of<AT, BROWS, GROUP, OT, 2, 2, 4, 4, 2>(p, s);
+  } else {
+    if (t128 <= t256) return tiled_of<AT, BROWS, GROUP, OT, 4, 2, 2, 4, 4>(p, s);
+    return tiled_of<AT, BROWS, GROUP, OT, 2, 4, 8, 4, 2>(p, s);
+  }
 }
 
 template <int AT, int OT>
