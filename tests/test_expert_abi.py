@@ -75,6 +75,10 @@ def test_constants_and_structs_match_the_header():
     for name, cls, size in (("ds_expert_plan", B.ds_expert_plan, 56), ("ds_block_operand", B.ds_block_operand, 32)):
         body = re.search(rf"typedef struct {name} \{{(.*?)\}}", text, re.S).group(1)
         assert re.findall(r"(\w+);", body) == [f for f, _ in cls._fields_] and ctypes.sizeof(cls) == size
+    # the binding's bytes are the structures'
+    p, o = _plan(), B.ds_block_operand(X, W, 128, ts.E5M2, 1)
+    assert B._pack_plan(P, O, F, 4, 32, 8, 64, 1, 0) == bytes(p)
+    assert B._pack_operand(X, W, 128, ts.E5M2, 1) == bytes(o)
 
 
 @pytest.mark.parametrize("align", [1, 16, 128, 100, 1024])

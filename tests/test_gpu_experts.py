@@ -438,6 +438,91 @@ def test_product(m, n, k, a, of_b, out):
     assert torch.equal(got, ts.ds_block_product(qa.cuda(), sa.cuda(), qb.cuda(), sb.cuda(), out_dtype=DT[out]))
 
 
+def _exact_on_device(va, vb):
+    """The definition in 64 bits for larger sizes: elementary products on the device."""
+    a, b = torch.from_numpy(va).cuda(), torch.from_numpy(vb).cuda()
+    return (a @ b.t()).cpu().numpy(), (a.abs() @ b.abs().t()).cpu().numpy()
+
+
+# Sizes at which every kernel is chosen (the tile is noted), with fewer blocks of the inner axis than are under
+# way at a time, as many, and more; with a rest and without; with rows and columns past the last tile.
+LARGER = [(500, 2000, 16), (500, 1999, 128), (450, 2000, 640), (511, 1990, 1040), (512, 2048, 768),  # 64 x 128
+          (1000, 4000, 144), (1023, 4001, 512), (1024, 4096, 1296),  # 128 x 128
+          (2000, 2048, 272), (2047, 2050, 128), (1999, 2048, 400),  # exact sums: 128 x 128
+          (4000, 4001, 144), (4096, 4096, 256), (4095, 4000, 416)]  # 256 x 256
+
+
+@pytest.mark.parametrize("m,n,k", LARGER)
+@pytest.mark.parametrize("a,of_b,out", [("e4m3", 128, "bf16"), ("e5m2", 1, "bf16"), ("e5m2", 128, "fp32"),
+                                        ("e4m3", 1, "fp32")])
+def test_larger_product(m, n, k, a, of_b, out):
+    say(f"larger product {m} x {n} x {k}, {a}, {of_b}, {out}")
+    qa, sa, va = _operand(m, m, k, a)
+    qb, sb, vb = _operand(n + 1, n, k, "e4m3", of_b)
+    want, size = _exact_on_device(va, vb)
+    base = torch.full((m + 2, n + 8), KEPT, dtype=DT[out], device="cuda")
+    got = ts.ds_block_product(_strided8(qa, 16), sa.cuda(), qb.cuda(), sb.cuda(), out=base[1:m + 1, 3:n + 3])
+    _close(got, want, _product_tol(k, size, want, out), "product")
+    got.fill_(KEPT)
+    assert (base == KEPT).all()  # nothing was written around it
+
+
+@pytest.mark.parametrize("m,n,k", [(500, 2000, 300), (1024, 4096, 300), (4096, 4096, 300)])
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+def test_larger_product_keeps_nan_in_its_rows(m, n, k, out):
+    say(f"larger product nan {m} x {n}, {out}")
+    k -= k % 16
+    qa, sa, _ = _operand(1, m, k, "e5m2")
+    qb, sb, _ = _operand(2, n, k, "e4m3", 128)
+    clean = ts.ds_block_product(qa.cuda(), sa.cuda(), qb.cuda(), sb.cuda(), out_dtype=DT[out])
+    assert clean.isfinite().all()
+    sa[5, 1] = float("nan")
+    qa.view(torch.uint8)[m - 1, k - 1] = 0x7C  # an infinity
+    qb.view(torch.uint8)[n - 3, 7] = 0x7F  # a NaN
+    got = ts.ds_block_product(qa.cuda(), sa.cuda(), qb.cuda(), sb.cuda(), out_dtype=DT[out])
+    assert got[5].isnan().all() and got[:, n - 3].isnan().all() and not got[m - 1].isfinite().any()
+    rest = torch.ones(m, n, dtype=torch.bool)
+    rest[5], rest[m - 1], rest[:, n - 3] = False, False, False
+    assert torch.equal(got.cpu()[rest], clean.cpu()[rest])
+
+
+@pytest.mark.parametrize("loads", [[700, 0, 130, 64, 1, 400], [300] * 20, [1] * 1000 + [0] * 24, [2000, 3, 0, 900]],
+                         ids=["few", "even", "many", "uneven"])
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+def test_larger_product_of_segments(loads, out):
+    n, k = (500, 272) if len(loads) > 100 else (2000, 400)
+    say(f"larger product of segments, {len(loads)}, {out}")
+    offsets = np.concatenate([[0], np.cumsum(loads)]).astype(np.int32)
+    m, G = int(offsets[-1]) + 3, len(loads)
+    qa, sa, va = _operand(m, m, k, "e4m3")
+    qb, sb, vb = _operand(7, G * n, k, "e4m3")
+    got = ts.ds_block_product(qa.cuda(), sa.cuda(), qb.cuda().view(G, n, k), sb.cuda().view(G, n, -1),
+                              offsets=torch.from_numpy(offsets).cuda(),
+                              out=torch.full((m, n), KEPT, dtype=DT[out], device="cuda"))
+    assert (got[m - 3:] == KEPT).all()
+    a, b = torch.from_numpy(va).cuda(), torch.from_numpy(vb).cuda().view(G, n, k)
+    for g in range(G):
+        lo, hi = int(offsets[g]), int(offsets[g + 1])
+        if hi > lo:
+            want, size = (a[lo:hi] @ b[g].t()).cpu().numpy(), (a[lo:hi].abs() @ b[g].abs().t()).cpu().numpy()
+            _close(got[lo:hi], want, _product_tol(k, size, want, out), f"segment {g}")
+
+
+@pytest.mark.parametrize("m,n", [(600, 1000), (2048, 1000)])
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+def test_larger_product_along_segments(m, n, out):
+    say(f"larger product along segments {m} x {n}, {out}")
+    ends, k = [0, 128, 128, 1024, 1152, 2560, 2704], 2704
+    qa, sa, va = _operand(m, m, k, "e5m2")
+    qb, sb, vb = _operand(n + 1, n, k, "e4m3")
+    got = ts.ds_block_product(qa.cuda(), sa.cuda(), qb.cuda(), sb.cuda(), inner=True, out_dtype=DT[out],
+                              offsets=torch.tensor(ends, dtype=torch.int32).cuda())
+    for g in range(len(ends) - 1):
+        lo, hi = ends[g], ends[g + 1]
+        want, size = _exact_on_device(np.ascontiguousarray(va[:, lo:hi]), np.ascontiguousarray(vb[:, lo:hi]))
+        _close(got[g], want, _product_tol(k, size, want, out), f"segment {g}")
+
+
 LOADS = [[5], [0, 3, 0], [16, 16, 16, 16], [1] * 40, [130, 0, 7, 64, 1], [0] * 70 + [9] + [0] * 70 + [33], [300, 520, 2],
          [70, 60, 50, 90], [1000, 40]]
 

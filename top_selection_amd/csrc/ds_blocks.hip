@@ -5,10 +5,11 @@
 namespace ds {
 namespace {
 
-// scale = max(|block|, 2^-100) / largest; q = x / scale. The quotient is the correctly rounded one by
-// Markstein's theorem: with inv the correctly rounded reciprocal and q0 = x inv, q0 + (x - q0 scale) inv in
-// two fused steps is x / scale rounded once, as long as the remainder is no subnormal: blocks below 2^-60 are
-// multiplied by 2^64 first (scale too), which is exact.
+// scale = max(|block|, 2^-100) / largest; q = x / scale. With inv the rounded reciprocal, q0 = x inv is within two
+// steps of the quotient, its remainder x - q0 scale comes from one fused step, and q0 + remainder inv, before its
+// one rounding, is off by less than 2^-45 of the quotient (P. Markstein, 1990), as long as the remainder is no
+// subnormal: blocks below 2^-60 are multiplied by 2^64 first (scale too), which is exact. A division takes three
+// times the instructions.
 template <int QT>
 struct Eight;
 template <>
