@@ -494,7 +494,7 @@ int ds_expert_capacity(int64_t rows, int k, int experts, int align, int64_t* cap
  * out_idx; entries outside [0, experts) are slots without an expert). An expert's slots keep their
  * order, so the result does not depend on timing. An expert may fill several slots of a row.
  *   idx        may not share memory with the plan's arrays, nor those with one another.
- *   workspace  ds_expert_sort_workspace_size bytes, 8-byte aligned, as in ds_softmax.
+ *   workspace  ds_expert_sort_workspace_size bytes, 16-byte aligned, as in ds_softmax.
  * rows == 0 writes offsets of 0 and an order of -1.
  */
 int ds_expert_sort(const int32_t* idx, const ds_expert_plan* plan, void* workspace, size_t ws_bytes, void* stream);

@@ -93,6 +93,16 @@ def test_sort(rows, k, experts, align, dropped, hot):
     assert np.array_equal(_np(plan.order), order)
 
 
+@pytest.mark.parametrize("rows,k,experts,align", [(400000, 8, 300, 128), (200000, 6, 1023, 1), (100, 64, 2, 16)])
+def test_sort_of_many_and_of_equal_slots(rows, k, experts, align):
+    """More slots than 256 chunks of 4096; an expert that fills most slots of every row."""
+    say(f"sort many {rows} x {k} of {experts}")
+    idx = _choices(rows, rows, k, experts, 0.05, hot=True)
+    plan = ts.ds_expert_sort(idx.cuda(), experts, align)
+    for got, want in zip(plan, orc.sort(idx.numpy(), experts, align, plan.order.numel())):
+        assert np.array_equal(_np(got), want)
+
+
 def test_sort_into_longer_arrays_and_a_dirty_workspace():
     say("sort into given arrays")
     idx = _choices(3, 20000, 4, 77).cuda()
@@ -261,6 +271,15 @@ def test_far_offsets():
     assert np.array_equal(_np(got.float())[:, :n], want_q) and np.array_equal(_np(s), want_s)
     b, sb = ts.ds_block_quantize(w.cuda())
     assert torch.equal(ts.ds_block_product(q, s, b, sb), ts.ds_block_product(b, sb, b, sb))
+    # (rows 2^24 bytes apart are past the tiles' 32-bit offsets)
+    step = 1 << 24
+    many = far.view(torch.uint8)[:299 * step + 144].view(torch.float8_e4m3fn).as_strided((300, 144), (step, 1))
+    w = torch.randn(300, n, generator=_gen(4)).cuda()
+    got, s = ts.ds_block_quantize(w, out=many)
+    b, sb = ts.ds_block_quantize(w)
+    assert torch.equal(got.view(torch.uint8), b.view(torch.uint8)) and torch.equal(s, sb)
+    assert torch.equal(ts.ds_block_product(many, s, many, s, out_dtype=torch.float32),
+                       ts.ds_block_product(b, sb, b, sb, out_dtype=torch.float32))
 
 
 def test_broken_plans_stay_in_bounds():
@@ -628,7 +647,65 @@ def test_product_gradients(a, b_of):
         assert abs(_np(db)[i] - slope) <= _product_tol(m, size, want, "fp32")[i] + 2.0 ** -30 * size[i]
 
 
+def test_product_into_rows_apart():
+    say("product into rows apart")
+    m, n, k, ends = 70, 90, 384, [0, 128, 384]
+    qa, sa, _ = _operand(1, m, k, "e4m3")
+    qb, sb, _ = _operand(2, n, k, "e4m3")
+    args = (qa.cuda(), sa.cuda(), qb.cuda(), sb.cuda(), torch.tensor(ends, dtype=torch.int32).cuda(), True)
+    base = torch.full((2, m, n + 6), KEPT, device="cuda")
+    got = ts.ds_block_product(*args, out=base[:, :, 3:n + 3])
+    assert torch.equal(got, ts.ds_block_product(*args, out_dtype=torch.float32))
+    got.fill_(KEPT)
+    assert (base == KEPT).all()
+
+
 # --------------------------------------------------------------------------------------- together
+def test_every_call_on_a_given_stream():
+    """Work that a stream still has to do before the calls on it: they see its result, not what was there before."""
+    say("given stream")
+    stream = torch.cuda.Stream()
+    E, rows, n = 8, 500, 512
+    idx = _choices(1, rows, 2, E, 0).cuda()
+    x, w = torch.randn(rows, n, generator=_gen(1)).cuda(), torch.rand(rows, 2, generator=_gen(2)).cuda()
+    wt = torch.randn(E, n, n, generator=_gen(3)).cuda() * n ** -0.5
+
+    def all_of(x, **kw):
+        plan = ts.ds_expert_sort(idx, E, 128, **kw)
+        cap = plan.order.numel()
+        rows_of = ts.ds_expert_gather(x, plan, out=torch.zeros(cap, n, device="cuda"), **kw)
+        q, s = ts.ds_block_quantize(x, plan=plan, out=torch.zeros(cap, n, device="cuda").to(torch.float8_e4m3fn),
+                                    out_scales=torch.zeros(cap, n // 128, device="cuda"), **kw)
+        b, t = ts.ds_block_quantize(wt, ts.BLOCK_TILE, **kw)
+        y = ts.ds_block_product(q, s, b, t, offsets=plan.offsets, out=torch.zeros(cap, n, device="cuda"), **kw)
+        out = ts.ds_expert_combine(y, plan, w, **kw)
+        gy, gw = ts.ds_expert_combine_grad(out, y, plan, w, out_y=torch.zeros(cap, n, device="cuda"), **kw)
+        return rows_of, q.view(torch.uint8), s, y, out, gy, gw
+
+    want = all_of(x)
+    torch.cuda.synchronize()
+    late = torch.zeros_like(x)
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(20_000_000)
+        late.copy_(x)
+        got = all_of(late)
+    with torch.cuda.stream(stream):
+        late.zero_()
+        torch.cuda._sleep(20_000_000)
+        late.copy_(x)
+    stream.wait_stream(torch.cuda.current_stream())
+    q2, s2 = ts.ds_block_quantize(late, stream=stream)
+    out2 = ts.ds_expert_combine(ts.ds_expert_gather(late, ts.ds_expert_sort(idx, E, 128, stream=stream), stream=stream),
+                                ts.ds_expert_sort(idx, E, 128, stream=stream), w, stream=stream)
+    stream.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    q, s = ts.ds_block_quantize(x)
+    assert torch.equal(q2.view(torch.uint8), q.view(torch.uint8)) and torch.equal(s2, s)
+    plan = ts.ds_expert_sort(idx, E, 128)
+    assert torch.equal(out2, ts.ds_expert_combine(ts.ds_expert_gather(x, plan), plan, w))
+
+
 def _layer(x, logits, w1, w2, k, align, g=None):
     """A layer of experts as a program runs it: route, sort, quantise to the experts, two products with a
     rectifier between, combine; with g also every gradient."""

@@ -29,13 +29,15 @@ struct SortParams {
   int64_t capacity;
   int64_t chunk;
   int32_t chunks;
-  int32_t* counts;  // [chunks][experts], the workspace (NULL for one chunk)
+  int32_t* counts;  // [chunks][counts_wide(experts)], the workspace (NULL for one chunk)
 };
 struct SortCut {
   int64_t chunk;
   int32_t chunks;
 };
 SortCut cut_sort(int64_t slots);
+// A chunk's counts, in whole vectors of four.
+__host__ __device__ constexpr int32_t counts_wide(int32_t experts) { return (experts + 3) / 4 * 4; }
 hipError_t launch_sort(const SortParams& p, hipStream_t s);
 
 // Gather, combine and its gradient: teams of lanes walk a row in vectors.

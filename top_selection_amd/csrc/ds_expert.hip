@@ -33,7 +33,9 @@ __global__ __launch_bounds__(1024) void sort_count_kernel(SortParams p) {
       if (e[i] >= 0) atomicAdd(&hist[e[i]], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < p.experts; e += 1024) p.counts[static_cast<int64_t>(blockIdx.x) * p.experts + e] = hist[e];
+  const int wide = counts_wide(p.experts);
+  for (int e = threadIdx.x; e < wide; e += 1024)
+    p.counts[static_cast<int64_t>(blockIdx.x) * wide + e] = e < p.experts ? hist[e] : 0;
 }
 
 // Places of a chunk's slots. Every workgroup adds up all chunks' counts for itself (they are few and in L2),
@@ -63,18 +65,27 @@ __global__ __launch_bounds__(WAVES * 64) void sort_place_kernel(SortParams p) {
       if (e[i] >= 0) atomicAdd(&mine[e[i]], 1);
   }
   if (p.chunks > 1) {
-    // threads that share an expert take every so many-th chunk
-    const int wide = E <= 64 ? 64 : 1 << (32 - __clz(E - 1)), every = T >= wide ? T / wide : 1;
-    for (int e = tid % wide; e < E; e += T >= wide ? wide : T) {
-      int all = 0, early = 0;
+    // a thread adds up four experts' counts of every so many-th chunk
+    const int quads = counts_wide(E) / 4, every = T / quads, from = tid / quads, e = (tid - from * quads) * 4;
+    int all[4] = {}, early[4] = {};
+    if (from < every) {
 #pragma unroll 8
-      for (int c = T >= wide ? tid / wide : 0; c < p.chunks; c += every) {
-        const int v = p.counts[static_cast<int64_t>(c) * E + e];
-        all += v;
-        early += c < static_cast<int>(blockIdx.x) ? v : 0;
+      for (int c = from; c < p.chunks; c += every) {
+        const int4 v = *reinterpret_cast<const int4*>(p.counts + static_cast<int64_t>(c) * quads * 4 + e);
+        const bool before_this = c < static_cast<int>(blockIdx.x);
+        const int q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          all[i] += q[i];
+          early[i] += before_this ? q[i] : 0;
+        }
       }
-      atomicAdd(&total[e], all);
-      atomicAdd(&before[e], early);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (e + i < E) {
+          atomicAdd(&total[e + i], all[i]);
+          atomicAdd(&before[e + i], early[i]);
+        }
     }
     __syncthreads();
   } else {

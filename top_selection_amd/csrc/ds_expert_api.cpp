@@ -70,7 +70,7 @@ ds::Plan plan_of(const ds_expert_plan& p) {
 }
 
 size_t sort_bytes(const ds::SortCut& c, int experts) {
-  return c.chunks > 1 ? static_cast<size_t>(c.chunks) * experts * sizeof(int32_t) : 0;
+  return c.chunks > 1 ? static_cast<size_t>(c.chunks) * ds::counts_wide(experts) * sizeof(int32_t) : 0;
 }
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -108,7 +108,7 @@ int ds_expert_sort(const int32_t* idx, const ds_expert_plan* plan, void* workspa
   const size_t need = sort_bytes(c, plan->experts);
   if (need > 0) {
     if (!workspace || ws_bytes < need) return DS_ERR_WORKSPACE;
-    if (misaligned(workspace, 8)) return DS_ERR_ALIGNMENT;
+    if (misaligned(workspace, 16)) return DS_ERR_ALIGNMENT;
   }
   if (clash({place_range(*plan), order_range(*plan), offsets_range(*plan), range(need ? workspace : nullptr, need)},
             {range(idx, slots * 4)}))
