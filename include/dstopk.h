@@ -547,8 +547,8 @@ int ds_expert_combine_grad(const void* g, int64_t g_stride, const void* y, int64
 
 /*
  * ds_block_quantize -- 8-bit floats with a scale for each block of 128:
- *   scale = max(|block|, 2^-100) / largest of q_dtype, in fp32;  q = x / scale, rounded to fp32 and
- *   then to the nearest 8-bit float, ties to even.
+ *   scale = max(|block|, 2^-100) / largest of q_dtype, in fp32;  q = x / scale, rounded once to the
+ *   nearest 8-bit float, ties to even.
  * A block that holds an infinity or a NaN has scale NaN and q of 0, so all that is computed from it is
  * NaN. Blocks start at multiples of 128; the last of a row may be shorter. With P the positions
  * (the plan's capacity, or rows without a plan) and ceil16 the next multiple of 16:

@@ -76,7 +76,7 @@ def quantize(x, rows, to):
                 continue
             most = np.float32(max(float(np.abs(part).max()), LEAST))
             scales[i, j] = most / np.float32(LARGEST[to])
-            q[at] = round8((part / scales[i, j]).astype(np.float64), to)
+            q[at] = round8(part.astype(np.float64) / np.float64(scales[i, j]), to)
     return q, scales
 
 

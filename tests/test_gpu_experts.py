@@ -408,6 +408,36 @@ def test_quantize_extremes(to, layout):
     assert np.array_equal(_np(q.float()), want)
 
 
+@pytest.mark.parametrize("to", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("layout", [0, 1, 2])
+@pytest.mark.parametrize("exponent", [0, -70, -110])
+def test_quantize_next_to_ties(to, layout, exponent):
+    """Quotients within a few 2^-24 of every tie of 8-bit floats, on either side: fp32 makes many of them the tie."""
+    say(f"quantize next to ties {to}, layout {layout}, 2^{exponent}")
+    every = torch.arange(256, dtype=torch.uint8).view(E8[to]).float()
+    every = every[every.isfinite()].sort()[0].double()
+    mid = (every[1:] + every[:-1]) / 2
+    x = torch.randn(128, 4 * 128, generator=_gen(exponent + 500)).double() * 2.0 ** exponent
+    for r in range(128 if layout == 0 else 1):
+        for b in range(4):
+            at = (slice(r, r + 1), slice(128 * b, 128 * b + 128)) if layout == 0 else (slice(None), slice(128 * b, 128 * b + 128))
+            for part in ([x[at]] if layout != 1 else [x[at][:, c:c + 1] for c in range(128)]):
+                most = part.abs().max().float()
+                scale = (most.clamp(min=2.0 ** -100) / orc.LARGEST[to]).double()
+                flat = part.reshape(-1)
+                n = flat.numel() - 1
+                t = mid[torch.randint(0, mid.numel(), (n,), generator=_gen(r * 4 + b))]
+                near = (t * scale).float()
+                near = near * (1 + 2.0 ** -23 * torch.randint(-1, 2, (n,), generator=_gen(r + b)))
+                new = torch.cat([most.double()[None], near.double()]).view(part.shape)
+                part.copy_(new)
+    x = x.float()
+    q, s = ts.ds_block_quantize(x.cuda(), layout, dtype=E8[to])
+    want, want_s = _quantized(x, layout, to)
+    assert np.array_equal(_np(s), want_s)
+    assert np.array_equal(_np(q.float()), want)
+
+
 def test_quantize_a_stack_of_weights():
     say("quantize a stack")
     for rows in (128, 100):

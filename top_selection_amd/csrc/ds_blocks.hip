@@ -5,11 +5,15 @@
 namespace ds {
 namespace {
 
-// scale = max(|block|, 2^-100) / largest; q = x / scale. With inv the rounded reciprocal, q0 = x inv is within two
-// steps of the quotient, its remainder x - q0 scale comes from one fused step, and q0 + remainder inv, before its
-// one rounding, is off by less than 2^-45 of the quotient (P. Markstein, 1990), as long as the remainder is no
-// subnormal: blocks below 2^-60 are multiplied by 2^64 first (scale too), which is exact. A division takes three
-// times the instructions.
+// scale = max(|block|, 2^-100) / largest; q = x / scale, rounded once. With inv the rounded reciprocal, q0 = x inv
+// is within two steps of the quotient, its remainder x - q0 scale comes from one fused step, and q0 + remainder inv,
+// before its rounding to fp32, is off by less than 2^-45 of the quotient (P. Markstein, 1990), as long as the
+// remainder is no subnormal: blocks below 2^-60 are multiplied by 2^64 first (scale too), which is exact. A
+// division takes three times the instructions.
+// Rounded to 8 bits from there, a quotient would be off where fp32 made it a tie of 8-bit floats (one bf16 element
+// in 1500, one of fp32 in 2^23), so its remainder decides between it and its odd neighbours first: five instructions
+// more an element (8192 x 4096 bf16 16.7 to 19.0 us; only where a lane's quotient ends in 16 zeros, by fours or
+// by sixteens, 20.8).
 template <int QT>
 struct Eight;
 template <>
@@ -44,16 +48,30 @@ __device__ __forceinline__ Scale scale_of(uint32_t most) {
   return {scale, scale * raise, 1.0f / (scale * raise), raise};
 }
 
-// Four elements. A block without a scale is 0 (its infinities and NaN are not converted).
+// x / scale from its rounding to fp32: it or the odd float next to it on the quotient's side, so that rounding that
+// to fewer bits rounds the quotient itself.
+__device__ __forceinline__ float settled(float q, float x, float by) {
+  const uint32_t even = __float_as_uint(q) & 0x7FFFFFFEu;
+  const float rest = __builtin_fmaf(-__uint_as_float(even), by, __builtin_fabsf(x));  // exact
+  int32_t side;  // of its sign, 0 of 0
+  asm("v_med3_i32 %0, %1, -1, 1" : "=v"(side) : "v"(rest));
+  return __builtin_copysignf(__uint_as_float(even + side), q);
+}
+
+// Sixteen elements. A block without a scale is 0 (its infinities and NaN are not converted).
 template <int QT, bool RAISE>
-__device__ __forceinline__ uint32_t quantize4(float a, float b, float c, float d, const Scale& s) {
-  const auto one = [&](float v) {
-    const float x = RAISE ? v * s.raise : v, q0 = x * s.inv;
-    return __builtin_fmaf(__builtin_fmaf(-q0, s.by, x), s.inv, q0);
+__device__ __forceinline__ uint4 quantize16_of(const float (&v)[16], const Scale& s) {
+  const auto one = [&](int i) {
+    const float x = RAISE ? v[i] * s.raise : v[i], q0 = x * s.inv;
+    return settled(__builtin_fmaf(__builtin_fmaf(-q0, s.by, x), s.inv, q0), x, s.by);
   };
-  const int lo = Eight<QT>::template pack<false>(one(a), one(b), 0);
-  const uint32_t q = static_cast<uint32_t>(Eight<QT>::template pack<true>(one(c), one(d), lo));
-  return s.inv == 0.0f ? 0u : q;
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int lo = Eight<QT>::template pack<false>(one(4 * i), one(4 * i + 1), 0);
+    w[i] = static_cast<uint32_t>(Eight<QT>::template pack<true>(one(4 * i + 2), one(4 * i + 3), lo));
+  }
+  return s.inv == 0.0f ? uint4{0, 0, 0, 0} : uint4{w[0], w[1], w[2], w[3]};
 }
 
 // Sixteen elements of a row from column c on, 0 past n.
@@ -83,11 +101,7 @@ __device__ __forceinline__ uint32_t most16(const float (&v)[16]) {
 
 template <int QT>
 __device__ __forceinline__ uint4 quantize16(const float (&v)[16], const Scale& s) {
-  if (__any(s.raise != 1.0f))
-    return {quantize4<QT, true>(v[0], v[1], v[2], v[3], s), quantize4<QT, true>(v[4], v[5], v[6], v[7], s),
-            quantize4<QT, true>(v[8], v[9], v[10], v[11], s), quantize4<QT, true>(v[12], v[13], v[14], v[15], s)};
-  return {quantize4<QT, false>(v[0], v[1], v[2], v[3], s), quantize4<QT, false>(v[4], v[5], v[6], v[7], s),
-          quantize4<QT, false>(v[8], v[9], v[10], v[11], s), quantize4<QT, false>(v[12], v[13], v[14], v[15], s)};
+  return __any(s.raise != 1.0f) ? quantize16_of<QT, true>(v, s) : quantize16_of<QT, false>(v, s);
 }
 
 __device__ __forceinline__ int64_t plan_end(const Plan& q) {
@@ -153,8 +167,8 @@ __global__ __launch_bounds__(256) void quantize_row_kernel(QuantizeParams p) {
 // once: first the rows' numbers, then the rows), and a thread takes 32 elements of one (fp32) or two (bf16)
 // columns, four or eight lanes a column, whose 16-byte stores make whole lines. The rows' distance in LDS makes the
 // reads down the columns meet every bank once. A position's row is quantised anew for every expert, since the
-// blocks run over positions: 28000 positions of 2001 fp32 columns 36 us, bound by vector instructions (about five
-// an element; 43 k of 69 k cycles a SIMD), memory would take 20.
+// blocks run over positions: 28000 positions of 2001 fp32 columns 38.5 us, bound by vector instructions (about ten
+// an element), memory would take 20.
 template <int DT, int QT>
 __global__ __launch_bounds__(256, 4) void quantize_column_kernel(QuantizeParams p) {
   using T = typename Elem<DT>::T;

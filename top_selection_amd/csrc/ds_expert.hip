@@ -11,8 +11,9 @@ namespace {
 // waves of the chunk + in earlier lanes. A wave takes its slots in order, 64 at a time; lanes
 // with equal experts find one another by ballots over the experts' bits, so no atomic decides a place.
 // Up to 8192 slots one workgroup does it all (4 x 8 of 256 experts: 4.8 us, a chain of a dozen dependent LDS and
-// memory accesses); above, a launch counts and one places (65536 x 8: 2.8 and 11 us, for 8 MB that take 2: the
-// scattered 4-byte stores and the chain again).
+// memory accesses); above, a launch counts and one places (65536 x 8: 2.9 and 11.8 us, for 8 MB that take 2: the
+// chain again. Neither the scattered 4-byte stores nor the sums over all chunks' counts show: with both confined to
+// a few KB the time stays; chunks of half the size take as long with 16 waves and 1.5 us longer with eight).
 
 __device__ __forceinline__ int expert_of(const SortParams& p, int64_t slot, int64_t end) {
   const int e = slot < end ? p.idx[slot] : -1;
