@@ -278,10 +278,11 @@ struct Stage {
 // (32 cycles of the unit), so that a wave of 128 x 64 has 128 registers of sums and one SIMD two such waves.
 // Measured: 8192 x 8192 x 8192 runs at 2.2 PFLOP/s, 64 segments of 1024 +- 300 rows x 4096 x 4096 at 1.77 of live rows
 // (1.25 ms; a tenth of the tiles' rows are past their segment). With random operands in registers the unit alone reaches
-// 4.0 and with the multiply-adds 3.4 (with zeros 5.0 and 4.2). Bound by the steps between a block's waits: 3500 to
-// 3700 cycles for the unit's 2048, at the 2.0 GHz that random operands leave of 2.4; a block's start, end and search for
-// its rows are a tenth. Loads of a block sent further ahead or spread over its products, tile after tile in one
-// workgroup, other orders of tiles, priorities and 32 x 32 fragments all left it there or made it slower.
+// 4.0 and with the multiply-adds 3.4 (with zeros 5.0 and 4.2). A block takes 3500 to
+// 3700 cycles for the unit's 2048 (2600 without its loads, 3200 with all of them from L2), at the 2.1 GHz that random
+// operands leave of 2.4; a tile's start, end and search for its rows are an eighth. Loads of a block sent further ahead
+// or spread over its products, four blocks' scales held in registers, tile after tile in one workgroup, other
+// orders of tiles, priorities and 32 x 32 fragments all left it there or made it slower.
 // For exact sums the unit takes bf16, of which registers alone allow 1.8 PFLOP/s, and 1.5 with the widening (as many
 // vector instructions as the scaling): 8192 x 8192 x 8192 runs at 1.0, and 16 segments of 2048 +- 500 x 4096 x
 // 2048, whose results are 537 MB more, take 675 us, 0.81 PFLOP/s.
