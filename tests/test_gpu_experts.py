@@ -535,8 +535,9 @@ def test_larger_product_keeps_nan_in_its_rows(m, n, k, out):
     assert torch.equal(got.cpu()[rest], clean.cpu()[rest])
 
 
-@pytest.mark.parametrize("loads", [[700, 0, 130, 64, 1, 400], [300] * 20, [1] * 1000 + [0] * 24, [2000, 3, 0, 900]],
-                         ids=["few", "even", "many", "uneven"])
+@pytest.mark.parametrize("loads", [[700, 0, 130, 64, 1, 400], [300] * 20, [1] * 1000 + [0] * 24, [2000, 3, 0, 900],
+                                   [100, 3, 128, 0, 77] * 13, [40, 33] * 4],
+                         ids=["few", "even", "many", "uneven", "short", "eight"])
 @pytest.mark.parametrize("out", ["bf16", "fp32"])
 def test_larger_product_of_segments(loads, out):
     n, k = (500, 272) if len(loads) > 100 else (2000, 400)

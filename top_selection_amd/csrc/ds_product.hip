@@ -584,10 +584,12 @@ hipError_t tiled_of(ProductParams& p, hipStream_t s) {
 
 // Which kernel. Up to 16 rows (a segment, on average) b's bytes are all that counts: narrow workgroups, the
 // narrower where there are few. Above, the one whose rounds of tiles take least. A round's time hardly depends on
-// how full it is (us for 32 blocks of the inner axis, measured: tiles of 32 x 32 11, through LDS 64 x 128 20, 128 x 128
-// 28, 256 x 256 62; with exact sums 16, 36 and 58); where tiles share a CU (the smallest; the largest of exact
-// sums, two of which hide each other's starts and ends: 665 us for a weights' gradient that 256 x 128 alone
-// took 740 for) parts of rounds count.
+// how full it is; it is a tile's start and end and its blocks of the inner axis (us measured, bf16 | fp32: tiles of
+// 32 x 32 1 + 0.3 a block | 1.5 + 0.45, through LDS 64 x 128 3.5 + 0.5 | 4 + 1, 128 x 128 5.6 + 0.7 | 9 + 1.5, 256 x 256
+// 11 + 1.6), and 2 where a segment has to be found (64 x 128: 4). Waves whose rows are all past their segment only
+// load (64 segments of 100 rows x 2048 x 512: 26 us by 256 x 256, 37 by 128 x 128; of 64 rows x 4096 160 and 149).
+// Where tiles share a CU (the smallest; the largest of exact sums, two of which hide each other's starts and ends: 665
+// us for a weights' gradient that 256 x 128 alone took 740 for) parts of rounds count.
 template <int AT, int BROWS, int GROUP, int OT>
 hipError_t product_of(ProductParams p, hipStream_t s) {
   constexpr bool kExact = OT == DS_FP32;
@@ -600,9 +602,14 @@ hipError_t product_of(ProductParams p, hipStream_t s) {
     return small_of<AT, BROWS, GROUP, OT, 1, 1, 8>(p, s);
   }
   const auto shared = [&](int64_t tiles_, double by) { return tiles_ > kCus / by ? by * tiles_ / kCus : 1.0; };
-  const double small = (kExact ? 16 : 11) * shared(tiles(32, 32), 1.0), t64 = (kExact ? 36 : 20) * rounds(64, 128);
-  const double t128 = kExact ? 58 * shared(tiles(128, 128), 0.7) : 28 * rounds(128, 128);
-  const double t256 = kExact ? t128 : 62 * rounds(256, 256);
+  const double blocks = static_cast<double>(p.blocks) / (GROUP == DS_GROUP_INNER ? segments : 1);
+  const double find = GROUP == DS_GROUP_ROWS ? 2 : 0;
+  const auto round = [&](double ends, double block) { return find + ends + block * blocks; };
+  const double small = (kExact ? round(1.5, 0.45) : round(1, 0.3)) * shared(tiles(32, 32), 1.0);
+  const double t64 = (find + (kExact ? round(4, 1) : round(3.5, 0.5))) * rounds(64, 128);
+  const double t128 =
+      kExact ? round(9, 1.5) * shared(tiles(128, 128), 0.7) : round(5.6, 0.7) * rounds(128, 128);
+  const double t256 = kExact ? t128 : (rows <= 128 ? round(8, 1.3) : round(11, 1.6)) * rounds(256, 256);
   // (a tile's rows are reached by 32-bit offsets)
   const bool near = p.a_stride < (1 << 23) && p.b_stride < (1 << 23);
   if (!near || (small <= t64 && small <= t128 && small <= t256)) return small_of<AT, BROWS, GROUP, OT, 2, 2, 8>(p, s);
