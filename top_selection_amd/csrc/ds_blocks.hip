@@ -206,7 +206,10 @@ __global__ __launch_bounds__(256, 4) void quantize_column_kernel(QuantizeParams 
   typename Vt::type d[kEach];
 #pragma unroll
   for (int i = 0; i < kEach; ++i) from[i] = rows[tr + i * kRows];
-  if (c0 + kCols <= p.n) {
+  if (p.rows == 0) {  // a plan of no rows whose offsets are broken: all is padding, and there is no first row
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) d[i] = typename Vt::type{};
+  } else if (c0 + kCols <= p.n) {
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
       d[i] = *reinterpret_cast<const typename Vt::unaligned*>(x + (from[i] < 0 ? 0 : from[i]) + c0 + tc);
