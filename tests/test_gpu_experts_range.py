@@ -37,3 +37,24 @@ def test_columns_of_a_plan_without_rows(dtype, n, end):
     assert (_np(q.float())[:, :end] == 0).all() and (_np(q.float())[:, end:] == 2).all()
     least = np.float32(orc.LEAST) / np.float32(orc.LARGEST["e4m3"])
     assert (_np(s)[:, :end // 128] == least).all() and (_np(s)[:, end // 128:] == KEPT).all()
+
+
+@pytest.mark.parametrize("padding", [100, 5])
+def test_sort_next_to_the_largest_position(padding):
+    """As many slots of one expert as 2^31 - 2 positions hold: neither the padded count nor the walk through the padding
+    may pass 2^31 - 1 on the way."""
+    rows, align = 2 ** 31 - 2 - padding, 126
+    say(f"sort of {rows} slots")
+    cap = ts.ds_expert_capacity(rows, 1, 1, align)
+    assert cap == 2 ** 31 - 2
+    idx = torch.zeros(rows, 1, dtype=torch.int32, device="cuda")
+    plan = ts.ds_expert_sort(idx, 1, align)
+    del idx
+    assert _np(plan.offsets).tolist() == [0, cap]
+    assert (plan.order[rows:] == -1).all()
+    for lo in range(0, rows, 2 ** 28):
+        hi = min(rows, lo + 2 ** 28)
+        want = torch.arange(lo, hi, dtype=torch.int32, device="cuda")
+        assert torch.equal(plan.place[lo:hi, 0], want) and torch.equal(plan.order[lo:hi], want)
+    del plan, want
+    torch.cuda.empty_cache()

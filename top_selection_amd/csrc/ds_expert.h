@@ -38,6 +38,12 @@ struct SortCut {
 SortCut cut_sort(int64_t slots);
 // A chunk's counts, in whole vectors of four.
 __host__ __device__ constexpr int32_t counts_wide(int32_t experts) { return (experts + 3) / 4 * 4; }
+// n slots in whole runs of `align`. The result is a position, below 2^31; n + align - 1 may not be.
+__host__ __device__ constexpr int32_t padded(int32_t n, int32_t align) {
+  return static_cast<int32_t>((static_cast<uint32_t>(n) + static_cast<uint32_t>(align - 1)) / static_cast<uint32_t>(align) *
+                              static_cast<uint32_t>(align));
+}
+static_assert(padded(0, 126) == 0 && padded(1, 126) == 126 && padded(2147483546, 126) == 2147483646, "");
 hipError_t launch_sort(const SortParams& p, hipStream_t s);
 
 // Gather, combine and its gradient: teams of lanes walk a row in vectors.

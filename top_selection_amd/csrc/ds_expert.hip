@@ -105,9 +105,9 @@ __global__ __launch_bounds__(WAVES * 64) void sort_place_kernel(SortParams p) {
 
   // offsets: an exclusive sum of the padded counts, a run of experts a thread
   const int per = (E + T - 1) / T, e0 = tid * per, e1 = e0 + per < E ? e0 + per : E;
-  const auto padded = [&](int n) { return p.align == 1 ? n : (n + p.align - 1) / p.align * p.align; };
+  const auto room = [&](int n) { return p.align == 1 ? n : padded(n, p.align); };
   int run = 0;
-  for (int e = e0; e < e1; ++e) run += padded(total[e]);
+  for (int e = e0; e < e1; ++e) run += room(total[e]);
   int incl = run;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -121,7 +121,7 @@ __global__ __launch_bounds__(WAVES * 64) void sort_place_kernel(SortParams p) {
   for (int w = 0; w < WAVES; ++w) at += w < wave ? wave_sums[w] : 0;
   for (int e = e0; e < e1; ++e) {
     start[e] = at;
-    at += padded(total[e]);
+    at += room(total[e]);
     if (e == E - 1) start[E] = at;
   }
   __syncthreads();
@@ -170,8 +170,8 @@ __global__ __launch_bounds__(WAVES * 64) void sort_place_kernel(SortParams p) {
       const int from = e < E ? start[e] + total[e] : 0, to = e < E ? start[e + 1] : 0;
       for (uint64_t left = __ballot(from < to); left; left &= left - 1) {
         const int l = __ffsll(static_cast<unsigned long long>(left)) - 1;
-        const int end = __builtin_amdgcn_readlane(to, l);
-        for (int i = __builtin_amdgcn_readlane(from, l) + lane; i < end; i += 64) p.order[i] = -1;
+        const int64_t end = __builtin_amdgcn_readlane(to, l), begin = __builtin_amdgcn_readlane(from, l);
+        for (int64_t i = begin + lane; i < end; i += 64) p.order[i] = -1;
       }
     }
   }
