@@ -1,4 +1,6 @@
 // Products of 8-bit operands with a scale for each block of 128 along the inner axis.
+#include <stddef.h>
+
 #include <type_traits>
 
 #include "ds_expert.h"
@@ -271,8 +273,9 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"i"(LEFT) : "memory");
 }
 
+// A block of a tile in LDS. Its rows are written and read by sixteen bytes.
 template <int TM, int TN, int BROWS>
-struct Stage {
+struct alignas(16) Stage {
   float sa[TM];
   float sb[BROWS == 1 ? TN : 64];
   uint8_t a[TM][128];
@@ -300,6 +303,8 @@ struct Tiled {
   static constexpr int kLoadsA = TM / 8 / kWaves, kLoadsB = TN / 8 / kWaves;  // of eight rows, a wave
   using S = Stage<TM, TN, BROWS>;
   static constexpr uint32_t kStage = sizeof(S);
+  static_assert(alignof(S) == 16 && sizeof(S) % 16 == 0 && offsetof(S, a) % 16 == 0 && offsetof(S, b) % 16 == 0 &&
+                offsetof(S, sb) % 16 == 0, "sixteen bytes at a time");
 
   // A block's rows to LDS: a wave's load is eight rows, its lane l a part of row l / 8.
   // Rows past the last repeat it (they are not stored).
