@@ -5,6 +5,7 @@ import re
 import pytest
 
 import top_selection_amd as ts
+from test_expert_abi import _product
 
 CSRC = os.path.join(os.path.dirname(ts.__file__), "csrc")
 SOURCES = sorted(f for f in os.listdir(CSRC) if f.endswith((".hip", ".h")))
@@ -29,3 +30,14 @@ def test_registers_that_assembly_writes_are_declared(name):
 def test_the_reader_of_assembly_finds_the_loads():
     found = [t for t, _ in _asm(open(os.path.join(CSRC, "ds_product.hip")).read()) if "m0" in t]
     assert len(found) == 2
+
+
+def test_exact_sums_are_asked_for_with_the_result_type():
+    text = open(ts._binding.HEADER_PATH).read()
+    assert int(re.search(r"#define DS_EXACT_SUMS (\d+)", text).group(1)) == ts.DS_EXACT_SUMS
+    for otype in (ts.E4M3 | ts.DS_EXACT_SUMS, ts.DS_EXACT_SUMS << 1, -1):
+        assert _product(otype=otype) == ts.DS_ERR_INVALID_ARG
+    for otype in (ts.BF16, ts.FP32):  # the flag is no other type: its alignment is asked for
+        assert _product(otype=otype | ts.DS_EXACT_SUMS, out=(8 << 40) + 1) == ts.DS_ERR_ALIGNMENT
+    assert _product(otype=ts.FP32 | ts.DS_EXACT_SUMS, out=(8 << 40) + 2) == ts.DS_ERR_ALIGNMENT
+    assert _product(otype=ts.BF16 | ts.DS_EXACT_SUMS, m=0, a=None, out=None) == 0

@@ -58,3 +58,78 @@ def test_sort_next_to_the_largest_position(padding):
         assert torch.equal(plan.place[lo:hi, 0], want) and torch.equal(plan.order[lo:hi], want)
     del plan, want
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------------------------ exact sums
+def _small_beside_large(seed, rows, k, sign):
+    """Runs of eight along k: two of 256 (the second with `sign`) and six small whole numbers."""
+    v = torch.randint(-3, 4, (rows, k), generator=torch.Generator().manual_seed(seed)).float()
+    v[:, 0::8], v[:, 1::8] = 256, 256 * sign
+    return v
+
+
+def _ones(q):
+    return torch.ones(q.shape[0], -(-q.shape[1] // 128))
+
+
+# one size for each kernel that exact sums choose: 16 x 16, 16 x 32, 32 x 32, 64 x 128, 128 x 128
+EXACT = [(4, 300, 1296), (16, 16400, 272), (100, 333, 528), (500, 2000, 640), (511, 1990, 1040), (2000, 2048, 272),
+         (4095, 4000, 144)]
+
+
+@pytest.mark.parametrize("m,n,k", EXACT)
+@pytest.mark.parametrize("a", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("of_b", [1, 128])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_exact_sums_keep_what_is_small(m, n, k, a, of_b, out):
+    """In every eight products two of 2^16 cancel beside small whole numbers: all partial sums are whole and below
+    2^24, so fp32 sums are exact in any order, and the result is the whole number, rounded once. (A sum that cuts
+    below 2^-13 of the largest product loses what is below 8.)"""
+    say(f"exact sums {m} x {n} x {k}, {a}, {of_b}, {out}")
+    va, vb = _small_beside_large(1, m, k, 1), _small_beside_large(2, n, k, -1)
+    want = (va.cuda() @ vb.cuda().t()).double()  # (whole numbers below 2^24: exact)
+    qa, qb = va.to(E8[a]).cuda(), vb.to(E8["e4m3"]).cuda()
+    sb = _ones(qb)[::of_b].contiguous().cuda()
+    got = ts.ds_block_product(qa, _ones(qa).cuda(), qb, sb, out_dtype=out, exact=True)
+    assert got.dtype == out and torch.equal(got, want.to(out))
+
+
+@pytest.mark.parametrize("loads", [[4] * 6, [700, 0, 130, 64, 1, 400], [300] * 20, [2000, 3, 0, 900]],
+                         ids=["few", "uneven", "even", "large"])
+@pytest.mark.parametrize("of_b", [1, 128])
+def test_exact_sums_of_segments(loads, of_b):
+    n, k, G = 1000, 400, len(loads)
+    say(f"exact sums of segments {loads[:4]}, {of_b}")
+    offsets = np.concatenate([[0], np.cumsum(loads)]).astype(np.int32)
+    va = _small_beside_large(3, int(offsets[-1]), k, 1)
+    vb = _small_beside_large(4, G * n, k, -1).view(G, n, k)
+    qa, qb = va.to(E8["e4m3"]).cuda(), vb.to(E8["e4m3"]).cuda()
+    sb = torch.ones(G, -(-n // of_b), -(-k // 128), device="cuda")
+    got = ts.ds_block_product(qa, _ones(qa).cuda(), qb, sb, offsets=torch.from_numpy(offsets).cuda(), exact=True)
+    for g in range(G):
+        lo, hi = int(offsets[g]), int(offsets[g + 1])
+        assert torch.equal(got[lo:hi], (va[lo:hi].cuda() @ vb[g].cuda().t()).bfloat16()), g
+
+
+def test_exact_sums_along_segments():
+    say("exact sums along segments")
+    m, n, k, ends = 700, 900, 1040, [0, 256, 256, 1040]
+    va, vb = _small_beside_large(5, m, k, 1), _small_beside_large(6, n, k, -1)
+    qa, qb = va.to(E8["e5m2"]).cuda(), vb.to(E8["e4m3"]).cuda()
+    got = ts.ds_block_product(qa, _ones(qa).cuda(), qb, _ones(qb).cuda(), inner=True, exact=True,
+                              offsets=torch.tensor(ends, dtype=torch.int32, device="cuda"))
+    for g in range(3):
+        want = va[:, ends[g]:ends[g + 1]].cuda() @ vb[:, ends[g]:ends[g + 1]].cuda().t()
+        assert torch.equal(got[g], want.bfloat16()), g
+
+
+def test_exact_sums_of_a_row_do_not_depend_on_its_batch():
+    """The first rows alone and among many: with exact sums (of whole numbers) the same bits."""
+    say("exact sums and batches")
+    n, k = 2048, 1024
+    va, vb = _small_beside_large(7, 2048, k, 1), _small_beside_large(8, n, k, -1)
+    qa, qb = va.to(E8["e4m3"]).cuda(), vb.to(E8["e4m3"]).cuda()
+    sa, sb = _ones(qa).cuda(), _ones(qb).cuda()
+    all_of = ts.ds_block_product(qa, sa, qb, sb, exact=True)
+    for m in (1, 16, 40, 256, 1000):
+        assert torch.equal(ts.ds_block_product(qa[:m], sa[:m], qb, sb, exact=True), all_of[:m]), m

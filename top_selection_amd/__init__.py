@@ -13,5 +13,5 @@ from ._binding import (BF16, DS_ERR_ALIGNMENT, DS_ERR_DEVICE, DS_ERR_INVALID_ARG
                        ds_topk_merge, ds_topk_noalloc, ds_topk_plan, ds_topk_slices, ds_topk_workspace_size, dtype_code, ds_route, ds_route_grad, ds_softmax,
                        ds_softmax_workspace_size, ds_topk_softmax, ds_verify, ds_verify_workspace_size, header_functions, lib, stats_buffer,
                        E4M3, E5M2, DS_BLOCK, DS_MAX_EXPERT_ALIGN, BLOCK_ROW, BLOCK_COLUMN, BLOCK_TILE, GROUP_NONE, GROUP_ROWS,
-                       GROUP_INNER, ExpertPlan, ds_expert_capacity, ds_expert_sort, ds_expert_sort_workspace_size,
+                       GROUP_INNER, DS_EXACT_SUMS, ExpertPlan, ds_expert_capacity, ds_expert_sort, ds_expert_sort_workspace_size,
                        ds_expert_gather, ds_expert_combine, ds_expert_combine_grad, ds_block_quantize, ds_block_product)

@@ -43,6 +43,7 @@ DS_BLOCK = 128
 DS_MAX_EXPERT_ALIGN = 1024
 BLOCK_ROW, BLOCK_COLUMN, BLOCK_TILE = 0, 1, 2
 GROUP_NONE, GROUP_ROWS, GROUP_INNER = 0, 1, 2
+DS_EXACT_SUMS = 256
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # DS_LIBRARY names another build of the library (e.g. one with host-side sanitizers)
@@ -838,7 +839,7 @@ def _quantize_stack(x, layout, dtype, plan, out, out_scales, stream):
 
 
 def ds_block_product(a, a_scales, b, b_scales, offsets=None, inner: bool = False, out=None, out_dtype=None,
-                     stream=None):
+                     stream=None, exact: bool = False):
     """a b^T of 8-bit operands with a scale for each 128 along the inner axis (ds_block_quantize's);
     bf16 (or out_dtype / out's type: bf16 or fp32). a [m, k] with scales [m, ceil(k / 128)].
       offsets None   b [n, k]; [m, n].
@@ -847,7 +848,10 @@ def ds_block_product(a, a_scales, b, b_scales, offsets=None, inner: bool = False
       inner=True     offsets are segments of the inner axis, at multiples of 128; b [n, k] with scales
                      [n, ceil(k / 128)]; [groups, m, n].
     b is e4m3, with scales [.., n, ceil(k / 128)] or, in tiles, [.., ceil(n / 128), ceil(k / 128)]; a is e4m3
-    or e5m2. k is a multiple of 16. The gradients are products of the same kind (include/dstopk.h)."""
+    or e5m2. k is a multiple of 16. The gradients are products of the same kind (include/dstopk.h).
+    exact=True: bf16 results of exact products and fp32 sums, as fp32 results always are; without it large calls
+    leave the sums of blocks to the 8-bit matrix unit (up to twice the rate, errors a hundredth of bf16's rounding), so
+    that a row's bits may depend on the number of rows."""
     torch = _torch()
     m, k, a_stride = _matrix(a, "a")
     a_type, dev = _code8(a.dtype), a.device
@@ -886,7 +890,7 @@ def ds_block_product(a, a_scales, b, b_scales, offsets=None, inner: bool = False
                          a_type, 1)
     of_b = _pack_operand(b.data_ptr(), sp, b_stride, b_type, scale_rows)
     _call("ds_block_product", dev, stream, of_a, of_b, m, n, k, group, groups, op,
-          out.data_ptr(), stride, _code(out.dtype))
+          out.data_ptr(), stride, _code(out.dtype) | (DS_EXACT_SUMS if exact else 0))
     return out
 
 

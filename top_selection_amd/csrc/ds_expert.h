@@ -104,6 +104,6 @@ struct ProductParams {
   int64_t unit0;
   int64_t units;
 };
-hipError_t launch_product(int a_dtype, int b_scale_rows, int group, int out_dtype, ProductParams p, hipStream_t s);
+hipError_t launch_product(int a_dtype, int b_scale_rows, int group, int out_dtype, bool exact, ProductParams p, hipStream_t s);
 
 }  // namespace ds

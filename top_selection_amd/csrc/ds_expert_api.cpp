@@ -259,6 +259,8 @@ int ds_block_quantize(const void* x, int64_t rows, int64_t n, int64_t row_stride
 
 int ds_block_product(const ds_block_operand* a, const ds_block_operand* b, int64_t m, int64_t n, int64_t k, int group,
                      int groups, const int32_t* offsets, void* out, int64_t out_stride, int out_dtype, void* stream) {
+  const bool exact = (out_dtype & DS_EXACT_SUMS) != 0;
+  out_dtype &= ~DS_EXACT_SUMS;
   if (!a || !b || !known8(a->dtype) || !known8(b->dtype) || !known(out_dtype)) return DS_ERR_INVALID_ARG;
   if (group != DS_GROUP_NONE && group != DS_GROUP_ROWS && group != DS_GROUP_INNER) return DS_ERR_INVALID_ARG;
   if (groups < 1 || (group == DS_GROUP_NONE && (groups != 1 || offsets)) || (group != DS_GROUP_NONE && !offsets))
@@ -300,7 +302,8 @@ int ds_block_product(const ds_block_operand* a, const ds_block_operand* b, int64
   p.offsets = offsets;
   p.out = out;
   p.out_stride = out_stride;
-  return status(ds::launch_product(a->dtype, b->scale_rows, group, out_dtype, p, static_cast<hipStream_t>(stream)));
+  return status(
+      ds::launch_product(a->dtype, b->scale_rows, group, out_dtype, exact, p, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

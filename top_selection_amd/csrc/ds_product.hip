@@ -36,9 +36,11 @@ __device__ __forceinline__ v8h widen8(int lo, int hi) {
 
 // One block of 128 of sixteen rows of each side: lane l gives 32 of row l % 16's bytes, the same ones on
 // both sides (the sum's order is the hardware's), and gets elements (b row 4 (l / 16) + i, a row l % 16).
-// As bf16 the products are exact and the sums fp32: the 8-bit unit itself adds eight products at a time
-// aligned to the largest of them, and cuts what is below 2^-13 of it (measured: 1.5e-5 to 7e-5 of the
-// result for normal data, where this way is exact to fp32's rounding).
+// As bf16 the products are exact and the sums fp32. The 8-bit unit itself adds eight products at a time, aligned to the
+// largest of them, and cuts what is below 2^-13 of it towards zero. Measured against 64 bits (1024 x 1024 results, k of 128
+// to 16384 alike), the root mean square of that error over the results' is 1.4e-5 for normal data and 3.0e-5 and 5.3e-5
+// where magnitudes spread over 2^3 and 2^6; where all products have one sign the results are short by 2.4e-6, 1.1e-5 and
+// 4.5e-5. A result's rounding to bf16 is 1.7e-3 on that measure.
 struct Wide {
   v8h p[4];
 };
@@ -293,13 +295,13 @@ struct alignas(16) Stage {
 // operands leave of 2.4; a tile's start, end and search for its rows are an eighth. Loads of a block sent further ahead
 // or spread over its products, four blocks' scales held in registers, tile after tile in one workgroup, other
 // orders of tiles, priorities and 32 x 32 fragments all left it there or made it slower.
-// For exact sums the unit takes bf16, of which registers alone allow 1.8 PFLOP/s, and 1.5 with the widening (as many
-// vector instructions as the scaling): 8192 x 8192 x 8192 runs at 1.0, and 16 segments of 2048 +- 500 x 4096 x
-// 2048, whose results are 537 MB more, take 675 us, 0.81 PFLOP/s.
-template <int AT, int BROWS, int GROUP, int OT, int WM, int WN, int MF, int NF, int STAGES>
+// For exact sums (EXACT: fp32 results, and bf16 ones that ask for them) the unit takes bf16, of which registers alone
+// allow 1.8 PFLOP/s, and 1.5 with the widening (as many vector instructions as the scaling): 8192 x 8192 x 8192 takes 950 us
+// (bf16 results 920, where the 8-bit unit takes 500), the segments above 2.08 ms for 1.24, and 16 segments of 2048 +- 500
+// x 4096 x 2048, whose results are 537 MB more, 665 us, 0.82 PFLOP/s.
+template <int AT, int BROWS, int GROUP, int OT, bool EXACT, int WM, int WN, int MF, int NF, int STAGES>
 struct Tiled {
   static constexpr int kWaves = WM * WN, kThreads = kWaves * 64, TM = WM * MF * 16, TN = WN * NF * 16;
-  static constexpr bool kExact = OT == DS_FP32;
   static constexpr int kLoadsA = TM / 8 / kWaves, kLoadsB = TN / 8 / kWaves;  // of eight rows, a wave
   using S = Stage<TM, TN, BROWS>;
   static constexpr uint32_t kStage = sizeof(S);
@@ -413,8 +415,8 @@ struct Tiled {
   // replace this one's as their last products are issued.
   template <class F>
   static __device__ __forceinline__ void compute(Places& at, float sb, State& h, float (&acc)[MF][NF][4], F&& turn) {
-    Operand<DS_E4M3, kExact> b[NF];
-    Operand<AT, kExact> a;
+    Operand<DS_E4M3, EXACT> b[NF];
+    Operand<AT, EXACT> a;
 #pragma unroll
     for (int e = 0; e < MF; ++e) {
       a.set(h.a);
@@ -564,9 +566,9 @@ struct Tiled {
   }
 };
 
-template <int AT, int BROWS, int GROUP, int OT, int WM, int WN, int MF, int NF, int STAGES>
+template <int AT, int BROWS, int GROUP, int OT, bool EXACT, int WM, int WN, int MF, int NF, int STAGES>
 __global__ __launch_bounds__(WM * WN * 64, 2) void product_tiled_kernel(ProductParams p) {
-  using K = Tiled<AT, BROWS, GROUP, OT, WM, WN, MF, NF, STAGES>;
+  using K = Tiled<AT, BROWS, GROUP, OT, EXACT, WM, WN, MF, NF, STAGES>;
   __shared__ typename K::S stages[STAGES];
   K::run(p, stages);
 }
@@ -587,11 +589,11 @@ hipError_t small_of(ProductParams& p, hipStream_t s) {
   return launch_units(product_small_kernel<AT, BROWS, GROUP, OT, MF, NF, W>, p, p.units, W * 64, s);
 }
 
-template <int AT, int BROWS, int GROUP, int OT, int WM, int WN, int MF, int NF, int STAGES>
+template <int AT, int BROWS, int GROUP, int OT, bool EXACT, int WM, int WN, int MF, int NF, int STAGES>
 hipError_t tiled_of(ProductParams& p, hipStream_t s) {
   count_tiles<GROUP>(p, WM * MF * 16, WN * NF * 16);
-  return launch_units(product_tiled_kernel<AT, BROWS, GROUP, OT, WM, WN, MF, NF, STAGES>, p, (p.units + 255) / 256 * 256,
-                      WM * WN * 64, s);
+  return launch_units(product_tiled_kernel<AT, BROWS, GROUP, OT, EXACT, WM, WN, MF, NF, STAGES>, p,
+                      (p.units + 255) / 256 * 256, WM * WN * 64, s);
 }
 
 // Which kernel. Up to 16 rows (a segment, on average) b's bytes are all that counts: narrow workgroups, the
@@ -602,9 +604,8 @@ hipError_t tiled_of(ProductParams& p, hipStream_t s) {
 // load (64 segments of 100 rows x 2048 x 512: 26 us by 256 x 256, 37 by 128 x 128; of 64 rows x 4096 160 and 149).
 // Where tiles share a CU (the smallest; the largest of exact sums, two of which hide each other's starts and ends: 665
 // us for a weights' gradient that 256 x 128 alone took 740 for) parts of rounds count.
-template <int AT, int BROWS, int GROUP, int OT>
+template <int AT, int BROWS, int GROUP, int OT, bool EXACT>
 hipError_t product_of(ProductParams p, hipStream_t s) {
-  constexpr bool kExact = OT == DS_FP32;
   const int64_t rows = GROUP == DS_GROUP_ROWS ? (p.m + p.groups - 1) / p.groups : p.m;
   const int64_t segments = GROUP == DS_GROUP_NONE ? 1 : p.groups;
   const auto tiles = [&](int tm, int tn) { return segments * ((rows + tm - 1) / tm) * ((p.n + tn - 1) / tn); };
@@ -617,39 +618,45 @@ hipError_t product_of(ProductParams p, hipStream_t s) {
   const double blocks = static_cast<double>(p.blocks) / (GROUP == DS_GROUP_INNER ? segments : 1);
   const double find = GROUP == DS_GROUP_ROWS ? 2 : 0;
   const auto round = [&](double ends, double block) { return find + ends + block * blocks; };
-  const double small = (kExact ? round(1.5, 0.45) : round(1, 0.3)) * shared(tiles(32, 32), 1.0);
-  const double t64 = (find + (kExact ? round(4, 1) : round(3.5, 0.5))) * rounds(64, 128);
+  const double small = (EXACT ? round(1.5, 0.45) : round(1, 0.3)) * shared(tiles(32, 32), 1.0);
+  const double t64 = (find + (EXACT ? round(4, 1) : round(3.5, 0.5))) * rounds(64, 128);
   const double t128 =
-      kExact ? round(9, 1.5) * shared(tiles(128, 128), 0.7) : round(5.6, 0.7) * rounds(128, 128);
-  const double t256 = kExact ? t128 : (rows <= 128 ? round(8, 1.3) : round(11, 1.6)) * rounds(256, 256);
+      EXACT ? round(9, 1.5) * shared(tiles(128, 128), 0.7) : round(5.6, 0.7) * rounds(128, 128);
+  const double t256 = EXACT ? t128 : (rows <= 128 ? round(8, 1.3) : round(11, 1.6)) * rounds(256, 256);
   // (a tile's rows are reached by 32-bit offsets)
   const bool near = p.a_stride < (1 << 23) && p.b_stride < (1 << 23);
   if (!near || (small <= t64 && small <= t128 && small <= t256)) return small_of<AT, BROWS, GROUP, OT, 2, 2, 8>(p, s);
-  if (t64 <= t128 && t64 <= t256) return tiled_of<AT, BROWS, GROUP, OT, 2, 4, 2, 2, 6>(p, s);
-  if constexpr (kExact) {
-    return tiled_of<AT, BROWS, GROUP, OT, 2, 2, 4, 4, 2>(p, s);
+  if (t64 <= t128 && t64 <= t256) return tiled_of<AT, BROWS, GROUP, OT, EXACT, 2, 4, 2, 2, 6>(p, s);
+  if constexpr (EXACT) {
+    return tiled_of<AT, BROWS, GROUP, OT, EXACT, 2, 2, 4, 4, 2>(p, s);
   } else {
-    if (t128 <= t256) return tiled_of<AT, BROWS, GROUP, OT, 4, 2, 2, 4, 4>(p, s);
-    return tiled_of<AT, BROWS, GROUP, OT, 2, 4, 8, 4, 2>(p, s);
+    if (t128 <= t256) return tiled_of<AT, BROWS, GROUP, OT, EXACT, 4, 2, 2, 4, 4>(p, s);
+    return tiled_of<AT, BROWS, GROUP, OT, EXACT, 2, 4, 8, 4, 2>(p, s);
   }
 }
 
-template <int AT, int OT>
+template <int AT, int OT, bool EXACT>
 hipError_t product_by_group(int b_rows, int group, const ProductParams& p, hipStream_t s) {
-  if (group == DS_GROUP_INNER) return product_of<AT, 1, DS_GROUP_INNER, OT>(p, s);
+  if (group == DS_GROUP_INNER) return product_of<AT, 1, DS_GROUP_INNER, OT, EXACT>(p, s);
   if (group == DS_GROUP_ROWS)
-    return b_rows == 1 ? product_of<AT, 1, DS_GROUP_ROWS, OT>(p, s) : product_of<AT, 128, DS_GROUP_ROWS, OT>(p, s);
-  return b_rows == 1 ? product_of<AT, 1, DS_GROUP_NONE, OT>(p, s) : product_of<AT, 128, DS_GROUP_NONE, OT>(p, s);
+    return b_rows == 1 ? product_of<AT, 1, DS_GROUP_ROWS, OT, EXACT>(p, s)
+                       : product_of<AT, 128, DS_GROUP_ROWS, OT, EXACT>(p, s);
+  return b_rows == 1 ? product_of<AT, 1, DS_GROUP_NONE, OT, EXACT>(p, s)
+                     : product_of<AT, 128, DS_GROUP_NONE, OT, EXACT>(p, s);
+}
+
+template <int AT>
+hipError_t product_by_sums(int b_rows, int group, int out_dtype, bool exact, const ProductParams& p, hipStream_t s) {
+  if (out_dtype == DS_FP32) return product_by_group<AT, DS_FP32, true>(b_rows, group, p, s);
+  return exact ? product_by_group<AT, DS_BF16, true>(b_rows, group, p, s)
+               : product_by_group<AT, DS_BF16, false>(b_rows, group, p, s);
 }
 
 }  // namespace
 
-hipError_t launch_product(int a_dtype, int b_rows, int group, int out_dtype, ProductParams p, hipStream_t s) {
-  if (a_dtype == DS_E4M3)
-    return out_dtype == DS_BF16 ? product_by_group<DS_E4M3, DS_BF16>(b_rows, group, p, s)
-                                : product_by_group<DS_E4M3, DS_FP32>(b_rows, group, p, s);
-  return out_dtype == DS_BF16 ? product_by_group<DS_E5M2, DS_BF16>(b_rows, group, p, s)
-                              : product_by_group<DS_E5M2, DS_FP32>(b_rows, group, p, s);
+hipError_t launch_product(int a_dtype, int b_rows, int group, int out_dtype, bool exact, ProductParams p, hipStream_t s) {
+  return a_dtype == DS_E4M3 ? product_by_sums<DS_E4M3>(b_rows, group, out_dtype, exact, p, s)
+                            : product_by_sums<DS_E5M2>(b_rows, group, out_dtype, exact, p, s);
 }
 
 }  // namespace ds
