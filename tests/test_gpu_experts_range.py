@@ -10,7 +10,7 @@ import torch
 import top_selection_amd as ts
 from gpu_util import say
 from oracle import experts as orc
-from test_gpu_experts import E8, KEPT, _np
+from test_gpu_experts import E8, KEPT, U, _made, _np, _operand
 
 pytestmark = pytest.mark.gpu
 
@@ -133,3 +133,81 @@ def test_exact_sums_of_a_row_do_not_depend_on_its_batch():
     all_of = ts.ds_block_product(qa, sa, qb, sb, exact=True)
     for m in (1, 16, 40, 256, 1000):
         assert torch.equal(ts.ds_block_product(qa[:m], sa[:m], qb, sb, exact=True), all_of[:m]), m
+
+
+# ------------------------------------------------------------------- every tile, with tiles of scales
+def _values(q, s, of):
+    """What 8-bit values and scales for each `of` x 128 of them stand for, in 64 bits on the device."""
+    full = s.double().repeat_interleave(of, dim=-2)[..., :q.shape[-2], :].repeat_interleave(128, dim=-1)
+    return q.double() * full[..., :q.shape[-1]]
+
+
+def _within(got, a, b, k, out, label, exact=False):
+    want, size = a @ b.t(), a.abs() @ b.abs().t()
+    eight = 0 if exact or out == torch.float32 else 2.0 ** -10
+    tol = (eight + (273 + -(-k // 128)) * U) * size + U * want.abs()
+    if out == torch.bfloat16:
+        tol += 2.0 ** -8 * want.abs() + 2.0 ** -133
+    off = ~((got.double() - want).abs() <= tol)
+    assert not off.any(), f"{label}: {int(off.sum())} of {off.numel()} off, first at {off.nonzero()[0].tolist()}"
+
+
+SEGMENTS = {"uneven": [700, 0, 130, 64, 1, 400], "even": [300] * 20, "large": [2000, 3, 0, 900],
+            "short": [100, 3, 128, 0, 77] * 13, "eight": [40, 33] * 4}
+
+
+@pytest.mark.parametrize("loads", SEGMENTS)
+@pytest.mark.parametrize("a", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("out,exact", [(torch.bfloat16, False), (torch.bfloat16, True), (torch.float32, False)])
+def test_segments_with_tiles_of_scales(loads, a, out, exact):
+    """What a training step runs: every group has scales of its own for 128 x 128, of which the last cover fewer
+    columns (2000 = 15 * 128 + 80). By size these take tiles of 64 x 128, 128 x 128 and 256 x 256."""
+    say(f"segments with tiles of scales, {loads}, {a}, {out}, {exact}")
+    n, k = 2000, 400
+    loads = SEGMENTS[loads]
+    offsets, G = np.concatenate([[0], np.cumsum(loads)]).astype(np.int32), len(loads)
+    m = int(offsets[-1]) + 3
+    qa, sa, _ = _operand(m, m, k, a)
+    parts = [_operand(50 + g, n, k, "e4m3", 128)[:2] for g in range(G)]
+    qa, sa = qa.cuda(), sa.cuda()
+    qb = torch.stack([p[0].view(torch.uint8) for p in parts]).cuda().view(torch.float8_e4m3fn)
+    sb = torch.stack([p[1] for p in parts]).cuda()
+    got = ts.ds_block_product(qa, sa, qb, sb, offsets=torch.from_numpy(offsets).cuda(), exact=exact,
+                              out=torch.full((m, n), KEPT, dtype=out, device="cuda"))
+    assert (got[m - 3:] == KEPT).all()
+    va = _values(qa, sa, 1)
+    for g in range(G):
+        lo, hi = int(offsets[g]), int(offsets[g + 1])
+        if hi > lo:
+            _within(got[lo:hi], va[lo:hi], _values(qb[g], sb[g], 128), k, out, f"segment {g}", exact)
+
+
+@pytest.mark.parametrize("m,n", [(500, 2001), (1000, 4000), (4000, 4001)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_products_of_many_blocks(m, n, out):
+    """67 blocks of the inner axis: a lane holds the tile scales of 64, which are then read anew."""
+    say(f"many blocks {m} x {n}, {out}")
+    k = 8192 + 272
+    qa, sa, _ = _operand(m, m, k, "e4m3")
+    qb, sb, _ = _operand(n + 1, n, k, "e4m3", 128)
+    qa, sa, qb, sb = qa.cuda(), sa.cuda(), qb.cuda(), sb.cuda()
+    _within(ts.ds_block_product(qa, sa, qb, sb, out_dtype=out), _values(qa, sa, 1), _values(qb, sb, 128), k, out, "product")
+
+
+@pytest.mark.parametrize("loads", ["uneven", "eight"])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_segments_of_many_blocks(loads, out):
+    say(f"segments of many blocks, {loads}, {out}")
+    n, k, loads = 2001, 8192 + 272, SEGMENTS[loads]
+    offsets, G = np.concatenate([[0], np.cumsum(loads)]).astype(np.int32), len(loads)
+    qa, sa, _ = _operand(1, int(offsets[-1]), k, "e5m2")
+    parts = [_operand(70 + g, n, k, "e4m3", 128)[:2] for g in range(G)]
+    qa, sa = qa.cuda(), sa.cuda()
+    qb = torch.stack([p[0].view(torch.uint8) for p in parts]).cuda().view(torch.float8_e4m3fn)
+    sb = torch.stack([p[1] for p in parts]).cuda()
+    got = ts.ds_block_product(qa, sa, qb, sb, offsets=torch.from_numpy(offsets).cuda(), out_dtype=out)
+    va = _values(qa, sa, 1)
+    for g in range(G):
+        lo, hi = int(offsets[g]), int(offsets[g + 1])
+        if hi > lo:
+            _within(got[lo:hi], va[lo:hi], _values(qb[g], sb[g], 128), k, out, f"segment {g}")
