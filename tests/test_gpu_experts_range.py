@@ -211,3 +211,30 @@ def test_segments_of_many_blocks(loads, out):
         lo, hi = int(offsets[g]), int(offsets[g + 1])
         if hi > lo:
             _within(got[lo:hi], va[lo:hi], _values(qb[g], sb[g], 128), k, out, f"segment {g}")
+
+
+@pytest.mark.parametrize("m,n,k", [(8, 2048, 2048), (100, 333, 2048), (512, 2048, 768), (1000, 4000, 2048),
+                                   (4096, 4096, 2048), (512, 2048, 8192)])
+@pytest.mark.parametrize("of_b", [1, 128])
+@pytest.mark.parametrize("exact", [False, True])
+def test_mean_error_of_bf16_products(m, n, k, of_b, exact):
+    """The mean error of normal data, a bound about twenty times tighter than that of single elements. It is at most
+      * the mean rounding to bf16: half of half a step, 2^-9 of the value;
+      * the fp32 sums' (273 + blocks) u of the products' magnitudes;
+      * and where the 8-bit unit adds: it cuts seven of eight products towards zero by less than 2^-13 of the largest, so by
+        errors with the products' signs, which are even and independent for such data: the mean of their sum's magnitude is
+        at most the root of their squares' sum, over a block 112 (2^-13 of its largest |a| times its largest |b|)^2."""
+    say(f"mean error {m} x {n} x {k}, {of_b}, {exact}")
+    g = torch.Generator(device="cuda").manual_seed(m + n + k)
+    a, sa = ts.ds_block_quantize(torch.randn(m, k, generator=g, device="cuda"))
+    b, sb = ts.ds_block_quantize(torch.randn(n, k, generator=g, device="cuda"), ts.BLOCK_TILE if of_b == 128 else ts.BLOCK_ROW)
+    va, vb = _values(a, sa, 1), _values(b, sb, of_b)
+    want, size = va @ vb.t(), va.abs() @ vb.abs().t()
+    bound = 2.0 ** -9 * want.abs() + (273 + k // 128) * U * size
+    if not exact:
+        top = lambda v: v.abs().view(v.shape[0], -1, 128).amax(dim=2) ** 2  # noqa: E731
+        bound += 2.0 ** -13 * (112 * (top(va) @ top(vb).t())).sqrt()
+    got = ts.ds_block_product(a, sa, b, sb, exact=exact).double()
+    assert (got - want).abs().mean() <= bound.mean()
+    # neither above nor below: the mean of n m such errors of either sign
+    assert (got - want).mean().abs() <= 8 * bound.mean() / (m * n) ** 0.5 + 2.0 ** -13 * bound.mean()
