@@ -238,3 +238,122 @@ def test_mean_error_of_bf16_products(m, n, k, of_b, exact):
     assert (got - want).abs().mean() <= bound.mean()
     # neither above nor below: the mean of n m such errors of either sign
     assert (got - want).mean().abs() <= 8 * bound.mean() / (m * n) ** 0.5 + 2.0 ** -13 * bound.mean()
+
+
+# ---------------------------------------------------------------------- broken plans, guarded outputs
+class _Guarded:
+    """A device matrix in the middle of a larger one, all KEPT (8-bit: 2), and a check of what lies around it."""
+
+    def __init__(self, rows, n, dtype, groups=1):
+        self.fill = KEPT if dtype.itemsize > 1 else 2.0
+        self.base = torch.full((groups * rows + 64, n + 32), self.fill, device="cuda").to(dtype)
+        self.rows, self.n = groups * rows, n
+        self.view = self.base[32:32 + groups * rows, 16:16 + n]
+        if groups > 1:
+            self.view = self.base[32:32 + groups * rows].view(groups, rows, n + 32)[:, :, 16:16 + n]
+
+    def check(self):
+        around = self.base.float().clone()
+        around[32:32 + self.rows, 16:16 + self.n] = self.fill
+        assert (around == self.fill).all()
+
+
+def _broken(rows, k, experts, align, seed=1):
+    """A plan with positions, slots and offsets out of range; the positions that still hold a slot both ways, and that
+    slot's row."""
+    plan, place, order, _ = _made(seed, rows, k, experts, align, dropped=0)
+    bad = ts.ExpertPlan(plan.place.clone(), plan.order.clone(), plan.offsets.clone(), align)
+    bad.place[::2] = 2 ** 31 - 1
+    bad.place[1::4] = -5
+    bad.order[::3] = 2 ** 31 - 1
+    bad.order[1::7] = -9
+    bad.offsets[-1] = 2 ** 31 - 1
+    bad.offsets[0] = -7
+    flat, order = _np(bad.place).reshape(-1), _np(bad.order)
+    at = [p for p in range(order.size) if 0 <= order[p] < rows * k and flat[order[p]] == p]
+    assert len(at) >= 4
+    return bad, np.array(at), order[at] // k
+
+
+@pytest.mark.parametrize("n", [70, 257])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_of_broken_plans(n, dtype):
+    say(f"rows of broken plans, n {n}, {dtype}")
+    rows, k = 40, 3
+    plan, at, row = _broken(rows, k, 5, 16)
+    cap = plan.order.numel()
+    x, y = torch.randn(rows, n, device="cuda").to(dtype), torch.randn(cap, n, device="cuda").to(dtype)
+    w = torch.rand(rows, k, device="cuda")
+    out = _Guarded(cap, n, dtype)
+    ts.ds_expert_gather(x, plan, out=out.view)
+    out.check()
+    assert torch.equal(out.view[at], x[row])
+    # combining skips slots out of range, and its gradient gives them 0
+    place = _np(plan.place)
+    has = (place >= 0) & (place < cap)
+    back = _Guarded(rows, n, dtype)
+    ts.ds_expert_combine(y, plan, w, out=back.view)
+    back.check()
+    want, size = orc.combine(_np(y), np.where(has, place, -1), _np(w))
+    half = 2.0 ** -8 if dtype == torch.bfloat16 else 0
+    assert (np.abs(_np(back.view) - want) <= k * U * size + half * np.abs(want)).all()
+    grad = _Guarded(cap, n, dtype)
+    _, gw = ts.ds_expert_combine_grad(x, y, plan, w, out_y=grad.view)
+    grad.check()
+    _, want_w, size = orc.combine_grad(_np(x), _np(y), np.where(has, place, -1), _np(w), np.array([0]), np.zeros((cap, n)))
+    assert (np.abs(_np(gw) - want_w) <= (n / 64 + 24) * U * size).all() and (_np(gw)[~has] == 0).all()
+    slot = _np(plan.order)[at]
+    want = _np(x)[row] * _np(w).reshape(-1)[slot][:, None]
+    assert (np.abs(_np(grad.view)[at] - want) <= (U + half) * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("n", [70, 257])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_blocks_of_broken_plans(n, dtype):
+    say(f"blocks of broken plans, n {n}, {dtype}")
+    rows, k = 40, 3
+    x = torch.randn(rows, n, device="cuda").to(dtype)
+    plan, at, row = _broken(rows, k, 5, 16)
+    cap, wide = plan.order.numel(), -(-n // 16) * 16
+    q, s = _Guarded(cap, wide, E8["e4m3"]), torch.full((cap + 64, -(-n // 128)), KEPT, device="cuda")
+    ts.ds_block_quantize(x, plan=plan, out=q.view, out_scales=s[32:32 + cap])
+    q.check()
+    assert (s[:32] == KEPT).all() and (s[32 + cap:] == KEPT).all()
+    want, want_s = ts.ds_block_quantize(x)
+    assert torch.equal(q.view[at].view(torch.uint8), want[row].view(torch.uint8)) and torch.equal(s[32:][at], want_s[row])
+    # columns go by the order alone: what it has out of range is padding, up to the end, here the capacity
+    plan, _, _ = _broken(rows, k, 5, 128)
+    order, cap = _np(plan.order), plan.order.numel()
+    q, s = _Guarded(n, cap, E8["e5m2"]), torch.full((n + 64, cap // 128), KEPT, device="cuda")
+    ts.ds_block_quantize(x, ts.BLOCK_COLUMN, dtype=E8["e5m2"], plan=plan, out=q.view, out_scales=s[32:32 + n])
+    q.check()
+    assert (s[:32] == KEPT).all() and (s[32 + n:] == KEPT).all()
+    held = (order >= 0) & (order < rows * k)
+    v = np.where(held[:, None], _np(x)[np.where(held, order, 0) // k], 0).astype(np.float32)
+    want, want_s = orc.quantize(np.ascontiguousarray(v.T), 1, "e5m2")
+    assert np.array_equal(_np(q.view.float()), want) and np.array_equal(_np(s[32:32 + n]), want_s)
+
+
+@pytest.mark.parametrize("m,n,split", [(72, 20, 20), (1000, 2000, 200)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_products_of_broken_offsets(m, n, split, out):
+    """Offsets that fall, and lie below 0 and past the end: clamped, and segments that end before they start are empty.
+    By rows the first segment has the first `split` rows to itself."""
+    say(f"products of broken offsets {m} x {n}, {out}")
+    k = 384
+    far = torch.tensor([-4, m - 10, split, 2 ** 31 - 1, 7, -3], dtype=torch.int32, device="cuda")
+    qa, sa, _ = _operand(1, m, k, "e4m3")
+    qb, sb, _ = _operand(2, 5 * n, k, "e4m3")
+    qa, sa, qb, sb = qa.cuda(), sa.cuda(), qb.cuda(), sb.cuda()
+    o = _Guarded(m, n, out)
+    ts.ds_block_product(qa, sa, qb.view(5, n, k), sb.view(5, n, -1), offsets=far, out=o.view)
+    o.check()
+    _within(o.view[:split], _values(qa, sa, 1)[:split], _values(qb[:n], sb[:n], 1), k, out, "rows")
+    far = torch.tensor([-4, 90, 20, 2 ** 31 - 1, 7], dtype=torch.int32, device="cuda")
+    o = _Guarded(m, n, out, groups=4)
+    qb, sb = qb[:n], sb[:n]
+    ts.ds_block_product(qa, sa, qb, sb, offsets=far, inner=True, out=o.view)
+    o.check()
+    va, vb = _values(qa, sa, 1), _values(qb, sb, 1)
+    for g, (lo, hi) in enumerate([(0, 128), (128, 128), (128, k), (k, k)]):
+        _within(o.view[g], va[:, lo:hi], vb[:, lo:hi], k, out, f"segment {g}")
