@@ -2,6 +2,7 @@
 the choice of sums, and sizes at which each tile of ds_block_product is chosen. Tolerances as in
 test_gpu_experts.py, where the definitions' helpers are from."""
 import ctypes
+import threading
 
 import numpy as np
 import pytest
@@ -10,7 +11,7 @@ import torch
 import top_selection_amd as ts
 from gpu_util import say
 from oracle import experts as orc
-from test_gpu_experts import E8, KEPT, U, _made, _np, _operand
+from test_gpu_experts import E8, KEPT, U, _layer, _layer_input, _made, _np, _operand
 
 pytestmark = pytest.mark.gpu
 
@@ -357,3 +358,113 @@ def test_products_of_broken_offsets(m, n, split, out):
     va, vb = _values(qa, sa, 1), _values(qb, sb, 1)
     for g, (lo, hi) in enumerate([(0, 128), (128, 128), (128, k), (k, k)]):
         _within(o.view[g], va[:, lo:hi], vb[:, lo:hi], k, out, f"segment {g}")
+
+
+# ------------------------------------------------------------------------- launches, graphs, threads
+def _identity(rows):
+    """A plan of one expert and one slot a row: positions are rows."""
+    return ts.ds_expert_sort(torch.zeros(rows, 1, dtype=torch.int32, device="cuda"), 1)
+
+
+def test_rows_of_more_than_one_launch():
+    """A launch is at most 2^21 workgroups, of sixteen short rows (the gradient: four)."""
+    say("rows past a launch")
+    n = 8
+    rows = 16 * 2 ** 21 + 5
+    plan = _identity(rows)
+    x = torch.randint(-1000, 1000, (rows, n), dtype=torch.int16, device="cuda").bfloat16()
+    out = ts.ds_expert_gather(x, plan)
+    assert torch.equal(out, x)
+    assert torch.equal(ts.ds_expert_combine(out, plan, torch.full((rows, 1), 0.5, device="cuda")), x * 0.5)
+    rows = 4 * 2 ** 21 + 5
+    plan, x = _identity(rows), x[:rows]
+    w = torch.randint(1, 4, (rows, 1), device="cuda").float()
+    gy, gw = ts.ds_expert_combine_grad(x, x, plan, w)
+    assert torch.equal(gy, (w * x.float()).bfloat16()) and torch.equal(gw[:, 0], (x.float() ** 2).sum(dim=1))
+
+
+@pytest.mark.parametrize("layout,rows,n", [(0, 32 * 2 ** 21 + 40, 3), (1, 3, 64 * 2 ** 21 + 100), (2, 128 * 2 ** 21 + 130, 3)])
+def test_blocks_of_more_than_one_launch(layout, rows, n):
+    """As 2^21 workgroups take 32 blocks of a row, 64 columns, or a tile each: the same as in two calls."""
+    say(f"blocks past a launch, layout {layout}")
+    x = torch.randn(rows, n, device="cuda", dtype=torch.bfloat16)
+    q, s = ts.ds_block_quantize(x, layout)
+    half = 2 ** 26  # rows of q
+    for part in (slice(0, half), slice(half, None)):
+        want, want_s = ts.ds_block_quantize(x[:, part].contiguous() if layout == 1 else x[part], layout)
+        assert torch.equal(q[part].view(torch.uint8), want.view(torch.uint8))
+        assert torch.equal(s[slice(part.start // 128, part.stop and part.stop // 128) if layout == 2 else part], want_s)
+
+
+def test_a_product_of_more_than_one_launch():
+    say("product past a launch")
+    m, n, k = 2, 32 * 2 ** 21 + 70, 16
+    qb = torch.randint(0, 0x70, (n, k), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    sb = torch.rand(n, 1, device="cuda")
+    qa, sa = torch.randn(m, k, device="cuda").to(torch.float8_e4m3fn), torch.rand(m, 1, device="cuda")
+    got = ts.ds_block_product(qa, sa, qb, sb)
+    for part in (slice(0, 1000), slice(n - 1000, n)):
+        assert torch.equal(got[:, part], ts.ds_block_product(qa, sa, qb[part], sb[part]))
+    assert got.isfinite().all()
+
+
+def test_training_steps_replayed_from_graphs():
+    """Two captured layers of experts with all gradients, one of them with a sort in two launches, replayed in turn with
+    eager work and synchronisation between: every replay gives what eager work gives."""
+    say("training steps from graphs")
+    steps = []
+    for seed, rows, k in ((1, 150, 2), (2, 2100, 4)):
+        x, logits, w1, w2, g = _layer_input(seed, rows, 6, 128, 256)
+        run = lambda a=(x, logits, w1, w2, k, 128, g): _layer(*a)  # noqa: E731
+        want = [t.clone() for t in run()]
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            run()
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = run()
+        steps.append((graph, out, want, run))
+    for turn in range(4):
+        for graph, out, want, run in steps:
+            for t in out:
+                t.zero_()
+            graph.replay()
+            again = run()
+            torch.cuda.synchronize()
+            for got in (out, again):
+                assert all(torch.equal(a, b) for a, b in zip(got, want)), turn
+
+
+def test_calls_from_several_threads():
+    """Threads with streams of their own: plans, workspaces and outputs are each call's."""
+    say("threads")
+    jobs = []
+    for i in range(6):
+        idx = torch.randint(-1, 40, (3000 + 11 * i, 4), dtype=torch.int32, device="cuda")
+        x = torch.randn(idx.shape[0], 96 + i, device="cuda")
+        plan = ts.ds_expert_sort(idx, 40, 16)
+        end = int(plan.offsets[-1])
+        jobs.append((idx, x, end, [t.clone() for t in plan[:3]], ts.ds_expert_gather(x, plan)[:end].clone(),
+                     ts.ds_expert_combine(ts.ds_expert_gather(x, plan), plan).clone()))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(idx, x, end, arrays, rows, back):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                plan = ts.ds_expert_sort(idx, 40, 16)
+                got = ts.ds_expert_gather(x, plan)
+                out = ts.ds_expert_combine(got, plan)
+                if not (all(torch.equal(a, b) for a, b in zip(plan[:3], arrays)) and torch.equal(got[:end], rows)
+                        and torch.equal(out, back)):
+                    wrong.append(idx.shape)
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
