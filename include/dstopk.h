@@ -560,6 +560,9 @@ int ds_expert_combine_grad(const void* g, int64_t g_stride, const void* y, int64
  *   DS_BLOCK_TILE    q [rows, ceil16(n)], scales [ceil(rows / 128), ceil(n / 128)], without a plan.
  * What a plan's end leaves over (whole rows of q and scales, or columns) is left as it was; elements of q
  * from n (P) to its ceil16 are written as 0.
+ * Rows that lie at a plan's positions already (a second layer's) are quantised without a plan, all of them: what is
+ * behind the plan's end is read and written too, whatever it holds, and stays there (in columns if the plan's
+ * align is a multiple of 128), since a block meets one row or one expert's positions.
  *   x         [rows, n] of dtype (DS_BF16 or DS_FP32), rows row_stride elements apart.
  *   q         rows q_stride bytes apart; q and q_stride are multiples of 16 (DS_ERR_ALIGNMENT).
  *   q_dtype   DS_E4M3 or DS_E5M2.
@@ -595,14 +598,15 @@ typedef struct ds_block_operand {
 /*
  * ds_block_product -- out = a b^T of operands in blocks of 128 along the inner axis:
  *   out[i, j] = sum over blocks t of a.scale[i, t] * b.scale[j, t] * (sum over the block of a.q[i, .] * b.q[j, .])
- * With out_dtype DS_FP32, or DS_BF16 | DS_EXACT_SUMS, products are exact and all sums fp32 (and rounded once to bf16).
- * With DS_BF16 alone the sizes (m, n, k, groups) decide how a block's sum is made, so that the bits of a row's
- * result may depend on how many rows the call has. Calls of few rows (up to 16 a group, on average, and where small tiles
- * are chosen above) sum as with DS_EXACT_SUMS. The others leave a block's sum to the 8-bit matrix unit, at up to
- * twice the rate: eight products at a time, of which it cuts what lies below 2^-13 of the largest (together less than 2^-10 of the
- * products' magnitudes). Measured against 64 bits, the root mean square of that error over the results' is 1.4e-5 for
- * normal data at any k (3.0e-5, 5.3e-5 where magnitudes spread over 2^3, 2^6; rounding to bf16 is 1.7e-3). The blocks' sums
- * are scaled and added in fp32.
+ * With out_dtype DS_FP32, or DS_BF16 | DS_EXACT_SUMS, products are exact and all sums fp32 (and rounded once to
+ * bf16). With DS_BF16 alone the sizes (m, n, k, groups) decide how a block's sum is made, so that the bits of a row's
+ * result may depend on how many rows the call has. Calls of few rows (up to 16 a group, on average, and where small
+ * tiles are chosen above) sum as with DS_EXACT_SUMS. The others leave a block's sum to the 8-bit matrix unit, at up
+ * to twice the rate: eight products at a time, of which it cuts what lies below 2^-13 of the largest (together less
+ * than 2^-10 of the products' magnitudes). Measured against 64 bits, the root mean square of that error over the
+ * results' is 1.4e-5 for normal data at any k (3.0e-5, 5.3e-5 where magnitudes spread over 2^3, 2^6; rounding to bf16
+ * is 1.7e-3). The blocks' sums are scaled and added in fp32. The two scales are multiplied first: a term whose
+ * scales' product leaves fp32 is infinite or NaN, and one whose product is below 2^-126 loses bits.
  *   DS_GROUP_NONE   a [m, k], b [n, k], out [m, n]; groups is 1 and offsets NULL.
  *   DS_GROUP_ROWS   the rows of a and out are in `groups` segments, row i in [offsets[g], offsets[g + 1])
  *                   with b's group g: b [groups, n, k] (n rows `stride` bytes apart after another). Rows
@@ -611,7 +615,8 @@ typedef struct ds_block_operand {
  *                   [offsets[g], offsets[g + 1]) only, 0 where that is empty. Segments start and end at
  *                   multiples of 128 (others count as the next multiple); a.scale_rows and b.scale_rows are 1.
  * Offsets (device, [groups + 1]) rise from [0]; they are clamped to [0, m] ([0, k]), and a segment that
- * ends before it starts is empty. Segments that overlap leave the shared rows unspecified.
+ * ends before it starts is empty. Segments that overlap leave the shared rows unspecified, and where offsets
+ * fall the rows from the lower one on are. Nothing is written outside of out.
  *   m, n        1 <= n < 2^31, 0 <= m < 2^31; 1 <= groups <= DS_MAX_EXPERTS.
  *   k           a multiple of 16 (DS_ERR_ALIGNMENT otherwise) below 2^31; with 0 the operands are not looked
  *               at and the sums are 0.

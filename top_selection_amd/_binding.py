@@ -787,7 +787,9 @@ def ds_block_quantize(x, layout: int = BLOCK_ROW, dtype=None, plan: Optional[Exp
     scales): BLOCK_ROW q [P, n up to 16s], scales [P, ceil(n / 128)]; BLOCK_COLUMN (transposed)
     q [n, P up to 16s], scales [n, ceil(P / 128)]; BLOCK_TILE q [rows, n up to 16s], scales
     [ceil(rows / 128), ceil(n / 128)], P the plan's capacity or the rows. What lies behind the plan's
-    end is what the outputs held. BLOCK_TILE takes a stack x [groups, rows, n] too (experts' weights)."""
+    end is what the outputs held. Rows already at a plan's positions are quantised without a plan, whole.
+    BLOCK_TILE takes a stack x [groups, rows, n] too (experts' weights): one launch if rows is a multiple of
+    128, else one for each matrix."""
     torch = _torch()
     dtype = dtype or torch.float8_e4m3fn
     if x.dim() == 3:
@@ -813,7 +815,8 @@ def ds_block_quantize(x, layout: int = BLOCK_ROW, dtype=None, plan: Optional[Exp
 
 
 def _quantize_stack(x, layout, dtype, plan, out, out_scales, stream):
-    """ds_block_quantize of each matrix of a contiguous stack (one call where tiles do not cross them)."""
+    """ds_block_quantize of each matrix of a contiguous stack (one call where tiles do not cross them: 64 of 4096 x
+    4096 bf16 570 us; else one for each: 64 of 1000 x 1024 339 us, five a matrix, where the bytes take 39)."""
     torch = _torch()
     if layout != BLOCK_TILE or plan is not None:
         raise ValueError("a stack of matrices is quantised in tiles, without a plan")

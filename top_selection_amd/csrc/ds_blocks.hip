@@ -166,9 +166,10 @@ __global__ __launch_bounds__(256) void quantize_row_kernel(QuantizeParams p) {
 // A workgroup takes 128 positions of 64 columns through LDS: rows are read in vectors (all of a thread's at
 // once: first the rows' numbers, then the rows), and a thread takes 32 elements of one (fp32) or two (bf16)
 // columns, four or eight lanes a column, whose 16-byte stores make whole lines. The rows' distance in LDS makes the
-// reads down the columns meet every bank once. A position's row is quantised anew for every expert, since the
-// blocks run over positions: 28000 positions of 2001 fp32 columns 38.5 us, bound by vector instructions (about ten
-// an element), memory would take 20.
+// reads down the columns meet every bank once. A position's row is quantised anew for every expert, since the blocks
+// run over positions: 28000 positions of 2001 fp32 columns 38.8 us, bound by vector instructions (by the counters 17
+// an element: nine make the quotient and its rounding, the rest are magnitudes, padding, addresses and the way
+// through LDS), memory would take 20.
 template <int DT, int QT>
 __global__ __launch_bounds__(256, 4) void quantize_column_kernel(QuantizeParams p) {
   using T = typename Elem<DT>::T;
